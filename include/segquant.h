@@ -32,7 +32,8 @@
  *     never allocates or frees device memory and keeps no pointer after the
  *     call returns.  The only scratch memory is the optional, caller-owned
  *     workspace of segquant_gemm_w8a8_seg (its size from
- *     segquant_gemm_workspace_bytes).
+ *     segquant_gemm_workspace_bytes) and the caller-owned workspaces of
+ *     segquant_groupnorm_quantize and segquant_adapter_add.
  *   - Segment lists are HOST arrays (offset[n], width[n]), read only during
  *     the call: offsets start at 0, are contiguous, widths are positive and
  *     sum to the segmented dimension.  Every K-segment boundary except the
@@ -146,7 +147,9 @@ int segquant_quantize_dualscale(const uint16_t *x_bf16, int64_t M, int64_t K, in
                                 const int32_t *kseg_width, const float *act_scales,
                                 int8_t *q_out, int64_t ld_q, int32_t q_layout, void *stream);
 
-/* Activations for segquant_activate_quantize. */
+/* Activations for segquant_activate_quantize and (with SEGQ_ACT_NONE)
+ * segquant_groupnorm_quantize. */
+#define SEGQ_ACT_NONE 0 /* z itself (group norm only) */
 #define SEGQ_ACT_SILU 1 /* z / (1 + exp(-z)) */
 #define SEGQ_ACT_GELU 2 /* z/2 * (1 + erf(z / sqrt(2))), the exact form */
 
@@ -175,6 +178,148 @@ int segquant_activate_quantize(const uint16_t *z_bf16, int64_t M, int64_t K, int
                                const int32_t *kseg_width, const float *act_scales,
                                int8_t *q_out, int64_t ld_q, int32_t q_layout, uint16_t *x_out,
                                int64_t ld_xo, void *stream);
+
+/*
+ * segquant_groupnorm_quantize -- group norm of a channels-last image fused
+ * with the modulation, the activation and the quantisation: what an image
+ * UNet's layers read.  B samples of P pixels (rows) of C channels, row
+ * b * P + p; group g holds the D = C / groups neighbouring channels
+ * g*D .. g*D + D-1 of every row.  Per sample and group, over its P * D values:
+ *   mu = mean z, v = mean (z - mu)^2                                  (fp32)
+ *   t  = (z - mu) / sqrt(v + eps) * gamma[c] + beta[c]
+ *   t  = t * (1 + scale[b][c]) + shift[b][c]
+ *   x  = bf16_rne(act(t)); codes of x exactly as segquant_quantize_dualscale
+ *   z_bf16      device bf16 [B * P][ld_z]
+ *   groups      1 .. C, a divisor of C (groups = C: instance norm)
+ *   eps         > 0
+ *   gamma, beta device fp32 [C], each optional (NULL: 1 and 0)
+ *   scale, shift  device bf16 [B][ld_mod], each optional (NULL: 0): two chunks
+ *               of a conditioning layer's output as they are, ld_mod its
+ *               leading dimension (ignored when both are NULL)
+ *   act_kind    SEGQ_ACT_NONE, SEGQ_ACT_SILU or SEGQ_ACT_GELU
+ *   act_scales, q_out, ld_q, q_layout, x_out, ld_xo
+ *               the outputs of segquant_activate_quantize, K-segments over
+ *               the C channels.  x_out may be z_bf16 when ld_xo = ld_z.
+ *   workspace   device scratch, 16-byte aligned, of at least
+ *               segquant_groupnorm_workspace_bytes() bytes (SEGQ_ERR_UNSUPPORTED
+ *               with fewer), contents undefined afterwards; calls that share
+ *               one must be ordered.  NULL where that size is 0.
+ * One launch where a group of a sample fits a workgroup's registers, else
+ * two.  The order of every sum is fixed: the same call gives the same bits.
+ * Tensor pointers 16-byte aligned, ld_z, ld_xo and ld_mod multiples of 8,
+ * ld_q of 16; C needs no alignment.  C <= 2^20, B <= 65535.  B or P may be 0.
+ * Values above about 2^60 in magnitude overflow the fp32 squares.
+ */
+int segquant_groupnorm_quantize(const uint16_t *z_bf16, int64_t B, int64_t P, int64_t C,
+                                int64_t ld_z, int32_t groups, float eps, const float *gamma,
+                                const float *beta, const uint16_t *scale, const uint16_t *shift,
+                                int64_t ld_mod, int32_t act_kind, int32_t n_kseg,
+                                const int32_t *kseg_offset, const int32_t *kseg_width,
+                                const float *act_scales, int8_t *q_out, int64_t ld_q,
+                                int32_t q_layout, uint16_t *x_out, int64_t ld_xo, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* Workspace of segquant_groupnorm_quantize for these sizes (0: none).  On
+ * invalid sizes returns 0 and sets segquant_last_error(). */
+size_t segquant_groupnorm_workspace_bytes(int64_t B, int64_t P, int64_t C, int32_t groups);
+
+/*
+ * segquant_adanorm_quantize -- the AdaNorm block in front of a quantised
+ * layer: the gated residual update, layer norm, and the modulation by the
+ * shift and scale that the request's conditioning layer emits [P2 section 1;
+ * P1 SegLinear, the AdaNorm chunking], fused with the quantisation.  For row m
+ * of request r, over its K values:
+ *   h' = bf16_rne(h + gate[r] * branch)           (where branch is given)
+ *   mu = mean h', v = mean (h' - mu)^2                                (fp32)
+ *   t  = (h' - mu) / sqrt(v + eps) * gamma[k] + beta[k]
+ *   x  = bf16_rne(t * (1 + scale[r][k]) + shift[r][k])
+ *   codes of x exactly as segquant_quantize_dualscale
+ *   h_bf16      device bf16 [M][ld_h], the residual stream
+ *   branch      optional device bf16 [M][ld_b]: the last block's output
+ *   gate        optional, only with branch: device bf16 [n_req][ld_mod]
+ *               (NULL: 1)
+ *   h_out       optional, only with branch: device bf16 [M][ld_ho], h';
+ *               may be h_bf16 when ld_ho = ld_h
+ *   gamma, beta device fp32 [K], each optional (NULL: 1 and 0)
+ *   scale, shift  device bf16 [n_req][ld_mod], each optional (NULL: 0); scale,
+ *               shift and gate share ld_mod: chunks of one layer's output
+ *   n_req       >= 1
+ *   row_offset  device int32 [n_req + 1]: request r holds rows row_offset[r]
+ *               .. row_offset[r+1] - 1 (none where they are equal).  Rows
+ *               before the first or behind the last request are left as they
+ *               are in every output.  The offsets must not decrease; if they
+ *               do, which request's parameters a row gets is unspecified (no
+ *               access leaves the arrays).  NULL: n_req requests of M / n_req
+ *               rows each, n_req a divisor of M.
+ *   act_scales, q_out, ld_q, q_layout, x_out, ld_xo
+ *               the outputs of segquant_activate_quantize; here neither need
+ *               be given if h_out is
+ * One launch, no workspace.  Tensor pointers 16-byte aligned (row_offset 4),
+ * ld_h, ld_b, ld_ho, ld_xo and ld_mod multiples of 8, ld_q of 16; K needs no
+ * alignment.  M may be 0.  Outputs other than h_out must not overlap inputs.
+ */
+int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int64_t ld_h,
+                              const uint16_t *branch, int64_t ld_b, const uint16_t *gate,
+                              uint16_t *h_out, int64_t ld_ho, float eps, const float *gamma,
+                              const float *beta, const uint16_t *scale, const uint16_t *shift,
+                              int64_t ld_mod, int32_t n_req, const int32_t *row_offset,
+                              int32_t n_kseg, const int32_t *kseg_offset,
+                              const int32_t *kseg_width, const float *act_scales, int8_t *q_out,
+                              int64_t ld_q, int32_t q_layout, uint16_t *x_out, int64_t ld_xo,
+                              void *stream);
+
+/* Storage granularity and limit of adapter ranks. */
+#define SEGQ_ADAPTER_RANK_STEP 16
+#define SEGQ_ADAPTER_RANK_MAX 256
+
+/*
+ * segquant_adapter_add -- low-rank adapters of many requests beside a shared
+ * layer.  For row m of request r with adapter i = adapter[r], and column n in
+ * N-segment j:
+ *   t[q]    = alpha[i] * sum_k x[m][k] * a[i][j * rank + q][k]
+ *   y[m][n] = bf16_rne( base[m][n] + sum_{q < rank_of[i]} t[q] * b[i][n][q] )
+ * The products of bf16 values are summed in fp32; t is held to 16 bits or
+ * more of mantissa.  An output-segmented layer [P1 SegLinear, pattern one]
+ * has one pair of factors per N-segment; a single segment is the usual
+ * low-rank adapter.
+ *   x_bf16      device bf16 [M][ld_x]: the layer's input before quantisation
+ *   n_req, row_offset  as segquant_adanorm_quantize, row_offset required; rows
+ *               of no request are left as they are in y
+ *   adapter     device int32 [n_req]; an index outside [0, n_adapters) (-1,
+ *               say) means no adapter: y = base for that request's rows
+ *   rank        stored rank, a multiple of SEGQ_ADAPTER_RANK_STEP up to
+ *               SEGQ_ADAPTER_RANK_MAX
+ *   rank_of     optional device int32 [n_adapters]: true ranks, clamped to
+ *               [0, rank]; what a and b hold past them is never used (NULL:
+ *               every adapter has the stored rank)
+ *   a           device bf16 [n_adapters][n_nseg * rank][K]
+ *   b           device bf16 [n_adapters][N][rank]
+ *   alpha       optional device fp32 [n_adapters] (NULL: 1)
+ *   n_nseg, nseg_offset, nseg_width
+ *               N-segments (host), boundaries multiples of 16
+ *   base_bf16   optional device bf16 [M][ld_base]: the layer's output (NULL:
+ *               0); may be y_bf16 when ld_base = ld_y
+ *   y_bf16      device bf16 [M][ld_y]; must not overlap x, a or b
+ *   workspace   device scratch, 16-byte aligned, of at least
+ *               segquant_adapter_workspace_bytes() bytes (SEGQ_ERR_UNSUPPORTED
+ *               with fewer), contents undefined afterwards; calls that share
+ *               one must be ordered
+ * Two launches.  The order of every sum is fixed.  Requires K % 64 == 0,
+ * N % 16 == 0, 16-byte aligned tensor pointers (int32 arrays and alpha 4),
+ * ld_x, ld_base and ld_y multiples of 8, M <= 2^27.  M may be 0.
+ */
+int segquant_adapter_add(int64_t M, int64_t N, int64_t K, const uint16_t *x_bf16, int64_t ld_x,
+                         int32_t n_req, const int32_t *row_offset, const int32_t *adapter,
+                         int32_t n_adapters, int32_t rank, const int32_t *rank_of,
+                         const uint16_t *a, const uint16_t *b, const float *alpha, int32_t n_nseg,
+                         const int32_t *nseg_offset, const int32_t *nseg_width,
+                         const uint16_t *base_bf16, int64_t ld_base, uint16_t *y_bf16,
+                         int64_t ld_y, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace of segquant_adapter_add for these sizes.  On invalid sizes
+ * returns 0 and sets segquant_last_error(). */
+size_t segquant_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t n_req,
+                                        int32_t rank, int32_t n_nseg);
 
 /*
  * segquant_weight_packed_bytes -- size of the packed int8 weight for a

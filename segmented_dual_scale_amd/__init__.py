@@ -20,6 +20,7 @@ sections) and "SegQuant" (hliangzhao.me, sections 2 and 3).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence, Tuple
 
@@ -33,6 +34,9 @@ __all__ = [
     "SEGQ_GEMM_SINGLE_SCALE", "segquant_calibrate_amax_single",
     "SEGQ_ACT_SILU", "SEGQ_ACT_GELU", "segquant_activate_quantize", "SEGQ_GEMM_W4", "SEGQ_KERNEL_TILE", "SEGQ_KERNEL_SMALLM",
     "segquant_gemm_halves", "segquant_gemm_w8a8_seg_noalloc", "SEGQ_NOALLOC_SCRATCH_BYTES",
+    "SEGQ_ACT_NONE", "segquant_groupnorm_workspace_bytes", "segquant_groupnorm_quantize",
+    "segquant_adanorm_quantize", "segquant_adapter_workspace_bytes", "segquant_adapter_add",
+    "SEGQ_ADAPTER_RANK_STEP", "SEGQ_ADAPTER_RANK_MAX",
 ]
 
 SEGQ_OK = 0
@@ -52,11 +56,14 @@ SEGQ_GEMM_FORCE_SMALLM = 2
 SEGQ_GEMM_FUSED_QUANT = 4
 SEGQ_GEMM_SINGLE_SCALE = 8
 SEGQ_GEMM_W4 = 16
+SEGQ_ACT_NONE = 0
 SEGQ_ACT_SILU = 1
 SEGQ_ACT_GELU = 2
 SEGQ_KERNEL_TILE = 1
 SEGQ_KERNEL_SMALLM = 2
 SEGQ_NOALLOC_SCRATCH_BYTES = 64 << 20
+SEGQ_ADAPTER_RANK_STEP = 16
+SEGQ_ADAPTER_RANK_MAX = 256
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # SEGQUANT_LIBRARY names another build of the same library (the tests use it
@@ -86,6 +93,7 @@ def load_library():
                            "(the layer has no other implementation)")
     lib = ctypes.CDLL(_LIB_PATH)
     P, I64, I32, U32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32
+    F32 = ctypes.c_float
     sig = {
         "segquant_calibrate_amax": [P, I64, I64, I64, I32, P, P, P, P],
         "segquant_calibrate_amax_single": [P, I64, I64, I64, I32, P, P, P, P],
@@ -103,6 +111,14 @@ def load_library():
                                            P, P, I64, P, U32, P],
         "segquant_gemm_workspace_bytes": [I64, I64, I64, I32, P, P, U32],
         "segquant_gemm_kernel_for": [I64, I64, I64, U32],
+        "segquant_groupnorm_quantize": [P, I64, I64, I64, I64, I32, F32, P, P, P, P, I64, I32, I32,
+                                        P, P, P, P, I64, I32, P, I64, P, ctypes.c_size_t, P],
+        "segquant_groupnorm_workspace_bytes": [I64, I64, I64, I32],
+        "segquant_adanorm_quantize": [P, I64, I64, I64, P, I64, P, P, I64, F32, P, P, P, P, I64,
+                                      I32, P, I32, P, P, P, P, I64, I32, P, I64, P],
+        "segquant_adapter_add": [I64, I64, I64, P, I64, I32, P, P, I32, I32, P, P, P, P, I32, P, P,
+                                 P, I64, P, I64, P, ctypes.c_size_t, P],
+        "segquant_adapter_workspace_bytes": [I64, I64, I64, I32, I32, I32],
         "segquant_gemm_halves": [P, I32],
         "segquant_version": [],
         "segquant_status_string": [ctypes.c_int],
@@ -118,6 +134,8 @@ def load_library():
     lib.segquant_weight_packed_bytes.restype = ctypes.c_size_t
     lib.segquant_weight_packed_bytes_w4.restype = ctypes.c_size_t
     lib.segquant_gemm_workspace_bytes.restype = ctypes.c_size_t
+    lib.segquant_groupnorm_workspace_bytes.restype = ctypes.c_size_t
+    lib.segquant_adapter_workspace_bytes.restype = ctypes.c_size_t
     _lib = lib
     return lib
 
@@ -390,4 +408,244 @@ def segquant_gemm_w8a8_seg_noalloc(x, w_packed, w_scale, act_scales, out,
                                               _ptr(out), _ld(out, "out"), _ptr(acc_debug), flags,
                                               _stream(src)),
            "segquant_gemm_w8a8_seg_noalloc")
+    return out
+
+
+# ------------------------------------- norms before and adapters beside ----
+@functools.lru_cache(maxsize=256)
+def _seg_arrays(widths: Optional[Tuple[int, ...]], total: int):
+    off, wid = _segs(widths, total)
+    return len(wid), off.ctypes.data, wid.ctypes.data, (off, wid)  # kept with their addresses
+
+
+def _segments(widths, total: int):
+    return _seg_arrays(None if widths is None else tuple(int(w) for w in widths), total)
+
+
+def _want(t, name: str, dtype, shape, device):
+    """Check an operand and return its address (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
+        raise ValueError(f"{name} must be {dtype} of shape {shape} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _row_ld(t, name: str) -> int:
+    """Elements between the rows of a [..., K] tensor whose rows are evenly
+    spaced (any value fits a single row)."""
+    if t is None:
+        return 0
+    K = t.shape[-1]
+    if t.numel() and t.stride(-1) != 1 and K > 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    ld = None
+    for d in range(t.dim() - 2, -1, -1):
+        if t.shape[d] == 1:
+            continue
+        below = 1
+        for e in range(d + 1, t.dim() - 1):
+            below *= t.shape[e]
+        if ld is None:
+            if t.stride(d) % below:
+                raise ValueError(f"{name}: its rows are not evenly spaced")
+            ld = t.stride(d) // below
+        elif t.stride(d) != ld * below:
+            raise ValueError(f"{name}: its rows are not evenly spaced")
+    return -(-K // 8) * 8 if ld is None else ld
+
+
+def _contiguous(t, name: str):
+    if t is not None and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _on(device, fn, *args):
+    """fn(*args, stream) on `device`'s current stream, with it current."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {device}")
+    if device.index == torch.cuda.current_device():
+        return fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    with torch.cuda.device(device):
+        return fn(*args, torch.cuda.current_stream(device).cuda_stream)
+
+
+def _workspace(workspace, nbytes: int, device):
+    import torch
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError("workspace must be a tensor, None or 'auto'")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    if workspace is None:
+        return None, 0, 0
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}")
+    _contiguous(workspace, "workspace")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _codes_out(out, wanted: bool, M: int, K: int, layout: int, device, fill: bool):
+    """The int8 output tensor (or None), its address and leading dimension."""
+    import torch
+    if not wanted:
+        return None, 0, 0
+    if out is None:
+        ldq = (K + 15) // 16 * 16
+        shape = (M, ldq) if layout == SEGQ_Q_SIGNED else (2, M, ldq)
+        out = (torch.zeros if fill else torch.empty)(shape, dtype=torch.int8, device=device)
+    planes = layout != SEGQ_Q_SIGNED
+    if (out.dtype != torch.int8 or out.device != device or out.dim() != (3 if planes else 2) or
+            out.shape[-2] != M or out.shape[-1] < K or (planes and out.shape[0] != 2)):
+        raise ValueError(f"out must be an int8 tensor of {'2 planes of ' if planes else ''}{M} rows "
+                         f"of at least {K} codes on {device}, got {out.dtype} {tuple(out.shape)} on "
+                         f"{out.device}")
+    ld = _row_ld(out[0] if planes else out, "out") if M > 1 else (out.shape[-1] + 15) // 16 * 16
+    if planes and out.stride(0) != M * ld:
+        raise ValueError("out: the second plane must follow the first")
+    return out, out.data_ptr(), ld
+
+
+def segquant_groupnorm_workspace_bytes(B: int, P: int, C: int, groups: int) -> int:
+    return int(load_library().segquant_groupnorm_workspace_bytes(B, P, C, groups))
+
+
+def segquant_groupnorm_quantize(z, groups: int, eps: float = 1e-5, gamma=None, beta=None,
+                                scale=None, shift=None, act_kind: int = SEGQ_ACT_NONE,
+                                act_scales=None, kseg: Optional[Sequence[int]] = None,
+                                layout: int = SEGQ_Q_SIGNED, out=None, x_out=None,
+                                want_codes: bool = True, workspace="auto"):
+    """Channels-last group norm of bf16 z [B][P][C] (P pixels of C channels;
+    an image [B][H][W][C] is z.flatten(1, 2)), with optional fp32 gamma and
+    beta [C], bf16 modulation scale and shift [B][C], and activation.
+    Returns (codes or None, x or None): codes [B*P][C] as
+    segquant_quantize_dualscale (when act_scales is given and want_codes), x
+    the bf16 [B][P][C] result if a tensor is passed (or x_out=True to allocate
+    one)."""
+    import torch
+    fn = load_library().segquant_groupnorm_quantize
+    if z.dim() != 3 or z.dtype != torch.bfloat16:
+        raise ValueError(f"z must be bfloat16 [B][P][C], got {z.dtype} {tuple(z.shape)}")
+    (B, P, C), dev = z.shape, z.device
+    if x_out is True:
+        x_out = torch.empty((B, P, -(-C // 8) * 8), dtype=torch.bfloat16, device=dev)[:, :, :C]
+    n, off, wid, _ = _segments(kseg, C)
+    act = _want(act_scales, "act_scales", torch.float32, (4, n), dev)
+    _contiguous(act_scales, "act_scales")
+    out, q, ld_q = _codes_out(out, want_codes and act_scales is not None, B * P, C, layout, dev,
+                              False)
+    for t, name in ((gamma, "gamma"), (beta, "beta")):
+        _contiguous(t, name)
+    if scale is not None and shift is not None and B > 1 and scale.stride(0) != shift.stride(0):
+        raise ValueError("scale and shift must have the same row stride")
+    mod = scale if scale is not None else shift
+    workspace, ws, ws_bytes = _workspace(workspace, segquant_groupnorm_workspace_bytes(
+        B, P, C, groups) if isinstance(workspace, str) else 0, dev)
+    _check(_on(dev, fn, z.data_ptr(), B, P, C, _row_ld(z, "z"), groups, eps,
+               _want(gamma, "gamma", torch.float32, (C,), dev),
+               _want(beta, "beta", torch.float32, (C,), dev),
+               _want(scale, "scale", torch.bfloat16, (B, C), dev),
+               _want(shift, "shift", torch.bfloat16, (B, C), dev), _row_ld(mod, "scale or shift"),
+               act_kind, n, off, wid, act, q, ld_q, layout,
+               _want(x_out, "x_out", torch.bfloat16, (B, P, C), dev), _row_ld(x_out, "x_out"),
+               ws, ws_bytes), "segquant_groupnorm_quantize")
+    return out, x_out
+
+
+def segquant_adanorm_quantize(h, eps: float = 1e-6, gamma=None, beta=None, scale=None, shift=None,
+                              gate=None, branch=None, row_offset=None, n_req: Optional[int] = None,
+                              act_scales=None, kseg: Optional[Sequence[int]] = None,
+                              layout: int = SEGQ_Q_SIGNED, out=None, x_out=None, h_out=None,
+                              want_codes: bool = True):
+    """The AdaNorm block before a layer, on bf16 rows h [M][K]: h' = h + gate *
+    branch (when branch is given), layer norm of h' with optional fp32 gamma
+    and beta [K], then * (1 + scale) + shift with the bf16 parameters [R][K]
+    of the row's request.  row_offset (int32 [R + 1] on the device) says which
+    rows each request has; without it the R = n_req (default: the rows of
+    scale, shift or gate, else 1) requests are equal.  Returns (codes or None,
+    x or None, h' or None): codes as segquant_quantize_dualscale (when
+    act_scales is given and want_codes), x and h' if a tensor is passed (or
+    True to allocate one).  Rows of no request are left as they are, zeros in
+    a tensor allocated here."""
+    import torch
+    fn = load_library().segquant_adanorm_quantize
+    if h.dim() != 2 or h.dtype != torch.bfloat16:
+        raise ValueError(f"h must be bfloat16 [M][K], got {h.dtype} {tuple(h.shape)}")
+    (M, K), dev, bf = h.shape, h.device, torch.bfloat16
+    mods = [t for t in (scale, shift, gate) if t is not None]
+    if row_offset is not None:
+        n_req = row_offset.numel() - 1
+    elif n_req is None:
+        n_req = mods[0].shape[0] if mods else 1
+    fill = row_offset is not None
+    new = torch.zeros if fill else torch.empty
+    if x_out is True:
+        x_out = new((M, -(-K // 8) * 8), dtype=bf, device=dev)[:, :K]
+    if h_out is True:
+        h_out = new((M, -(-K // 8) * 8), dtype=bf, device=dev)[:, :K]
+    n, off, wid, _ = _segments(kseg, K)
+    act = _want(act_scales, "act_scales", torch.float32, (4, n), dev)
+    out, q, ld_q = _codes_out(out, want_codes and act_scales is not None, M, K, layout, dev, fill)
+    for t, name in ((gamma, "gamma"), (beta, "beta"), (row_offset, "row_offset"),
+                    (act_scales, "act_scales")):
+        _contiguous(t, name)
+    if n_req > 1 and any(t.stride(0) != mods[0].stride(0) for t in mods):
+        raise ValueError("scale, shift and gate must have the same row stride")
+    _check(_on(dev, fn, h.data_ptr(), M, K, _row_ld(h, "h"),
+               _want(branch, "branch", bf, (M, K), dev), _row_ld(branch, "branch"),
+               _want(gate, "gate", bf, (n_req, K), dev), _want(h_out, "h_out", bf, (M, K), dev),
+               _row_ld(h_out, "h_out"), eps, _want(gamma, "gamma", torch.float32, (K,), dev),
+               _want(beta, "beta", torch.float32, (K,), dev),
+               _want(scale, "scale", bf, (n_req, K), dev),
+               _want(shift, "shift", bf, (n_req, K), dev),
+               _row_ld(mods[0], "scale, shift or gate") if mods else 0, n_req,
+               _want(row_offset, "row_offset", torch.int32, (n_req + 1,), dev), n, off, wid, act,
+               q, ld_q, layout, _want(x_out, "x_out", bf, (M, K), dev), _row_ld(x_out, "x_out")),
+           "segquant_adanorm_quantize")
+    return out, x_out, h_out
+
+
+def segquant_adapter_workspace_bytes(M: int, N: int, K: int, n_req: int, rank: int,
+                                     n_nseg: int = 1) -> int:
+    return int(load_library().segquant_adapter_workspace_bytes(M, N, K, n_req, rank, n_nseg))
+
+
+def segquant_adapter_add(x, a, b, adapter, row_offset, base=None, alpha=None, rank=None,
+                         nseg: Optional[Sequence[int]] = None, out=None, workspace="auto"):
+    """Low-rank adapters of many requests beside a shared layer: y = base +
+    alpha (x a^T) b^T with the adapter of each row's request.
+
+    x: bf16 [M][K], the layer's input; a: bf16 [n_adapters][n_nseg * r][K]
+    and b: bf16 [n_adapters][N][r], r the stored rank (a multiple of 16);
+    adapter: int32 [R], each request's adapter (-1: none); row_offset: int32
+    [R + 1]; base: bf16 [M][N], the layer's output (None: 0); alpha: fp32
+    [n_adapters]; rank: int32 [n_adapters], the true ranks; nseg: the layer's
+    N-segments.  Everything but nseg is on the device.  Returns bf16 y [M][N];
+    out may be base.  Rows of no request are left as they are, zeros in a
+    tensor allocated here."""
+    import torch
+    fn = load_library().segquant_adapter_add
+    bf, dev = torch.bfloat16, x.device
+    if x.dim() != 2 or x.dtype != bf or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x must be bfloat16 [M][K], a and b 3-D")
+    (M, K), (n_adapters, N, r), n_req = x.shape, b.shape, adapter.numel()
+    n, off, wid, _ = _segments(nseg, N)
+    if out is None:
+        out = torch.zeros((M, N), dtype=bf, device=dev)
+    for t, name in ((a, "a"), (b, "b"), (adapter, "adapter"), (row_offset, "row_offset"),
+                    (alpha, "alpha"), (rank, "rank")):
+        _contiguous(t, name)
+    workspace, ws, ws_bytes = _workspace(workspace, segquant_adapter_workspace_bytes(
+        M, N, K, n_req, r, n) if isinstance(workspace, str) else 0, dev)
+    _check(_on(dev, fn, M, N, K, x.data_ptr(), _row_ld(x, "x"), n_req,
+               _want(row_offset, "row_offset", torch.int32, (n_req + 1,), dev),
+               _want(adapter, "adapter", torch.int32, (n_req,), dev), n_adapters, r,
+               _want(rank, "rank", torch.int32, (n_adapters,), dev),
+               _want(a, "a", bf, (n_adapters, n * r, K), dev),
+               _want(b, "b", bf, (n_adapters, N, r), dev),
+               _want(alpha, "alpha", torch.float32, (n_adapters,), dev), n, off, wid,
+               _want(base, "base", bf, (M, N), dev), _row_ld(base, "base"),
+               _want(out, "out", bf, (M, N), dev), _row_ld(out, "out"), ws, ws_bytes),
+           "segquant_adapter_add")
     return out

@@ -26,6 +26,7 @@
 // of rows.  Inside a workgroup each wave walks rows; L lanes (a power of two
 // up to 64) share one row and step through it 8 elements (16 bytes) at a
 // time, so narrow segments (64 columns = 8 chunks) still fill the wave.
+#include "sq_activation.hpp"
 #include "sq_device.hpp"
 #include "sq_launch.hpp"
 
@@ -211,57 +212,6 @@ __global__ __launch_bounds__(256) void quantize_kernel(ActArgs a) {
       }
     }
   }
-}
-
-// GELU in its exact form z/2 (1 + erf(z / sqrt 2)), evaluated as
-// z/2 erfc(-z / sqrt 2): the same function, but 1 + erf cancels to nothing in
-// fp32 for z below about -4 while erfc keeps its relative precision.
-// erfc(x), x = |z| / sqrt 2 >= 0, in the form of Numerical Recipes (Press et
-// al., "Numerical Recipes in C", 2nd ed., section 6.2): t exp(-x^2 + P(t)),
-// t = 1 / (1 + x/2), P a degree-9 Chebyshev fit, relative error below 1.2e-7
-// for every x >= 0.  Branch free: erfc(-x) = 2 - erfc(x) gives z >= 0.
-// Rounding x itself would cost about 2 x^2 ulps in the tail, so x enters
-// only t; -x^2 = -z^2/2 is carried as an exact pair (one product and its FMA
-// error), and its product with log2 e is split so that exp2 of the large
-// part sees none of the small part's rounding.  With one-ulp reciprocal and
-// exp2 the result is within 2^-20 of the true value, relative, over the
-// whole bf16 input range (swept on the CPU with those errors injected).
-// Large parts below -120 are evaluated 64 binades up and scaled back
-// exactly, so results in the subnormal range are not flushed.
-__device__ __forceinline__ float gelu_f32(float z) {
-  const float kLog2e = 1.44269504f;             // log2 e, rounded to fp32
-  const float kLog2eLo = 1.92596303e-08f;       // log2 e - kLog2e
-  const float a = fminf(fabsf(z), 20.0f);  // erfc(20 / sqrt 2) underflows: the same result
-  const float x = a * 0.70710678f;
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, x, 1.0f));
-  float P = __builtin_fmaf(t, 0.17087277f, -0.82215223f);
-  P = __builtin_fmaf(t, P, 1.48851587f);
-  P = __builtin_fmaf(t, P, -1.13520398f);
-  P = __builtin_fmaf(t, P, 0.27886807f);
-  P = __builtin_fmaf(t, P, -0.18628806f);
-  P = __builtin_fmaf(t, P, 0.09678418f);
-  P = __builtin_fmaf(t, P, 0.37409196f);
-  P = __builtin_fmaf(t, P, 1.00002368f);
-  P = __builtin_fmaf(t, P, -1.26551223f);
-  const float p = a * a, e = __builtin_fmaf(a, a, -p);  // z^2 = p + e exactly
-  const float q = -0.5f * p, qe = -0.5f * e;           // -x^2 = q + qe exactly
-  const float hi = q * kLog2e;
-  float lo = __builtin_fmaf(q, kLog2e, -hi);
-  lo = __builtin_fmaf(q, kLog2eLo, lo);
-  lo = __builtin_fmaf(qe + P, kLog2e, lo);
-  const bool deep = hi < -120.0f;
-  const float eh = __builtin_amdgcn_exp2f(deep ? hi + 64.0f : hi) * (deep ? 0x1p-64f : 1.0f);
-  const float E = t * eh * __builtin_amdgcn_exp2f(lo);
-  return 0.5f * z * (z < 0.0f ? E : 2.0f - E);
-}
-
-// SiLU z / (1 + e^-z) as z sigmoid(z), the sigmoid from e^-|z| (library
-// expf): e^-z itself overflows for z below about -88.7, where z / (1 + e^-z)
-// would give 0 while the true value is still a normal float.
-__device__ __forceinline__ float silu_f32(float z) {
-  const float ez = expf(-fabsf(z));
-  const float r = 1.0f / (1.0f + ez);
-  return z * (z >= 0.0f ? r : ez * r);
 }
 
 // Activation of one element in fp32 [P1/P2: the SiLU and GELU outputs whose

@@ -238,7 +238,7 @@ const char *segquant_status_string(int status) {
 
 const char *segquant_last_error(void) { return g_err.c_str(); }
 
-int segquant_version(void) { return 100; }
+int segquant_version(void) { return 110; }
 
 size_t segquant_weight_packed_bytes_w4(int64_t K, int64_t N) {
   return segquant_weight_packed_bytes(K, N) / 2;
@@ -323,6 +323,263 @@ int segquant_activate_quantize(const uint16_t *z_bf16, int64_t M, int64_t K, int
   return hip_status(sq::launch_act_quantize(z_bf16, M, K, ld_z, act_kind, ks, act_scales, q_out,
                                             ld_q, q_layout, x_out, ld_xo, (hipStream_t)stream),
                     "activate-quantize launch");
+}
+
+// The outputs shared by the calls that produce a layer's input: int8 codes
+// (with their scales), bf16 x, or both, of M rows of K columns.
+static int check_norm_out(int64_t M, int64_t K, int32_t n_kseg, const int32_t *kseg_offset,
+                          const int32_t *kseg_width, const float *act_scales, int8_t *q_out,
+                          int64_t ld_q, int32_t q_layout, uint16_t *x_out, int64_t ld_xo,
+                          sq::NormOut &o) {
+  if (q_out) {
+    if (!act_scales) return fail(SEGQ_ERR_NULL, "act_scales is NULL");
+    if (q_layout != SEGQ_Q_SIGNED && q_layout != SEGQ_Q_PLANES)
+      return fail(SEGQ_ERR_SHAPE, "unknown q_layout %d", q_layout);
+    if (ld_q < K) return fail(SEGQ_ERR_SHAPE, "ld_q %lld < K %lld", (long long)ld_q, (long long)K);
+    if (ld_q % 16 != 0)
+      return fail(SEGQ_ERR_ALIGN, "ld_q %lld is not a multiple of 16", (long long)ld_q);
+    if (!aligned16(q_out)) return fail(SEGQ_ERR_ALIGN, "q_out is not 16-byte aligned");
+  }
+  if (x_out) {
+    if (ld_xo < K) return fail(SEGQ_ERR_SHAPE, "ld_xo %lld < K %lld", (long long)ld_xo, (long long)K);
+    if (ld_xo % 8 != 0 || !aligned16(x_out))
+      return fail(SEGQ_ERR_ALIGN, "x_out must be 16-byte aligned with ld_xo a multiple of 8");
+  }
+  o.x = x_out;
+  o.ld_x = ld_xo;
+  o.q = q_out;
+  o.ld_q = ld_q;
+  o.plane_stride = q_layout == SEGQ_Q_PLANES ? M * ld_q : 0;
+  o.act = act_scales;
+  return read_kseg(n_kseg, kseg_offset, kseg_width, K, 0, o.ks);
+}
+
+// An optional bf16 matrix: pointer, leading dimension, row length.
+static int check_rows(const uint16_t *p, int64_t ld, int64_t len, const char *what) {
+  if (!p) return SEGQ_OK;
+  if (ld < len)
+    return fail(SEGQ_ERR_SHAPE, "%s: leading dimension %lld < %lld", what, (long long)ld,
+                (long long)len);
+  if (ld % 8 != 0 || !aligned16(p))
+    return fail(SEGQ_ERR_ALIGN, "%s must be 16-byte aligned with a leading dimension that is a "
+                "multiple of 8", what);
+  return SEGQ_OK;
+}
+
+static int check_norm_params(const float *gamma, const float *beta, float eps) {
+  if (!(eps > 0.0f) || eps > 3.0e38f) return fail(SEGQ_ERR_SHAPE, "eps must be positive and finite");
+  if (!aligned16(gamma) || !aligned16(beta))
+    return fail(SEGQ_ERR_ALIGN, "gamma or beta is not 16-byte aligned");
+  return SEGQ_OK;
+}
+
+static int groupnorm_sizes(int64_t B, int64_t P, int64_t C, int32_t groups,
+                           sq::GroupNormProblem &p) {
+  if (B < 0 || P < 0 || C < 1 || B > kI32Max || P > kI32Max || C > kI32Max ||
+      (P > 0 && B > kI32Max / P))
+    return fail(SEGQ_ERR_SHAPE, "bad shape B=%lld P=%lld C=%lld", (long long)B, (long long)P,
+                (long long)C);
+  if (groups < 1 || C % groups != 0)
+    return fail(SEGQ_ERR_SHAPE, "%d groups do not divide %lld channels", groups, (long long)C);
+  if (C > (1 << 20) || B > 65535)
+    return fail(SEGQ_ERR_UNSUPPORTED, "C %lld > 2^20 or B %lld > 65535", (long long)C,
+                (long long)B);
+  p.B = B;
+  p.P = P;
+  p.C = (int32_t)C;
+  p.G = groups;
+  p.D = (int32_t)(C / groups);
+  return SEGQ_OK;
+}
+
+size_t segquant_groupnorm_workspace_bytes(int64_t B, int64_t P, int64_t C, int32_t groups) {
+  sq::GroupNormProblem p{};
+  if (groupnorm_sizes(B, P, C, groups, p)) return 0;
+  ok();
+  return B && P ? sq::groupnorm_workspace_bytes(p) : 0;
+}
+
+int segquant_groupnorm_quantize(const uint16_t *z_bf16, int64_t B, int64_t P, int64_t C,
+                                int64_t ld_z, int32_t groups, float eps, const float *gamma,
+                                const float *beta, const uint16_t *scale, const uint16_t *shift,
+                                int64_t ld_mod, int32_t act_kind, int32_t n_kseg,
+                                const int32_t *kseg_offset, const int32_t *kseg_width,
+                                const float *act_scales, int8_t *q_out, int64_t ld_q,
+                                int32_t q_layout, uint16_t *x_out, int64_t ld_xo, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+  sq::GroupNormProblem p{};
+  int st = groupnorm_sizes(B, P, C, groups, p);
+  if (st) return st;
+  const int64_t M = B * P;
+  if ((st = check_x(z_bf16, M, C, ld_z))) return st;
+  if ((st = check_norm_params(gamma, beta, eps))) return st;
+  if ((st = check_rows(scale, ld_mod, C, "scale"))) return st;
+  if ((st = check_rows(shift, ld_mod, C, "shift"))) return st;
+  if (act_kind != SEGQ_ACT_NONE && act_kind != SEGQ_ACT_SILU && act_kind != SEGQ_ACT_GELU)
+    return fail(SEGQ_ERR_SHAPE, "unknown act_kind %d", act_kind);
+  if (M > 0 && !q_out && !x_out) return fail(SEGQ_ERR_NULL, "neither q_out nor x_out is given");
+  if ((st = check_norm_out(M, C, n_kseg, kseg_offset, kseg_width, act_scales, q_out, ld_q, q_layout,
+                           x_out, ld_xo, p.out)))
+    return st;
+  if (x_out && x_out == z_bf16 && ld_xo != ld_z)
+    return fail(SEGQ_ERR_SHAPE, "x_out on z_bf16 needs ld_xo = ld_z");
+  if (M == 0) return ok();
+  const size_t need = sq::groupnorm_workspace_bytes(p);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(SEGQ_ERR_UNSUPPORTED,
+                "this shape needs a workspace of at least %zu bytes "
+                "(segquant_groupnorm_workspace_bytes)", need);
+  if (workspace && !aligned16(workspace))
+    return fail(SEGQ_ERR_ALIGN, "workspace is not 16-byte aligned");
+  p.z = z_bf16;
+  p.ld_z = ld_z;
+  p.eps = eps;
+  p.gamma = gamma;
+  p.beta = beta;
+  p.scale = scale;
+  p.shift = shift;
+  p.ld_mod = ld_mod;
+  p.act = act_kind;
+  p.part = static_cast<float *>(workspace);
+  return hip_status(sq::launch_groupnorm(p, (hipStream_t)stream), "groupnorm launch");
+}
+
+int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int64_t ld_h,
+                              const uint16_t *branch, int64_t ld_b, const uint16_t *gate,
+                              uint16_t *h_out, int64_t ld_ho, float eps, const float *gamma,
+                              const float *beta, const uint16_t *scale, const uint16_t *shift,
+                              int64_t ld_mod, int32_t n_req, const int32_t *row_offset,
+                              int32_t n_kseg, const int32_t *kseg_offset,
+                              const int32_t *kseg_width, const float *act_scales, int8_t *q_out,
+                              int64_t ld_q, int32_t q_layout, uint16_t *x_out, int64_t ld_xo,
+                              void *stream) {
+  sq::AdaNormProblem p{};
+  int st = check_x(h_bf16, M, K, ld_h);
+  if (st) return st;
+  if (n_req < 1) return fail(SEGQ_ERR_SHAPE, "n_req %d < 1", n_req);
+  if (!row_offset && M % n_req != 0)
+    return fail(SEGQ_ERR_SHAPE, "%d equal requests do not divide %lld rows", n_req, (long long)M);
+  if (reinterpret_cast<uintptr_t>(row_offset) & 3u)
+    return fail(SEGQ_ERR_ALIGN, "row_offset is not 4-byte aligned");
+  if (!branch && (gate || h_out)) return fail(SEGQ_ERR_NULL, "gate or h_out without branch");
+  if ((st = check_norm_params(gamma, beta, eps))) return st;
+  if ((st = check_rows(branch, ld_b, K, "branch"))) return st;
+  if ((st = check_rows(h_out, ld_ho, K, "h_out"))) return st;
+  if ((st = check_rows(gate, ld_mod, K, "gate"))) return st;
+  if ((st = check_rows(scale, ld_mod, K, "scale"))) return st;
+  if ((st = check_rows(shift, ld_mod, K, "shift"))) return st;
+  if (h_out && h_out == h_bf16 && ld_ho != ld_h)
+    return fail(SEGQ_ERR_SHAPE, "h_out on h_bf16 needs ld_ho = ld_h");
+  if (M > 0 && !q_out && !x_out && !h_out)
+    return fail(SEGQ_ERR_NULL, "none of q_out, x_out and h_out is given");
+  if ((st = check_norm_out(M, K, n_kseg, kseg_offset, kseg_width, act_scales, q_out, ld_q, q_layout,
+                           x_out, ld_xo, p.out)))
+    return st;
+  if (M == 0) return ok();
+  p.h = h_bf16;
+  p.M = M;
+  p.K = K;
+  p.ld_h = ld_h;
+  p.branch = branch;
+  p.gate = gate;
+  p.ld_b = ld_b;
+  p.h_out = h_out;
+  p.ld_ho = ld_ho;
+  p.eps = eps;
+  p.gamma = gamma;
+  p.beta = beta;
+  p.scale = scale;
+  p.shift = shift;
+  p.ld_mod = ld_mod;
+  p.row_offset = row_offset;
+  p.n_req = n_req;
+  p.rows_per_req = M / n_req;
+  return hip_status(sq::launch_adanorm(p, (hipStream_t)stream), "adanorm launch");
+}
+
+static int adapter_sizes(int64_t M, int64_t N, int64_t K, int32_t n_req, int32_t rank,
+                         int32_t n_nseg, sq::AdapterProblem &p) {
+  if (M < 0 || N < 1 || K < 1 || M > kI32Max || N > kI32Max || K > kI32Max)
+    return fail(SEGQ_ERR_SHAPE, "bad shape M=%lld N=%lld K=%lld", (long long)M, (long long)N,
+                (long long)K);
+  if (K % 64 || N % 16)
+    return fail(SEGQ_ERR_ALIGN, "adapters need K %% 64 == 0 and N %% 16 == 0 (K=%lld N=%lld)",
+                (long long)K, (long long)N);
+  if (M > (1 << 27) || n_req > (1 << 23))
+    return fail(SEGQ_ERR_UNSUPPORTED, "M %lld > 2^27 or n_req %d > 2^23", (long long)M, n_req);
+  if (n_req < 1) return fail(SEGQ_ERR_SHAPE, "n_req %d < 1", n_req);
+  if (rank < 1 || rank % SEGQ_ADAPTER_RANK_STEP)
+    return fail(SEGQ_ERR_ALIGN, "rank %d is not a multiple of %d", rank, SEGQ_ADAPTER_RANK_STEP);
+  if (rank > SEGQ_ADAPTER_RANK_MAX)
+    return fail(SEGQ_ERR_UNSUPPORTED, "rank %d > %d", rank, SEGQ_ADAPTER_RANK_MAX);
+  if (n_nseg < 1) return fail(SEGQ_ERR_SEGMENTS, "N-segment count %d < 1", n_nseg);
+  if (n_nseg > sq::kMaxNSeg)
+    return fail(SEGQ_ERR_UNSUPPORTED, "N-segment count %d > %d", n_nseg, sq::kMaxNSeg);
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.n_req = n_req;
+  p.rank = rank;
+  p.ns.n = n_nseg;
+  return SEGQ_OK;
+}
+
+size_t segquant_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t n_req,
+                                        int32_t rank, int32_t n_nseg) {
+  sq::AdapterProblem p{};
+  if (adapter_sizes(M, N, K, n_req, rank, n_nseg, p)) return 0;
+  ok();
+  return M ? sq::adapter_workspace_bytes(p) : 0;
+}
+
+int segquant_adapter_add(int64_t M, int64_t N, int64_t K, const uint16_t *x_bf16, int64_t ld_x,
+                         int32_t n_req, const int32_t *row_offset, const int32_t *adapter,
+                         int32_t n_adapters, int32_t rank, const int32_t *rank_of,
+                         const uint16_t *a, const uint16_t *b, const float *alpha, int32_t n_nseg,
+                         const int32_t *nseg_offset, const int32_t *nseg_width,
+                         const uint16_t *base_bf16, int64_t ld_base, uint16_t *y_bf16,
+                         int64_t ld_y, void *workspace, size_t workspace_bytes, void *stream) {
+  sq::AdapterProblem p{};
+  int st = adapter_sizes(M, N, K, n_req, rank, n_nseg, p);
+  if (st) return st;
+  if (n_adapters < 1) return fail(SEGQ_ERR_SHAPE, "n_adapters %d < 1", n_adapters);
+  if ((st = check_x(x_bf16, M, K, ld_x))) return st;
+  if ((st = read_nseg(n_nseg, nseg_offset, nseg_width, N, p.ns))) return st;
+  for (int32_t i = 0; i < p.ns.n; ++i)
+    if (p.ns.off[i] % 16)
+      return fail(SEGQ_ERR_ALIGN, "N-segment boundary %d is not a multiple of 16", p.ns.off[i]);
+  if (M == 0) return ok();
+  if (!row_offset || !adapter || !a || !b || !y_bf16)
+    return fail(SEGQ_ERR_NULL, "row_offset, adapter, a, b or y_bf16 is NULL");
+  if (!aligned16(a) || !aligned16(b)) return fail(SEGQ_ERR_ALIGN, "a or b is not 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(row_offset) | reinterpret_cast<uintptr_t>(adapter) |
+       reinterpret_cast<uintptr_t>(rank_of) | reinterpret_cast<uintptr_t>(alpha)) & 3u)
+    return fail(SEGQ_ERR_ALIGN, "row_offset, adapter, rank_of or alpha is not 4-byte aligned");
+  if ((st = check_rows(base_bf16, ld_base, N, "base_bf16"))) return st;
+  if ((st = check_rows(y_bf16, ld_y, N, "y_bf16"))) return st;
+  if (base_bf16 == y_bf16 && ld_base != ld_y)
+    return fail(SEGQ_ERR_SHAPE, "base_bf16 on y_bf16 needs ld_base = ld_y");
+  const size_t need = sq::adapter_workspace_bytes(p);
+  if (!workspace || workspace_bytes < need)
+    return fail(SEGQ_ERR_UNSUPPORTED,
+                "adapters need a workspace of at least %zu bytes "
+                "(segquant_adapter_workspace_bytes)", need);
+  if (!aligned16(workspace)) return fail(SEGQ_ERR_ALIGN, "workspace is not 16-byte aligned");
+  p.x = x_bf16;
+  p.ld_x = ld_x;
+  p.row_offset = row_offset;
+  p.adapter = adapter;
+  p.n_adapters = n_adapters;
+  p.rank_of = rank_of;
+  p.a = a;
+  p.b = b;
+  p.alpha = alpha;
+  p.base = base_bf16;
+  p.ld_base = ld_base;
+  p.y = y_bf16;
+  p.ld_y = ld_y;
+  p.t = static_cast<float *>(workspace);
+  return hip_status(sq::launch_adapter(p, (hipStream_t)stream), "adapter launch");
 }
 
 static int quantize_weight(const float *w, int64_t K, int64_t N, int64_t ld_w, int32_t n_kseg,

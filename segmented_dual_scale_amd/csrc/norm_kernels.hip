@@ -1,0 +1,818 @@
+// norm_kernels.hip -- the normalisations in front of a quantised linear layer,
+// fused with the activation, the modulation and the DualScale quantisation:
+//   * channels-last group norm with SiLU / GELU (image UNets), and
+//   * layer norm modulated by a request's shift and scale, with the gated
+//     residual update before it: the AdaNorm block whose conditioning layer
+//     emits shift, scale and gate [P2 section 1; P1 "SegLinear", the AdaNorm
+//     chunking].
+// Both emit the layer's input as bf16 X, as its int8 codes, or both, so the
+// normalised X need not return from memory to be quantised.
+//
+// [P1] "SegQuant: A Semantics-Aware and Generalizable Quantization Framework
+//      for Diffusion Models" (papernotes.org notes).
+// [P2] "SegQuant" (hliangzhao.me).
+//
+// Statistics are fp32 and never E[x^2] - E[x]^2: the mean is known, or taken
+// over a few values in registers, before squares are summed, and pieces are
+// joined as (count, mean, sum of squared deviations).
+#include "sq_activation.hpp"
+#include "sq_device.hpp"
+#include "sq_launch.hpp"
+
+namespace sq {
+
+namespace {
+
+// ------------------------------------------------------ 8-element pieces --
+__device__ __forceinline__ void unpack8(v4u v, float f[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = bf16_lo(v[j]);
+    f[2 * j + 1] = bf16_hi(v[j]);
+  }
+}
+
+__device__ __forceinline__ v4u pack8(const float f[8]) {
+  v4u v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+  return v;
+}
+
+// Up to 8 bf16 at p, 16-byte aligned; the elements from n on read as 0 and
+// are not touched (a row's last piece may end with the allocation).  TAIL:
+// rows end inside a piece; without it n is 8 or 0, and the element-wise code
+// of every access (half of the kernel's registers) is not built.
+template <bool TAIL>
+__device__ __forceinline__ v4u load8(const uint16_t *p, int n) {
+  v4u v = {0u, 0u, 0u, 0u};
+  if (n >= 8) return *reinterpret_cast<const v4u *>(p);
+  if (!TAIL) return v;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) v[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+  return v;
+}
+
+template <bool TAIL>
+__device__ __forceinline__ void store8(uint16_t *p, v4u v, int n) {
+  if (n >= 8) *reinterpret_cast<v4u *>(p) = v;
+  if (!TAIL || n >= 8) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) p[j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+}
+
+template <bool TAIL>
+__device__ __forceinline__ void store8(int8_t *p, v2u v, int n) {
+  if (n >= 8) *reinterpret_cast<v2u *>(p) = v;
+  if (!TAIL || n >= 8) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) p[j] = (int8_t)(v[j >> 2] >> (8 * (j & 3)));
+}
+
+// 8 fp32 parameters at p (16-byte aligned), dflt where there are none.
+template <bool TAIL>
+__device__ __forceinline__ void load8f(const float *p, int n, float dflt, float f[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = dflt;
+  if (!p) return;
+  if (n >= 8) {
+    const v4f lo = *reinterpret_cast<const v4f *>(p), hi = *reinterpret_cast<const v4f *>(p + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = lo[j], f[4 + j] = hi[j];
+  } else if (TAIL) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) f[j] = p[j];
+  }
+}
+
+// Inverse scales of the K-segment that holds column k (every boundary is a
+// multiple of 64, so an 8-element piece lies in one segment).
+__device__ __forceinline__ void seg_scales(const NormOut &o, int64_t k, float &ip, float &in) {
+  int seg = 0;
+  while (seg + 1 < o.ks.n && k >= o.ks.end[seg]) ++seg;
+  ip = o.act[2 * o.ks.n + seg];
+  in = o.act[3 * o.ks.n + seg];
+}
+
+// Bf16 piece x of row `row`, columns k .. k+n-1 -> the outputs asked for.
+template <bool TAIL>
+__device__ __forceinline__ void emit8(const NormOut &o, int64_t row, int64_t k, int n, v4u x,
+                                      float ip, float in) {
+  if (o.x) store8<TAIL>(o.x + row * o.ld_x + k, x, n);
+  if (o.q) {
+    int8_t *q = o.q + row * o.ld_q + k;
+    if (o.plane_stride) {
+      v2u p, m;
+      quant8_planes(x, ip, in, p, m);
+      store8<TAIL>(q, p, n);
+      store8<TAIL>(q + o.plane_stride, m, n);
+    } else {
+      store8<TAIL>(q, quant8_signed(x, ip, in), n);
+    }
+  }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// ------------------------------------------------- modulated layer norm --
+// One row per TPR threads (a wave, or a workgroup of four), NCH 16-byte
+// pieces per thread held in registers: read once, mean and squared deviations
+// from the registers, written once.  A row group walks rows_per consecutive
+// rows and keeps the request's shift, scale and gate in registers between
+// them.
+
+// Sum over the TPR threads of a row.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float *lds) {
+  v = wave_sum(v);
+  if (TPR > 64) {
+    __syncthreads();  // the last sum's readers are done with lds
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < TPR / 64; ++w) v += lds[w];
+  }
+  return v;
+}
+
+template <int TPR, int NCH, bool TAIL>
+__global__ __launch_bounds__(256) void adanorm_kernel(AdaNormProblem a) {
+  __shared__ float lds[4];
+  const int t = threadIdx.x % TPR;
+  const int64_t first =
+      ((int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR) * a.rows_per;
+  const int64_t last = min(first + a.rows_per, a.M);
+  const float inv_k = 1.0f / (float)a.K;
+  // NCH is the piece count of thread 0: only the last piece can be short
+  const int n_last = min(8, max(0, (int)a.K - 8 * (t + (NCH - 1) * TPR)));
+#define SQ_N(c) ((c) < NCH - 1 ? 8 : n_last)
+  float ip[NCH], in[NCH];
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    ip[c] = in[c] = 0.0f;
+    if (a.out.q && SQ_N(c) > 0) seg_scales(a.out, 8 * (t + c * TPR), ip[c], in[c]);
+  }
+  v4u sc[NCH], sh[NCH], ga[NCH];
+  int64_t until = first;  // sc, sh and ga hold for the rows before this one
+  for (int64_t r = first; r < last; ++r) {
+    if (r >= until) {
+      int64_t req;
+      if (a.row_offset) {
+        const RowRequest f = find_request(a.row_offset, a.n_req, r);
+        if (f.req >= a.n_req) break;  // behind the last request: left as it is
+        if (f.req < 0) continue;      // before the first one
+        req = f.req;
+        until = f.end;
+      } else {
+        req = r / a.rows_per_req;
+        until = (req + 1) * a.rows_per_req;
+      }
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        const int64_t at = req * a.ld_mod + 8 * (t + c * TPR);
+        sc[c] = sh[c] = ga[c] = v4u{0u, 0u, 0u, 0u};
+        if (a.scale) sc[c] = load8<TAIL>(a.scale + at, SQ_N(c));
+        if (a.shift) sh[c] = load8<TAIL>(a.shift + at, SQ_N(c));
+        if (a.gate) ga[c] = load8<TAIL>(a.gate + at, SQ_N(c));
+      }
+    }
+    v4u h[NCH];
+    const uint16_t *hr = a.h + r * a.ld_h + 8 * t;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) h[c] = load8<TAIL>(hr + 8 * c * TPR, SQ_N(c));
+    if (a.branch) {
+      v4u y[NCH];
+      const uint16_t *br = a.branch + r * a.ld_b + 8 * t;
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) y[c] = load8<TAIL>(br + 8 * c * TPR, SQ_N(c));
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        float f[8], g[8], b[8];
+        unpack8(h[c], f);
+        unpack8(ga[c], g);
+        unpack8(y[c], b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = f[j] + (a.gate ? g[j] * b[j] : b[j]);
+        h[c] = pack8(f);  // the norm reads the residual stream as it is stored
+        if (a.h_out)
+          store8<TAIL>(a.h_out + r * a.ld_ho + 8 * (t + c * TPR), h[c], SQ_N(c));
+      }
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      float f[8];
+      unpack8(h[c], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += f[j];
+    }
+    const float mean = row_sum<TPR>(s, lds) * inv_k;
+    float s2 = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      float f[8];
+      unpack8(h[c], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float d = f[j] - mean;
+        if (c == NCH - 1 && j >= n_last) d = 0.0f;
+        s2 = __builtin_fmaf(d, d, s2);
+      }
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<TPR>(s2, lds) * inv_k + a.eps);
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      if (c == NCH - 1 && n_last == 0) continue;
+      const int k = 8 * (t + c * TPR);
+      float f[8], m[8], b[8];
+      unpack8(h[c], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = (f[j] - mean) * rstd;
+      if (a.gamma || a.beta) {
+        load8f<TAIL>(a.gamma ? a.gamma + k : nullptr, SQ_N(c), 1.0f, m);
+        load8f<TAIL>(a.beta ? a.beta + k : nullptr, SQ_N(c), 0.0f, b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf(f[j], m[j], b[j]);
+      }
+      unpack8(sc[c], m);
+      unpack8(sh[c], b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf(f[j], m[j], f[j]) + b[j];
+      emit8<TAIL>(a.out, r, k, SQ_N(c), pack8(f), ip[c], in[c]);
+    }
+  }
+#undef SQ_N
+}
+
+// Rows longer than the registers take: one workgroup per row, the row read
+// three times (the second and third from the cache).
+__global__ __launch_bounds__(256) void adanorm_long_kernel(AdaNormProblem a) {
+  __shared__ float lds[4];
+  for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
+    int64_t req;
+    if (a.row_offset) {
+      const RowRequest f = find_request(a.row_offset, a.n_req, r);
+      if (f.req < 0 || f.req >= a.n_req) continue;
+      req = f.req;
+    } else {
+      req = r / a.rows_per_req;
+    }
+    const uint16_t *h = a.h + r * a.ld_h;
+    const uint16_t *ga = a.gate ? a.gate + req * a.ld_mod : nullptr;
+    // h' of piece k, recomputed in each pass
+    auto piece = [&](int64_t k, int n, float f[8]) -> v4u {
+      v4u v = load8<true>(h + k, n);
+      if (a.branch) {
+        float g[8], b[8];
+        unpack8(v, f);
+        unpack8(load8<true>(a.branch + r * a.ld_b + k, n), b);
+        if (ga) unpack8(load8<true>(ga + k, n), g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = f[j] + (ga ? g[j] * b[j] : b[j]);
+        v = pack8(f);
+      }
+      unpack8(v, f);
+      return v;
+    };
+    float s = 0.0f, s2 = 0.0f, f[8];
+    for (int64_t k = 8 * (int64_t)threadIdx.x; k < a.K; k += 8 * 256) {
+      piece(k, (int)min((int64_t)8, a.K - k), f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += f[j];
+    }
+    const float mean = row_sum<256>(s, lds) / (float)a.K;
+    for (int64_t k = 8 * (int64_t)threadIdx.x; k < a.K; k += 8 * 256) {
+      const int n = (int)min((int64_t)8, a.K - k);
+      piece(k, n, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = j < n ? f[j] - mean : 0.0f;
+        s2 = __builtin_fmaf(d, d, s2);
+      }
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<256>(s2, lds) / (float)a.K + a.eps);
+    for (int64_t k = 8 * (int64_t)threadIdx.x; k < a.K; k += 8 * 256) {
+      const int n = (int)min((int64_t)8, a.K - k);
+      float m[8], b[8], ip = 0.0f, in = 0.0f;
+      // each thread reads its piece of h before it writes the same piece of
+      // h_out, and no later pass reads either: h_out may be h itself
+      const v4u v = piece(k, n, f);
+      if (a.branch && a.h_out) store8<true>(a.h_out + r * a.ld_ho + k, v, n);
+      load8f<true>(a.gamma ? a.gamma + k : nullptr, n, 1.0f, m);
+      load8f<true>(a.beta ? a.beta + k : nullptr, n, 0.0f, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf((f[j] - mean) * rstd, m[j], b[j]);
+      v4u sc = {0u, 0u, 0u, 0u}, sh = sc;
+      if (a.scale) sc = load8<true>(a.scale + req * a.ld_mod + k, n);
+      if (a.shift) sh = load8<true>(a.shift + req * a.ld_mod + k, n);
+      unpack8(sc, m);
+      unpack8(sh, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf(f[j], m[j], f[j]) + b[j];
+      if (a.out.q) seg_scales(a.out, k, ip, in);
+      emit8<true>(a.out, r, k, n, pack8(f), ip, in);
+    }
+  }
+}
+
+// ---------------------------------------------------------- group norm ----
+// Channels last: row p of a sample holds its C channels; a group is D = C/G
+// neighbouring channels of every row.  A workgroup covers `cb` 16-byte
+// columns (8 channels each) of a range of rows; thread t keeps column t % cb
+// and walks rows t / cb, + rs, ... so its per-channel values stay in
+// registers and consecutive threads read consecutive bytes.
+struct GnTile {
+  int cb, col, rsub, rs;  // columns; this thread's column, first row; rows per step
+  bool active;
+  int c0, c1;  // channels of the workgroup's columns
+  int g0, ng;  // groups they touch
+  int c, nv;   // this thread's first channel and how many of its 8 exist
+};
+
+template <int T, bool TAIL>
+__device__ __forceinline__ GnTile gn_tile(const GroupNormProblem &a, int c0, int c1) {
+  GnTile t;
+  t.c0 = c0;
+  t.c1 = c1;
+  t.cb = (c1 - c0 + 7) / 8;
+  t.rs = T / t.cb;
+  t.col = threadIdx.x % t.cb;
+  t.rsub = threadIdx.x / t.cb;
+  t.active = t.rsub < t.rs;
+  t.g0 = c0 / a.D;
+  t.ng = (c1 - 1) / a.D - t.g0 + 1;
+  t.c = c0 + 8 * t.col;
+  t.nv = TAIL ? min(8, c1 - t.c) : 8;
+  return t;
+}
+
+// LDS of a workgroup: T*8 thread values, then 8 cb channel sums, then two
+// values per group (at most 8 cb groups).
+template <int T>
+struct GnLds {
+  float *buf, *chan, *gs, *gr;
+  __device__ GnLds(float *base, int cb)
+      : buf(base), chan(base + T * 8), gs(chan + 8 * cb), gr(gs + 8 * cb) {}
+};
+
+size_t gn_lds_bytes(int T, int cb) { return sizeof(float) * ((size_t)T * 8 + 24 * (size_t)cb); }
+
+// Threads that share one group in a group-wise step: a power of two up to a
+// wave, as many as still cover all groups in one step.
+template <int T>
+__device__ __forceinline__ int threads_per_group(int ng) {
+  int n = 1;
+  while (n < 64 && 2 * n * ng <= T) n *= 2;
+  return n;
+}
+
+__device__ __forceinline__ float part_sum(float v, int n) {  // over n neighbouring lanes
+  for (int o = n >> 1; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// Sums of v over every group of the workgroup's columns, in a fixed order:
+// each channel over the threads that hold it, then each group over its
+// channels.  Result in l.gs[group - g0].
+template <int T>
+__device__ __forceinline__ void group_sum(const float v[8], const GnTile &t, const GnLds<T> &l,
+                                          int D) {
+  if (t.active) {
+    float *p = l.buf + threadIdx.x * 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = v[j];
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < 8 * t.cb; c += T) {
+    float s = 0.0f;
+    for (int r = 0; r < t.rs; ++r) s += l.buf[r * 8 * t.cb + c];
+    l.chan[c] = s;
+  }
+  __syncthreads();
+  const int n = threads_per_group<T>(t.ng);
+  for (int g = threadIdx.x / n; g < t.ng; g += T / n) {
+    const int lo = max((t.g0 + g) * D, t.c0) - t.c0, hi = min((t.g0 + g + 1) * D, t.c1) - t.c0;
+    float s = 0.0f;
+    for (int c = lo + (int)threadIdx.x % n; c < hi; c += n) s += l.chan[c];
+    s = part_sum(s, n);
+    if (threadIdx.x % n == 0) l.gs[g] = s;
+  }
+  __syncthreads();
+}
+
+// This thread's per-channel normalisation t = (z - mu) a + b, with the
+// group's mean (l.gs) and 1/sqrt(var + eps) (l.gr), the weight and the
+// sample's modulation folded into a and b.
+struct GnAffine {
+  float mu[8], a[8], b[8];
+};
+
+template <int T, bool TAIL>
+__device__ __forceinline__ GnAffine gn_affine(const GroupNormProblem &a, const GnTile &t,
+                                              const GnLds<T> &l, int64_t sample) {
+  GnAffine f;
+  float m[8], s[8];
+  load8f<TAIL>(a.gamma ? a.gamma + t.c : nullptr, t.nv, 1.0f, m);
+  load8f<TAIL>(a.beta ? a.beta + t.c : nullptr, t.nv, 0.0f, f.b);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int g = min((t.c + j) / a.D - t.g0, t.ng - 1);
+    f.mu[j] = l.gs[g];
+    f.a[j] = l.gr[g] * m[j];
+  }
+  if (a.scale) {
+    unpack8(load8<TAIL>(a.scale + sample * a.ld_mod + t.c, t.nv), m);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f.a[j] = __builtin_fmaf(f.a[j], m[j], f.a[j]);
+      f.b[j] = __builtin_fmaf(f.b[j], m[j], f.b[j]);
+    }
+  }
+  if (a.shift) {
+    unpack8(load8<TAIL>(a.shift + sample * a.ld_mod + t.c, t.nv), s);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.b[j] += s[j];
+  }
+  return f;
+}
+
+template <int ACT>
+__device__ __forceinline__ v4u gn_apply8(v4u z, const GnAffine &f) {
+  float v[8];
+  unpack8(z, v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = __builtin_fmaf(v[j] - f.mu[j], f.a[j], f.b[j]);
+    if (ACT == 1) v[j] = silu_hw(v[j]);
+    if (ACT == 2) v[j] = gelu_f32(v[j]);
+  }
+  return pack8(v);
+}
+
+// A group's whole slice of a sample in one workgroup's registers (U pieces
+// per thread): one launch, one read, one write.
+template <int T, int U, int ACT, bool TAIL>
+__global__ __launch_bounds__(T) void groupnorm_one_kernel(GroupNormProblem a) {
+  extern __shared__ float smem[];
+  const int64_t sample = blockIdx.y;
+  const int c0 = blockIdx.x * a.groups_per_block * a.D;
+  const GnTile t = gn_tile<T, TAIL>(a, c0, min(c0 + a.groups_per_block * a.D, a.C));
+  const GnLds<T> l(smem, t.cb);
+  const int64_t row0 = sample * a.P;
+  v4u z[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int p = t.rsub + u * t.rs;
+    z[u] = v4u{0u, 0u, 0u, 0u};
+    if (t.active && p < a.P) z[u] = load8<TAIL>(a.z + (row0 + p) * a.ld_z + t.c, t.nv);
+  }
+  float s[8], f[8], mu[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = 0.0f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    unpack8(z[u], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] += f[j];
+  }
+  const float inv_n = 1.0f / ((float)a.P * (float)a.D);
+  group_sum<T>(s, t, l, a.D);
+  int g[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    g[j] = min((t.c + j) / a.D - t.g0, t.ng - 1);
+    mu[j] = l.gs[g[j]] * inv_n;
+    s[j] = 0.0f;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const bool in = t.active && t.rsub + u * t.rs < a.P;
+    unpack8(z[u], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float d = in && j < t.nv ? f[j] - mu[j] : 0.0f;
+      s[j] = __builtin_fmaf(d, d, s[j]);
+    }
+  }
+  __syncthreads();  // every thread has read its means
+  group_sum<T>(s, t, l, a.D);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = l.gs[g[j]];
+  __syncthreads();
+  if (t.active) {  // the group's threads write equal values
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j < t.nv) {
+        l.gs[g[j]] = mu[j];
+        l.gr[g[j]] = 1.0f / sqrtf(s[j] * inv_n + a.eps);
+      }
+    }
+  }
+  __syncthreads();
+  if (!t.active) return;
+  const GnAffine af = gn_affine<T, TAIL>(a, t, l, sample);
+  float ip = 0.0f, in = 0.0f;
+  if (a.out.q) seg_scales(a.out, t.c, ip, in);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int p = t.rsub + u * t.rs;
+    if (p < a.P) emit8<TAIL>(a.out, row0 + p, t.c, t.nv, gn_apply8<ACT>(z[u], af), ip, in);
+  }
+}
+
+// Pieces of one workgroup's statistics: rows of block i of a sample, and the
+// channels of group g in its columns.
+__device__ __forceinline__ int gn_rows(const GroupNormProblem &a, int blk) {
+  return (int)min((int64_t)a.rows_per_block, a.P - (int64_t)blk * a.rows_per_block);
+}
+
+__device__ __forceinline__ int gn_chans(const GroupNormProblem &a, int g, int colblk) {
+  const int lo = max(g * a.D, colblk * a.cols_per_block);
+  const int hi = min((g + 1) * a.D, min((colblk + 1) * a.cols_per_block, a.C));
+  return max(0, hi - lo);
+}
+
+// Launch 1 of 2: mean and squared deviations of every group over one block of
+// rows (and columns), to a.part[sample][row block][column block][group].
+// Eight rows at a time per thread: their mean from registers, then their
+// deviations from it, joined to the running pair (Chan, Golub, LeVeque 1979).
+template <int T, bool TAIL>
+__global__ __launch_bounds__(T) void groupnorm_stats_kernel(GroupNormProblem a) {
+  constexpr int U = 8;
+  extern __shared__ float smem[];
+  const int blk = blockIdx.x, colblk = blockIdx.y;
+  const int64_t sample = blockIdx.z;
+  const int c0 = colblk * a.cols_per_block;
+  const GnTile t = gn_tile<T, TAIL>(a, c0, min(c0 + a.cols_per_block, a.C));
+  const GnLds<T> l(smem, t.cb);
+  const int64_t p0 = (int64_t)blk * a.rows_per_block;
+  const int rows = gn_rows(a, blk);
+  const uint16_t *z = a.z + (sample * a.P + p0) * a.ld_z + t.c;
+  float mean[8], m2[8], cnt = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) mean[j] = m2[j] = 0.0f;
+  if (t.active) {
+    for (int p = t.rsub; p < rows; p += U * t.rs) {
+      const int nb = min(U, (rows - p + t.rs - 1) / t.rs);  // rows of this batch
+      v4u v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        v[u] = load8<TAIL>(z + (int64_t)(p + min(u, nb - 1) * t.rs) * a.ld_z, t.nv);
+      const float n = (float)nb, inv = 1.0f / n, w = n / (cnt + n);
+      float s[8], f[8], q[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = q[j] = 0.0f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        unpack8(v[u], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += u < nb ? f[j] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] *= inv;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        unpack8(v[u], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float d = u < nb ? f[j] - s[j] : 0.0f;
+          q[j] = __builtin_fmaf(d, d, q[j]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = s[j] - mean[j];
+        mean[j] = __builtin_fmaf(d, w, mean[j]);
+        m2[j] += __builtin_fmaf(d * d, cnt * w, q[j]);
+      }
+      cnt += n;
+    }
+  }
+  // the channels past C hold zeros: they count nowhere
+  float s[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = j < t.nv ? cnt * mean[j] : 0.0f;
+  group_sum<T>(s, t, l, a.D);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int g = min((t.c + j) / a.D - t.g0, t.ng - 1);
+    const float mu = l.gs[g] / (float)(rows * (float)gn_chans(a, t.g0 + g, colblk));
+    const float d = mean[j] - mu;
+    s[j] = j < t.nv ? __builtin_fmaf(d * d, cnt, m2[j]) : 0.0f;
+  }
+  __syncthreads();
+  for (int g = threadIdx.x; g < t.ng; g += T) l.gr[g] = l.gs[g];
+  __syncthreads();
+  group_sum<T>(s, t, l, a.D);
+  float *part = a.part + 2 * ((sample * a.n_row_blocks + blk) * gridDim.y + colblk) * a.G;
+  for (int g = threadIdx.x; g < t.ng; g += T) {
+    part[2 * (t.g0 + g)] = l.gr[g] / (float)(rows * (float)gn_chans(a, t.g0 + g, colblk));
+    part[2 * (t.g0 + g) + 1] = l.gs[g];
+  }
+}
+
+// Launch 2 of 2: join the blocks' statistics, normalise, activate, store.
+// The blocks are joined around the first one's mean p: with n_i values of
+// mean m_i, S1 = sum n_i (m_i - p) and S2 = sum M2_i + n_i (m_i - p)^2 give
+// mean p + S1/N and variance S2/N - (S1/N)^2.  The first block is part of the
+// whole, so (mean - p)^2 <= (N/n_0) variance and the subtraction loses at
+// most log2 (N/n_0) <= 10 bits of fp32.
+template <int T, int ACT, bool TAIL>
+__global__ __launch_bounds__(T) void groupnorm_apply_kernel(GroupNormProblem a) {
+  constexpr int U = 4;
+  extern __shared__ float smem[];
+  const int blk = blockIdx.x, colblk = blockIdx.y, ncb = gridDim.y;
+  const int64_t sample = blockIdx.z;
+  const int c0 = colblk * a.cols_per_block;
+  const GnTile t = gn_tile<T, TAIL>(a, c0, min(c0 + a.cols_per_block, a.C));
+  const GnLds<T> l(smem, t.cb);
+  const float2 *part =
+      reinterpret_cast<const float2 *>(a.part) + sample * a.n_row_blocks * ncb * a.G;
+  const float inv_n = 1.0f / ((float)a.P * (float)a.D);
+  const int n = threads_per_group<T>(t.ng);
+  for (int i = threadIdx.x / n; i < t.ng; i += T / n) {
+    const int g = t.g0 + i;
+    const float pivot = part[(int64_t)(g * a.D / a.cols_per_block) * a.G + g].x;
+    float s1 = 0.0f, s2 = 0.0f;
+    for (int e = threadIdx.x % n; e < a.n_row_blocks * ncb; e += n) {
+      const float cnt = (float)gn_rows(a, e / ncb) * (float)gn_chans(a, g, e % ncb);
+      const float2 v = part[(int64_t)e * a.G + g];
+      const float d = cnt > 0.0f ? v.x - pivot : 0.0f;
+      s1 = __builtin_fmaf(cnt, d, s1);
+      s2 += cnt > 0.0f ? __builtin_fmaf(cnt * d, d, v.y) : 0.0f;
+    }
+    s1 = part_sum(s1, n) * inv_n;
+    s2 = part_sum(s2, n) * inv_n;
+    if (threadIdx.x % n == 0) {
+      l.gs[i] = pivot + s1;
+      l.gr[i] = 1.0f / sqrtf(fmaxf(s2 - s1 * s1, 0.0f) + a.eps);
+    }
+  }
+  __syncthreads();
+  if (!t.active) return;
+  const GnAffine af = gn_affine<T, TAIL>(a, t, l, sample);
+  float ip = 0.0f, in = 0.0f;
+  if (a.out.q) seg_scales(a.out, t.c, ip, in);
+  const int64_t p0 = sample * a.P + (int64_t)blk * a.rows_per_block;
+  const int rows = gn_rows(a, blk);
+  for (int p = t.rsub; p < rows; p += U * t.rs) {
+    v4u z[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      z[u] = load8<TAIL>(a.z + (p0 + min(p + u * t.rs, rows - 1)) * a.ld_z + t.c, t.nv);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (p + u * t.rs < rows)
+        emit8<TAIL>(a.out, p0 + p + u * t.rs, t.c, t.nv, gn_apply8<ACT>(z[u], af), ip, in);
+  }
+}
+
+}  // namespace
+
+// ------------------------------------------------------------- launches ----
+namespace {
+
+template <int TPR, int NCH>
+void launch_adanorm_n(const AdaNormProblem &a, hipStream_t s) {
+  const int64_t per = a.rows_per * (256 / TPR);
+  const dim3 grid((unsigned)((a.M + per - 1) / per));
+  if (a.K % 8)
+    hipLaunchKernelGGL((adanorm_kernel<TPR, NCH, true>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((adanorm_kernel<TPR, NCH, false>), grid, dim3(256), 0, s, a);
+}
+
+template <int TPR>
+void launch_adanorm_t(const AdaNormProblem &a, hipStream_t s) {
+  switch (((a.K + 7) / 8 + TPR - 1) / TPR) {
+    case 1: return launch_adanorm_n<TPR, 1>(a, s);
+    case 2: return launch_adanorm_n<TPR, 2>(a, s);
+    case 3: return launch_adanorm_n<TPR, 3>(a, s);
+    case 4: return launch_adanorm_n<TPR, 4>(a, s);
+    case 5: return launch_adanorm_n<TPR, 5>(a, s);
+    case 6: return launch_adanorm_n<TPR, 6>(a, s);
+    case 7: return launch_adanorm_n<TPR, 7>(a, s);
+    default: return launch_adanorm_n<TPR, 8>(a, s);
+  }
+}
+
+}  // namespace
+
+// A wave per row up to 4096 columns (8 pieces per lane), a workgroup per row
+// up to 16384; a workgroup too where the rows alone would leave most of the
+// 256 CUs without work.
+hipError_t launch_adanorm(const AdaNormProblem &p, hipStream_t s) {
+  AdaNormProblem a = p;
+  const int64_t chunks = (a.K + 7) / 8;
+  // rows per row group: 8192 waves where that is at most 16 rows; beyond, a
+  // grid of at most 2^20 workgroups
+  a.rows_per = (a.M + (1 << 20) - 1) >> 20;
+  if (a.M > 256 && chunks <= 64 * 8) {
+    const int64_t rows = (a.M + 8191) / 8192;
+    if (a.rows_per < rows) a.rows_per = rows < 16 ? rows : 16;
+    launch_adanorm_t<64>(a, s);
+  } else if (chunks <= 256 * 8) {
+    launch_adanorm_t<256>(a, s);
+  } else {
+    hipLaunchKernelGGL(adanorm_long_kernel, dim3((unsigned)(a.M < 65536 ? a.M : 65536)), dim3(256),
+                       0, s, a);
+  }
+  return hipGetLastError();
+}
+
+namespace {
+
+constexpr int kGnT = 512;       // threads of a group-norm workgroup
+constexpr int kGnOneMaxU = 16;  // pieces per thread that stay in registers
+
+// Smallest count of neighbouring groups whose channels start on a 16-byte
+// column wherever the block stands.
+int gn_groups_per_block(int G, int D) {
+  int g = 1;
+  while (g < G && (g * D) % 8) ++g;
+  return g < G ? g : G;
+}
+
+// Pieces per thread of the one-launch kernel, or 0 where a group block does
+// not fit its registers.
+int gn_one_pieces(const GroupNormProblem &a, int gpb) {
+  const int64_t cb = ((int64_t)gpb * a.D + 7) / 8;
+  if (cb > kGnT) return 0;
+  const int64_t rs = kGnT / cb;
+  const int64_t u = (a.P + rs - 1) / rs;
+  return u <= kGnOneMaxU ? (int)u : 0;
+}
+
+void gn_plan(GroupNormProblem &a) {
+  a.groups_per_block = gn_groups_per_block(a.G, a.D);
+  if (gn_one_pieces(a, a.groups_per_block)) {
+    a.n_row_blocks = 0;
+    return;
+  }
+  const int64_t chunks = ((int64_t)a.C + 7) / 8, ncb = (chunks + kGnT - 1) / kGnT;
+  a.cols_per_block = (int)(8 * ((chunks + ncb - 1) / ncb));
+  // about 512 workgroups in all, at least one full batch of rows for each
+  const int64_t rs = kGnT / (a.cols_per_block / 8);
+  int64_t want = 512 / (a.B * ncb);
+  if (want < 1) want = 1;
+  int64_t rows = (a.P + want - 1) / want;
+  if (rows < 4 * rs) rows = 4 * rs;
+  a.rows_per_block = (int)(rows < (1 << 20) ? rows : 1 << 20);
+  a.n_row_blocks = (int)((a.P + a.rows_per_block - 1) / a.rows_per_block);
+}
+
+}  // namespace
+
+size_t groupnorm_workspace_bytes(const GroupNormProblem &p) {
+  GroupNormProblem a = p;
+  gn_plan(a);
+  if (!a.n_row_blocks) return 0;
+  const int64_t ncb = (a.C + a.cols_per_block - 1) / a.cols_per_block;
+  return sizeof(float) * 2 * (size_t)a.B * (size_t)a.n_row_blocks * (size_t)ncb * (size_t)a.G;
+}
+
+template <int ACT, bool TAIL>
+static void launch_groupnorm_act(const GroupNormProblem &a, hipStream_t s) {
+  if (!a.n_row_blocks) {
+    const int gpb = a.groups_per_block, u = gn_one_pieces(a, gpb);
+    const dim3 grid((unsigned)((a.G + gpb - 1) / gpb), (unsigned)a.B);
+    const size_t lds = gn_lds_bytes(kGnT, (gpb * a.D + 7) / 8);
+#define SQ_GN_ONE(U) \
+  hipLaunchKernelGGL((groupnorm_one_kernel<kGnT, U, ACT, TAIL>), grid, dim3(kGnT), lds, s, a)
+    if (u <= 1) SQ_GN_ONE(1);
+    else if (u <= 2) SQ_GN_ONE(2);
+    else if (u <= 4) SQ_GN_ONE(4);
+    else if (u <= 8) SQ_GN_ONE(8);
+    else SQ_GN_ONE(16);
+#undef SQ_GN_ONE
+    return;
+  }
+  const unsigned ncb = (unsigned)((a.C + a.cols_per_block - 1) / a.cols_per_block);
+  const dim3 grid((unsigned)a.n_row_blocks, ncb, (unsigned)a.B);
+  const size_t lds = gn_lds_bytes(kGnT, a.cols_per_block / 8);
+  hipLaunchKernelGGL((groupnorm_stats_kernel<kGnT, TAIL>), grid, dim3(kGnT), lds, s, a);
+  hipLaunchKernelGGL((groupnorm_apply_kernel<kGnT, ACT, TAIL>), grid, dim3(kGnT), lds, s, a);
+}
+
+hipError_t launch_groupnorm(const GroupNormProblem &p, hipStream_t s) {
+  GroupNormProblem a = p;
+  gn_plan(a);
+  const bool tail = a.C % 8 != 0;
+#define SQ_GN(ACT) tail ? launch_groupnorm_act<ACT, true>(a, s) : launch_groupnorm_act<ACT, false>(a, s)
+  if (a.act == 1) SQ_GN(1);
+  else if (a.act == 2) SQ_GN(2);
+  else SQ_GN(0);
+#undef SQ_GN
+  return hipGetLastError();
+}
+
+}  // namespace sq

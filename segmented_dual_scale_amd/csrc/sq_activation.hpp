@@ -1,0 +1,73 @@
+// sq_activation.hpp -- the SiLU and GELU whose outputs the layer quantises
+// [P1 DualScale motivation; P2 section 3], shared by the kernels that produce
+// the layer's input (act_kernels.hip, norm_kernels.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+namespace sq {
+
+// GELU in its exact form z/2 (1 + erf(z / sqrt 2)), evaluated as
+// z/2 erfc(-z / sqrt 2): the same function, but 1 + erf cancels to nothing in
+// fp32 for z below about -4 while erfc keeps its relative precision.
+// erfc(x), x = |z| / sqrt 2 >= 0, in the form of Numerical Recipes (Press et
+// al., "Numerical Recipes in C", 2nd ed., section 6.2): t exp(-x^2 + P(t)),
+// t = 1 / (1 + x/2), P a degree-9 Chebyshev fit, relative error below 1.2e-7
+// for every x >= 0.  Branch free: erfc(-x) = 2 - erfc(x) gives z >= 0.
+// Rounding x itself would cost about 2 x^2 ulps in the tail, so x enters
+// only t; -x^2 = -z^2/2 is carried as an exact pair (one product and its FMA
+// error), and its product with log2 e is split so that exp2 of the large
+// part sees none of the small part's rounding.  With one-ulp reciprocal and
+// exp2 the result is within 2^-20 of the true value, relative, over the
+// whole bf16 input range (swept on the CPU with those errors injected).
+// Large parts below -120 are evaluated 64 binades up and scaled back
+// exactly, so results in the subnormal range are not flushed.
+__device__ __forceinline__ float gelu_f32(float z) {
+  const float kLog2e = 1.44269504f;             // log2 e, rounded to fp32
+  const float kLog2eLo = 1.92596303e-08f;       // log2 e - kLog2e
+  const float a = fminf(fabsf(z), 20.0f);  // erfc(20 / sqrt 2) underflows: the same result
+  const float x = a * 0.70710678f;
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, x, 1.0f));
+  float P = __builtin_fmaf(t, 0.17087277f, -0.82215223f);
+  P = __builtin_fmaf(t, P, 1.48851587f);
+  P = __builtin_fmaf(t, P, -1.13520398f);
+  P = __builtin_fmaf(t, P, 0.27886807f);
+  P = __builtin_fmaf(t, P, -0.18628806f);
+  P = __builtin_fmaf(t, P, 0.09678418f);
+  P = __builtin_fmaf(t, P, 0.37409196f);
+  P = __builtin_fmaf(t, P, 1.00002368f);
+  P = __builtin_fmaf(t, P, -1.26551223f);
+  const float p = a * a, e = __builtin_fmaf(a, a, -p);  // z^2 = p + e exactly
+  const float q = -0.5f * p, qe = -0.5f * e;           // -x^2 = q + qe exactly
+  const float hi = q * kLog2e;
+  float lo = __builtin_fmaf(q, kLog2e, -hi);
+  lo = __builtin_fmaf(q, kLog2eLo, lo);
+  lo = __builtin_fmaf(qe + P, kLog2e, lo);
+  const bool deep = hi < -120.0f;
+  const float eh = __builtin_amdgcn_exp2f(deep ? hi + 64.0f : hi) * (deep ? 0x1p-64f : 1.0f);
+  const float E = t * eh * __builtin_amdgcn_exp2f(lo);
+  return 0.5f * z * (z < 0.0f ? E : 2.0f - E);
+}
+
+// SiLU z / (1 + e^-z) as z sigmoid(z), the sigmoid from e^-|z| (library
+// expf): e^-z itself overflows for z below about -88.7, where z / (1 + e^-z)
+// would give 0 while the true value is still a normal float.
+__device__ __forceinline__ float silu_f32(float z) {
+  const float ez = expf(-fabsf(z));
+  const float r = 1.0f / (1.0f + ez);
+  return z * (z >= 0.0f ? r : ez * r);
+}
+
+// SiLU for a kernel that also normalises: e^-|z| and the reciprocal from the
+// hardware's one-ulp instructions, since the library expf and an IEEE divide
+// would make that kernel compute-bound.  Rounding the product |z| log2 e
+// costs 0.7 |z| 2^-24 of e^-|z|, so the result is within 2^-18 of the true
+// value, relative, down to z = -60 (and 2^-17 to -87, where it leaves the
+// normal range): bf16 rounds at 2^-9.
+__device__ __forceinline__ float silu_hw(float z) {
+  const float ez = __builtin_amdgcn_exp2f(fabsf(z) * -1.44269504f);
+  const float r = __builtin_amdgcn_rcpf(1.0f + ez);
+  return z * (z >= 0.0f ? r : ez * r);
+}
+
+}  // namespace sq

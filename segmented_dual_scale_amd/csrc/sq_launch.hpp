@@ -72,6 +72,83 @@ hipError_t launch_gemm_smallm(const GemmProblem &p, hipStream_t s);
 // the large-M kernel with both operands staged through LDS
 hipError_t launch_gemm_lds(const GemmProblem &p, hipStream_t s);
 
+// Where a producer of the layer's input puts it: bf16 x, int8 codes q, or
+// both.
+struct NormOut {
+  uint16_t *x;
+  int64_t ld_x;
+  int8_t *q;
+  int64_t ld_q;
+  int64_t plane_stride;  // elements between the + and - planes (0: signed)
+  const float *act;      // [4][n_kseg]
+  SegTable ks;
+};
+
+struct GroupNormProblem {
+  const uint16_t *z;  // [B * P][ld_z]
+  int64_t B, P, ld_z;
+  int32_t C, G, D;  // channels, groups, channels per group
+  float eps;
+  const float *gamma, *beta;       // [C], optional
+  const uint16_t *scale, *shift;   // [B][ld_mod], optional
+  int64_t ld_mod;
+  int32_t act;  // 0 none, 1 SiLU, 2 GELU
+  NormOut out;
+  float *part;  // workspace of the two-launch form
+  // launch shape, filled in by the launch
+  int32_t groups_per_block, rows_per_block, n_row_blocks, cols_per_block;
+};
+
+hipError_t launch_groupnorm(const GroupNormProblem &p, hipStream_t s);
+// Bytes of `part` the launch needs (B, P, C, G and D of the problem decide).
+size_t groupnorm_workspace_bytes(const GroupNormProblem &p);
+
+struct AdaNormProblem {
+  const uint16_t *h;
+  int64_t M, K, ld_h;
+  const uint16_t *branch, *gate;  // optional: h' = h + gate * branch
+  int64_t ld_b;
+  uint16_t *h_out;
+  int64_t ld_ho;
+  float eps;
+  const float *gamma, *beta;      // [K], optional
+  const uint16_t *scale, *shift;  // [n_req][ld_mod], as gate; optional
+  int64_t ld_mod;
+  const int32_t *row_offset;  // device [n_req + 1], or null: equal requests
+  int32_t n_req;
+  int64_t rows_per_req;
+  NormOut out;
+  int64_t rows_per;  // rows a row group walks, filled in by the launch
+};
+
+hipError_t launch_adanorm(const AdaNormProblem &p, hipStream_t s);
+
+struct AdapterProblem {
+  int64_t M, N, K;
+  const uint16_t *x;
+  int64_t ld_x;
+  const int32_t *row_offset;  // device [n_req + 1]
+  const int32_t *adapter;     // device [n_req]
+  int32_t n_req, n_adapters, rank;
+  const int32_t *rank_of;  // device [n_adapters], optional
+  const uint16_t *a;       // [n_adapters][ns.n * rank][K]
+  const uint16_t *b;       // [n_adapters][N][rank]
+  const float *alpha;      // device [n_adapters], optional
+  NSegTable ns;
+  const uint16_t *base;  // optional; may be y
+  int64_t ld_base;
+  uint16_t *y;
+  int64_t ld_y;
+  float *t;  // workspace [splits][M][ns.n * rank]
+  // launch shape, filled in by the launch
+  int32_t splits;
+  int64_t k_per_split;
+};
+
+hipError_t launch_adapter(const AdapterProblem &p, hipStream_t s);
+// Bytes of `t` (M, K, n_req, rank and ns.n of the problem decide).
+size_t adapter_workspace_bytes(const AdapterProblem &p);
+
 constexpr int kSmallMMax = 16;
 
 // Whether the streaming small-M kernel takes this shape (and so reads
