@@ -191,7 +191,7 @@ int segquant_activate_quantize(const uint16_t *z_bf16, int64_t M, int64_t K, int
  *   x  = bf16_rne(act(t)); codes of x exactly as segquant_quantize_dualscale
  *   z_bf16      device bf16 [B * P][ld_z]
  *   groups      1 .. C, a divisor of C (groups = C: instance norm)
- *   eps         > 0
+ *   eps         at least 2^-126
  *   gamma, beta device fp32 [C], each optional (NULL: 1 and 0)
  *   scale, shift  device bf16 [B][ld_mod], each optional (NULL: 0): two chunks
  *               of a conditioning layer's output as they are, ld_mod its

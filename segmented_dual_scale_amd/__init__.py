@@ -412,6 +412,7 @@ def segquant_gemm_w8a8_seg_noalloc(x, w_packed, w_scale, act_scales, out,
 
 
 # ------------------------------------- norms before and adapters beside ----
+# These run in microseconds, so the checks look at each operand once.
 @functools.lru_cache(maxsize=256)
 def _seg_arrays(widths: Optional[Tuple[int, ...]], total: int):
     off, wid = _segs(widths, total)
@@ -419,17 +420,24 @@ def _seg_arrays(widths: Optional[Tuple[int, ...]], total: int):
 
 
 def _segments(widths, total: int):
-    return _seg_arrays(None if widths is None else tuple(int(w) for w in widths), total)
+    return _seg_arrays(None if widths is None else tuple(widths), total)
 
 
 def _want(t, name: str, dtype, shape, device):
-    """Check an operand and return its address (0 for None)."""
+    """Check an operand (None: not given) and return its address."""
     if t is None:
-        return 0
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
-        raise ValueError(f"{name} must be {dtype} of shape {shape} on {device}, "
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
+
+
+def _want_array(t, name: str, dtype, shape, device):
+    """_want for an operand without a leading dimension of its own."""
+    if t is not None and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _want(t, name, dtype, shape, device)
 
 
 def _row_ld(t, name: str) -> int:
@@ -437,28 +445,19 @@ def _row_ld(t, name: str) -> int:
     spaced (any value fits a single row)."""
     if t is None:
         return 0
-    K = t.shape[-1]
-    if t.numel() and t.stride(-1) != 1 and K > 1:
+    shape, stride = t.shape, t.stride()
+    K = shape[-1]
+    if stride[-1] != 1 and K > 1 and t.numel():
         raise ValueError(f"{name} must have unit stride in its last dimension")
-    ld = None
-    for d in range(t.dim() - 2, -1, -1):
-        if t.shape[d] == 1:
-            continue
-        below = 1
-        for e in range(d + 1, t.dim() - 1):
-            below *= t.shape[e]
-        if ld is None:
-            if t.stride(d) % below:
+    ld, below = None, 1  # rows inside one step of dimension d
+    for d in range(len(shape) - 2, -1, -1):
+        if shape[d] != 1:
+            if ld is None:
+                ld = stride[d]
+            elif stride[d] != ld * below and t.numel():
                 raise ValueError(f"{name}: its rows are not evenly spaced")
-            ld = t.stride(d) // below
-        elif t.stride(d) != ld * below:
-            raise ValueError(f"{name}: its rows are not evenly spaced")
+            below *= shape[d]
     return -(-K // 8) * 8 if ld is None else ld
-
-
-def _contiguous(t, name: str):
-    if t is not None and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
 
 
 def _on(device, fn, *args):
@@ -472,39 +471,51 @@ def _on(device, fn, *args):
         return fn(*args, torch.cuda.current_stream(device).cuda_stream)
 
 
-def _workspace(workspace, nbytes: int, device):
+def _workspace(workspace, size, sizes, device):
+    """A workspace argument ("auto": size(*sizes) bytes from torch's
+    allocator) -> the tensor to keep, its address and bytes."""
     import torch
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be a tensor, None or 'auto'")
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+        nbytes = size(*sizes)
+        if not nbytes:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), nbytes
     if workspace is None:
-        return None, 0, 0
-    if workspace.device != device:
-        raise ValueError(f"workspace must be on {device}")
-    _contiguous(workspace, "workspace")
+        return None, None, 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _codes_out(out, wanted: bool, M: int, K: int, layout: int, device, fill: bool):
-    """The int8 output tensor (or None), its address and leading dimension."""
+def _codes_out(out, M: int, K: int, layout: int, device, new):
+    """The int8 output tensor, its address and leading dimension."""
     import torch
-    if not wanted:
-        return None, 0, 0
     if out is None:
         ldq = (K + 15) // 16 * 16
-        shape = (M, ldq) if layout == SEGQ_Q_SIGNED else (2, M, ldq)
-        out = (torch.zeros if fill else torch.empty)(shape, dtype=torch.int8, device=device)
+        out = new((M, ldq) if layout == SEGQ_Q_SIGNED else (2, M, ldq), dtype=torch.int8,
+                  device=device)
     planes = layout != SEGQ_Q_SIGNED
     if (out.dtype != torch.int8 or out.device != device or out.dim() != (3 if planes else 2) or
             out.shape[-2] != M or out.shape[-1] < K or (planes and out.shape[0] != 2)):
         raise ValueError(f"out must be an int8 tensor of {'2 planes of ' if planes else ''}{M} rows "
                          f"of at least {K} codes on {device}, got {out.dtype} {tuple(out.shape)} on "
                          f"{out.device}")
-    ld = _row_ld(out[0] if planes else out, "out") if M > 1 else (out.shape[-1] + 15) // 16 * 16
+    if M > 1:
+        ld = _row_ld(out[0] if planes else out, "out")
+    else:
+        ld = out.stride(0) if planes else (out.shape[-1] + 15) // 16 * 16
     if planes and out.stride(0) != M * ld:
         raise ValueError("out: the second plane must follow the first")
     return out, out.data_ptr(), ld
+
+
+@functools.lru_cache(maxsize=1024)
+def _sizes_of(name: str, *sizes: int) -> int:
+    """A workspace size; it depends on the sizes alone."""
+    return int(getattr(load_library(), name)(*sizes))
 
 
 def segquant_groupnorm_workspace_bytes(B: int, P: int, C: int, groups: int) -> int:
@@ -522,34 +533,37 @@ def segquant_groupnorm_quantize(z, groups: int, eps: float = 1e-5, gamma=None, b
     Returns (codes or None, x or None): codes [B*P][C] as
     segquant_quantize_dualscale (when act_scales is given and want_codes), x
     the bf16 [B][P][C] result if a tensor is passed (or x_out=True to allocate
-    one)."""
+    one).  workspace: a device tensor, None, or "auto" (from torch's allocator
+    when the library asks for one)."""
     import torch
     fn = load_library().segquant_groupnorm_quantize
-    if z.dim() != 3 or z.dtype != torch.bfloat16:
+    bf, f32 = torch.bfloat16, torch.float32
+    if z.dim() != 3 or z.dtype is not bf:
         raise ValueError(f"z must be bfloat16 [B][P][C], got {z.dtype} {tuple(z.shape)}")
-    (B, P, C), dev = z.shape, z.device
+    shape, dev = z.shape, z.device
+    B, P, C = shape
     if x_out is True:
-        x_out = torch.empty((B, P, -(-C // 8) * 8), dtype=torch.bfloat16, device=dev)[:, :, :C]
+        x_out = torch.empty((B, P, -(-C // 8) * 8), dtype=bf, device=dev)[:, :, :C]
     n, off, wid, _ = _segments(kseg, C)
-    act = _want(act_scales, "act_scales", torch.float32, (4, n), dev)
-    _contiguous(act_scales, "act_scales")
-    out, q, ld_q = _codes_out(out, want_codes and act_scales is not None, B * P, C, layout, dev,
-                              False)
-    for t, name in ((gamma, "gamma"), (beta, "beta")):
-        _contiguous(t, name)
+    act = q = None
+    ld_q = 0
+    if act_scales is not None and want_codes:
+        act = _want_array(act_scales, "act_scales", f32, (4, n), dev)
+        out, q, ld_q = _codes_out(out, B * P, C, layout, dev, torch.empty)
+    else:
+        out = None
+    mod = scale if scale is not None else shift
     if scale is not None and shift is not None and B > 1 and scale.stride(0) != shift.stride(0):
         raise ValueError("scale and shift must have the same row stride")
-    mod = scale if scale is not None else shift
-    workspace, ws, ws_bytes = _workspace(workspace, segquant_groupnorm_workspace_bytes(
-        B, P, C, groups) if isinstance(workspace, str) else 0, dev)
+    workspace, ws, ws_bytes = _workspace(
+        workspace, _sizes_of, ("segquant_groupnorm_workspace_bytes", B, P, C, groups), dev)
     _check(_on(dev, fn, z.data_ptr(), B, P, C, _row_ld(z, "z"), groups, eps,
-               _want(gamma, "gamma", torch.float32, (C,), dev),
-               _want(beta, "beta", torch.float32, (C,), dev),
-               _want(scale, "scale", torch.bfloat16, (B, C), dev),
-               _want(shift, "shift", torch.bfloat16, (B, C), dev), _row_ld(mod, "scale or shift"),
-               act_kind, n, off, wid, act, q, ld_q, layout,
-               _want(x_out, "x_out", torch.bfloat16, (B, P, C), dev), _row_ld(x_out, "x_out"),
-               ws, ws_bytes), "segquant_groupnorm_quantize")
+               _want_array(gamma, "gamma", f32, (C,), dev),
+               _want_array(beta, "beta", f32, (C,), dev),
+               _want(scale, "scale", bf, (B, C), dev), _want(shift, "shift", bf, (B, C), dev),
+               _row_ld(mod, "scale or shift"), act_kind, n, off, wid, act, q, ld_q, layout,
+               _want(x_out, "x_out", bf, shape, dev), _row_ld(x_out, "x_out"), ws, ws_bytes),
+           "segquant_groupnorm_quantize")
     return out, x_out
 
 
@@ -570,39 +584,44 @@ def segquant_adanorm_quantize(h, eps: float = 1e-6, gamma=None, beta=None, scale
     a tensor allocated here."""
     import torch
     fn = load_library().segquant_adanorm_quantize
-    if h.dim() != 2 or h.dtype != torch.bfloat16:
+    bf, f32 = torch.bfloat16, torch.float32
+    if h.dim() != 2 or h.dtype is not bf:
         raise ValueError(f"h must be bfloat16 [M][K], got {h.dtype} {tuple(h.shape)}")
-    (M, K), dev, bf = h.shape, h.device, torch.bfloat16
-    mods = [t for t in (scale, shift, gate) if t is not None]
+    shape, dev = h.shape, h.device
+    M, K = shape
+    mod = scale if scale is not None else shift if shift is not None else gate
     if row_offset is not None:
         n_req = row_offset.numel() - 1
     elif n_req is None:
-        n_req = mods[0].shape[0] if mods else 1
-    fill = row_offset is not None
-    new = torch.zeros if fill else torch.empty
+        n_req = mod.shape[0] if mod is not None else 1
+    new = torch.empty if row_offset is None else torch.zeros
     if x_out is True:
         x_out = new((M, -(-K // 8) * 8), dtype=bf, device=dev)[:, :K]
     if h_out is True:
         h_out = new((M, -(-K // 8) * 8), dtype=bf, device=dev)[:, :K]
     n, off, wid, _ = _segments(kseg, K)
-    act = _want(act_scales, "act_scales", torch.float32, (4, n), dev)
-    out, q, ld_q = _codes_out(out, want_codes and act_scales is not None, M, K, layout, dev, fill)
-    for t, name in ((gamma, "gamma"), (beta, "beta"), (row_offset, "row_offset"),
-                    (act_scales, "act_scales")):
-        _contiguous(t, name)
-    if n_req > 1 and any(t.stride(0) != mods[0].stride(0) for t in mods):
-        raise ValueError("scale, shift and gate must have the same row stride")
-    _check(_on(dev, fn, h.data_ptr(), M, K, _row_ld(h, "h"),
-               _want(branch, "branch", bf, (M, K), dev), _row_ld(branch, "branch"),
-               _want(gate, "gate", bf, (n_req, K), dev), _want(h_out, "h_out", bf, (M, K), dev),
-               _row_ld(h_out, "h_out"), eps, _want(gamma, "gamma", torch.float32, (K,), dev),
-               _want(beta, "beta", torch.float32, (K,), dev),
-               _want(scale, "scale", bf, (n_req, K), dev),
-               _want(shift, "shift", bf, (n_req, K), dev),
-               _row_ld(mods[0], "scale, shift or gate") if mods else 0, n_req,
-               _want(row_offset, "row_offset", torch.int32, (n_req + 1,), dev), n, off, wid, act,
-               q, ld_q, layout, _want(x_out, "x_out", bf, (M, K), dev), _row_ld(x_out, "x_out")),
-           "segquant_adanorm_quantize")
+    act = q = None
+    ld_q = 0
+    if act_scales is not None and want_codes:
+        act = _want_array(act_scales, "act_scales", f32, (4, n), dev)
+        out, q, ld_q = _codes_out(out, M, K, layout, dev, new)
+    else:
+        out = None
+    if n_req > 1:
+        for t in (scale, shift, gate):
+            if t is not None and t.stride(0) != mod.stride(0):
+                raise ValueError("scale, shift and gate must have the same row stride")
+    params = (n_req, K)
+    _check(_on(dev, fn, h.data_ptr(), M, K, _row_ld(h, "h"), _want(branch, "branch", bf, shape, dev),
+               _row_ld(branch, "branch"), _want(gate, "gate", bf, params, dev),
+               _want(h_out, "h_out", bf, shape, dev), _row_ld(h_out, "h_out"), eps,
+               _want_array(gamma, "gamma", f32, (K,), dev),
+               _want_array(beta, "beta", f32, (K,), dev),
+               _want(scale, "scale", bf, params, dev), _want(shift, "shift", bf, params, dev),
+               _row_ld(mod, "scale, shift or gate"), n_req,
+               _want_array(row_offset, "row_offset", torch.int32, (n_req + 1,), dev), n, off, wid,
+               act, q, ld_q, layout, _want(x_out, "x_out", bf, shape, dev),
+               _row_ld(x_out, "x_out")), "segquant_adanorm_quantize")
     return out, x_out, h_out
 
 
@@ -623,29 +642,30 @@ def segquant_adapter_add(x, a, b, adapter, row_offset, base=None, alpha=None, ra
     [n_adapters]; rank: int32 [n_adapters], the true ranks; nseg: the layer's
     N-segments.  Everything but nseg is on the device.  Returns bf16 y [M][N];
     out may be base.  Rows of no request are left as they are, zeros in a
-    tensor allocated here."""
+    tensor allocated here.  workspace: a device tensor, or "auto" (from
+    torch's allocator)."""
     import torch
     fn = load_library().segquant_adapter_add
-    bf, dev = torch.bfloat16, x.device
-    if x.dim() != 2 or x.dtype != bf or a.dim() != 3 or b.dim() != 3:
+    bf, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, x.device
+    if x.dim() != 2 or x.dtype is not bf or a.dim() != 3 or b.dim() != 3:
         raise ValueError("x must be bfloat16 [M][K], a and b 3-D")
-    (M, K), (n_adapters, N, r), n_req = x.shape, b.shape, adapter.numel()
+    M, K = x.shape
+    n_adapters, N, r = b.shape
+    n_req = adapter.numel()
     n, off, wid, _ = _segments(nseg, N)
+    y_shape = (M, N)
     if out is None:
-        out = torch.zeros((M, N), dtype=bf, device=dev)
-    for t, name in ((a, "a"), (b, "b"), (adapter, "adapter"), (row_offset, "row_offset"),
-                    (alpha, "alpha"), (rank, "rank")):
-        _contiguous(t, name)
-    workspace, ws, ws_bytes = _workspace(workspace, segquant_adapter_workspace_bytes(
-        M, N, K, n_req, r, n) if isinstance(workspace, str) else 0, dev)
+        out = torch.zeros(y_shape, dtype=bf, device=dev)
+    workspace, ws, ws_bytes = _workspace(
+        workspace, _sizes_of, ("segquant_adapter_workspace_bytes", M, N, K, n_req, r, n), dev)
     _check(_on(dev, fn, M, N, K, x.data_ptr(), _row_ld(x, "x"), n_req,
-               _want(row_offset, "row_offset", torch.int32, (n_req + 1,), dev),
-               _want(adapter, "adapter", torch.int32, (n_req,), dev), n_adapters, r,
-               _want(rank, "rank", torch.int32, (n_adapters,), dev),
-               _want(a, "a", bf, (n_adapters, n * r, K), dev),
-               _want(b, "b", bf, (n_adapters, N, r), dev),
-               _want(alpha, "alpha", torch.float32, (n_adapters,), dev), n, off, wid,
-               _want(base, "base", bf, (M, N), dev), _row_ld(base, "base"),
-               _want(out, "out", bf, (M, N), dev), _row_ld(out, "out"), ws, ws_bytes),
+               _want_array(row_offset, "row_offset", i32, (n_req + 1,), dev),
+               _want_array(adapter, "adapter", i32, (n_req,), dev), n_adapters, r,
+               _want_array(rank, "rank", i32, (n_adapters,), dev),
+               _want_array(a, "a", bf, (n_adapters, n * r, K), dev),
+               _want_array(b, "b", bf, (n_adapters, N, r), dev),
+               _want_array(alpha, "alpha", f32, (n_adapters,), dev), n, off, wid,
+               _want(base, "base", bf, y_shape, dev), _row_ld(base, "base"),
+               _want(out, "out", bf, y_shape, dev), _row_ld(out, "out"), ws, ws_bytes),
            "segquant_adapter_add")
     return out

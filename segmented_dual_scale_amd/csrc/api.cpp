@@ -367,7 +367,8 @@ static int check_rows(const uint16_t *p, int64_t ld, int64_t len, const char *wh
 }
 
 static int check_norm_params(const float *gamma, const float *beta, float eps) {
-  if (!(eps > 0.0f) || eps > 3.0e38f) return fail(SEGQ_ERR_SHAPE, "eps must be positive and finite");
+  if (!(eps >= 1.17549435e-38f) || eps > 3.0e38f)
+    return fail(SEGQ_ERR_SHAPE, "eps must be positive, finite and at least 2^-126");
   if (!aligned16(gamma) || !aligned16(beta))
     return fail(SEGQ_ERR_ALIGN, "gamma or beta is not 16-byte aligned");
   return SEGQ_OK;

@@ -35,7 +35,7 @@ __device__ __forceinline__ void unpack8(v4u v, float f[8]) {
 __device__ __forceinline__ v4u pack8(const float f[8]) {
   v4u v;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+  for (int j = 0; j < 4; ++j) v[j] = cvt_bf16x2(f[2 * j], f[2 * j + 1]);
   return v;
 }
 
@@ -116,11 +116,23 @@ __device__ __forceinline__ void emit8(const NormOut &o, int64_t row, int64_t k, 
   }
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+// Sum over n neighbouring lanes (a power of two up to 64), in each of them.
+// Within 16 lanes by data-parallel moves: once the lanes of a quad (of half a
+// row) agree, mirroring the half row (the row) pairs a lane with the other.
+__device__ __forceinline__ float part_sum(float v, int n) {
+#define SQ_DPP(ctrl) \
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xf, 0xf, false))
+  if (n > 1) SQ_DPP(0xB1);   // quad_perm [1,0,3,2]
+  if (n > 2) SQ_DPP(0x4E);   // quad_perm [2,3,0,1]
+  if (n > 4) SQ_DPP(0x141);  // row_half_mirror
+  if (n > 8) SQ_DPP(0x140);  // row_mirror
+#undef SQ_DPP
+  if (n > 16) v += __shfl_xor(v, 16, 64);
+  if (n > 32) v += __shfl_xor(v, 32, 64);
   return v;
 }
+
+__device__ __forceinline__ float wave_sum(float v) { return part_sum(v, 64); }
 
 // ------------------------------------------------- modulated layer norm --
 // One row per TPR threads (a wave, or a workgroup of four), NCH 16-byte
@@ -228,7 +240,7 @@ __global__ __launch_bounds__(256) void adanorm_kernel(AdaNormProblem a) {
         s2 = __builtin_fmaf(d, d, s2);
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<TPR>(s2, lds) * inv_k + a.eps);
+    const float rstd = __builtin_amdgcn_rsqf(row_sum<TPR>(s2, lds) * inv_k + a.eps);
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       if (c == NCH - 1 && n_last == 0) continue;
@@ -299,7 +311,7 @@ __global__ __launch_bounds__(256) void adanorm_long_kernel(AdaNormProblem a) {
         s2 = __builtin_fmaf(d, d, s2);
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<256>(s2, lds) / (float)a.K + a.eps);
+    const float rstd = __builtin_amdgcn_rsqf(row_sum<256>(s2, lds) / (float)a.K + a.eps);
     for (int64_t k = 8 * (int64_t)threadIdx.x; k < a.K; k += 8 * 256) {
       const int n = (int)min((int64_t)8, a.K - k);
       float m[8], b[8], ip = 0.0f, in = 0.0f;
@@ -344,90 +356,123 @@ __device__ __forceinline__ GnTile gn_tile(const GroupNormProblem &a, int c0, int
   t.c0 = c0;
   t.c1 = c1;
   t.cb = (c1 - c0 + 7) / 8;
-  t.rs = T / t.cb;
-  t.col = threadIdx.x % t.cb;
-  t.rsub = threadIdx.x / t.cb;
+  t.rs = div24(T, t.cb);
+  t.rsub = div24(threadIdx.x, t.cb);
+  t.col = threadIdx.x - t.rsub * t.cb;
   t.active = t.rsub < t.rs;
-  t.g0 = c0 / a.D;
-  t.ng = (c1 - 1) / a.D - t.g0 + 1;
+  t.g0 = div24(c0, a.D);
+  t.ng = div24(c1 - 1, a.D) - t.g0 + 1;
   t.c = c0 + 8 * t.col;
   t.nv = TAIL ? min(8, c1 - t.c) : 8;
   return t;
 }
 
-// LDS of a workgroup: T*8 thread values, then 8 cb channel sums, then two
-// values per group (at most 8 cb groups).
+// How the threads of a workgroup share out the groups of its columns: n
+// neighbouring threads (a power of two) per group, as many as there are, so
+// each looks at about eight of the workgroup's 8T per-channel values.
 template <int T>
-struct GnLds {
-  float *buf, *chan, *gs, *gr;
-  __device__ GnLds(float *base, int cb)
-      : buf(base), chan(base + T * 8), gs(chan + 8 * cb), gr(gs + 8 * cb) {}
+struct GroupShare {
+  int n, log2n;  // threads per group
+  int first;     // this thread's place among them
+  int step;      // groups handled at a time
+  __device__ explicit GroupShare(int ng) {
+    log2n = 0;
+    while ((ng << (log2n + 1)) <= T) ++log2n;
+    n = 1 << log2n;
+    first = threadIdx.x & (n - 1);
+    step = T >> log2n;
+  }
+  // Sum over the n threads, in each of them.  Above a wave (then there is one
+  // step) every thread of the workgroup has to call it.
+  __device__ __forceinline__ float total(float v, float *waves) const {
+    if (n <= 64) return part_sum(v, n);
+    v = part_sum(v, 64);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
+    const int w0 = (threadIdx.x & ~(n - 1)) >> 6;
+    for (int w = 0; w < n / 64; ++w) v += waves[w0 + w];
+    return v;
+  }
 };
 
-size_t gn_lds_bytes(int T, int cb) { return sizeof(float) * ((size_t)T * 8 + 24 * (size_t)cb); }
-
-// Threads that share one group in a group-wise step: a power of two up to a
-// wave, as many as still cover all groups in one step.
-template <int T>
-__device__ __forceinline__ int threads_per_group(int ng) {
-  int n = 1;
-  while (n < 64 && 2 * n * ng <= T) n *= 2;
-  return n;
+// Calls f(row step, LDS index) for this thread's share of a group's values,
+// which stand at row step r and channel c of [rs][8 cb].
+template <int T, class F>
+__device__ __forceinline__ void each_value(const GnTile &t, const GroupShare<T> &sh, int g, int D,
+                                           F f) {
+  const int lo = max((t.g0 + g) * D, t.c0) - t.c0;
+  const int d = min((t.g0 + g + 1) * D, t.c1) - t.c0 - lo;
+  const int dr = div24(sh.n, d), dc = sh.n - dr * d;
+  int r = div24(sh.first, d), c = sh.first - r * d;
+  while (r < t.rs) {
+    f(r, r * 8 * t.cb + lo + c);
+    r += dr;
+    c += dc;
+    if (c >= d) {
+      c -= d;
+      ++r;
+    }
+  }
 }
 
-__device__ __forceinline__ float part_sum(float v, int n) {  // over n neighbouring lanes
-  for (int o = n >> 1; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-
-// Sums of v over every group of the workgroup's columns, in a fixed order:
-// each channel over the threads that hold it, then each group over its
-// channels.  Result in l.gs[group - g0].
-template <int T>
-__device__ __forceinline__ void group_sum(const float v[8], const GnTile &t, const GnLds<T> &l,
-                                          int D) {
-  if (t.active) {
-    float *p = l.buf + threadIdx.x * 8;
+// Group (less t.g0) of each of this thread's 8 channels; past the last
+// channel, the last group.
+__device__ __forceinline__ void gn_groups(const GnTile &t, int D, int g[8]) {
+  int at = div24(t.c, D), left = (at + 1) * D - t.c;
+  at -= t.g0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) p[j] = v[j];
+  for (int j = 0; j < 8; ++j) {
+    g[j] = min(at, t.ng - 1);
+    if (--left == 0) {
+      ++at;
+      left = D;
+    }
+  }
+}
+
+// Sums of v over every group of the workgroup's columns, in a fixed order, to
+// gs[group - g0].  buf: 8T floats, waves: T/64.
+template <int T>
+__device__ __forceinline__ void group_sum(const float v[8], const GnTile &t, float *buf,
+                                          float *waves, float *gs, int D) {
+  if (t.active) {
+    v4f *p = reinterpret_cast<v4f *>(buf + threadIdx.x * 8);
+    p[0] = v4f{v[0], v[1], v[2], v[3]};
+    p[1] = v4f{v[4], v[5], v[6], v[7]};
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < 8 * t.cb; c += T) {
+  const GroupShare<T> sh(t.ng);
+  for (int g0 = 0; g0 < t.ng; g0 += sh.step) {
+    const int g = g0 + (threadIdx.x >> sh.log2n);
     float s = 0.0f;
-    for (int r = 0; r < t.rs; ++r) s += l.buf[r * 8 * t.cb + c];
-    l.chan[c] = s;
-  }
-  __syncthreads();
-  const int n = threads_per_group<T>(t.ng);
-  for (int g = threadIdx.x / n; g < t.ng; g += T / n) {
-    const int lo = max((t.g0 + g) * D, t.c0) - t.c0, hi = min((t.g0 + g + 1) * D, t.c1) - t.c0;
-    float s = 0.0f;
-    for (int c = lo + (int)threadIdx.x % n; c < hi; c += n) s += l.chan[c];
-    s = part_sum(s, n);
-    if (threadIdx.x % n == 0) l.gs[g] = s;
+    if (g < t.ng) each_value<T>(t, sh, g, D, [&](int, int at) { s += buf[at]; });
+    s = sh.total(s, waves);
+    if (g < t.ng && sh.first == 0) gs[g] = s;
   }
   __syncthreads();
 }
 
-// This thread's per-channel normalisation t = (z - mu) a + b, with the
-// group's mean (l.gs) and 1/sqrt(var + eps) (l.gr), the weight and the
-// sample's modulation folded into a and b.
+// This thread's per-channel normalisation t = (z - mu) a + b from its
+// groups' means and 1/sqrt(var + eps), the weight and the sample's modulation
+// folded into a and b.
 struct GnAffine {
   float mu[8], a[8], b[8];
 };
 
-template <int T, bool TAIL>
+template <bool TAIL>
 __device__ __forceinline__ GnAffine gn_affine(const GroupNormProblem &a, const GnTile &t,
-                                              const GnLds<T> &l, int64_t sample) {
+                                              const float mu[8], const float rstd[8],
+                                              int64_t sample) {
   GnAffine f;
   float m[8], s[8];
   load8f<TAIL>(a.gamma ? a.gamma + t.c : nullptr, t.nv, 1.0f, m);
   load8f<TAIL>(a.beta ? a.beta + t.c : nullptr, t.nv, 0.0f, f.b);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int g = min((t.c + j) / a.D - t.g0, t.ng - 1);
-    f.mu[j] = l.gs[g];
-    f.a[j] = l.gr[g] * m[j];
+    f.mu[j] = mu[j];
+    f.a[j] = rstd[j] * m[j];
   }
   if (a.scale) {
     unpack8(load8<TAIL>(a.scale + sample * a.ld_mod + t.c, t.nv), m);
@@ -466,7 +511,7 @@ __global__ __launch_bounds__(T) void groupnorm_one_kernel(GroupNormProblem a) {
   const int64_t sample = blockIdx.y;
   const int c0 = blockIdx.x * a.groups_per_block * a.D;
   const GnTile t = gn_tile<T, TAIL>(a, c0, min(c0 + a.groups_per_block * a.D, a.C));
-  const GnLds<T> l(smem, t.cb);
+  float *buf = smem, *waves = buf + 8 * T, *gs = waves + T / 64;
   const int64_t row0 = sample * a.P;
   v4u z[U];
 #pragma unroll
@@ -485,12 +530,12 @@ __global__ __launch_bounds__(T) void groupnorm_one_kernel(GroupNormProblem a) {
     for (int j = 0; j < 8; ++j) s[j] += f[j];
   }
   const float inv_n = 1.0f / ((float)a.P * (float)a.D);
-  group_sum<T>(s, t, l, a.D);
   int g[8];
+  gn_groups(t, a.D, g);
+  group_sum<T>(s, t, buf, waves, gs, a.D);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    g[j] = min((t.c + j) / a.D - t.g0, t.ng - 1);
-    mu[j] = l.gs[g[j]] * inv_n;
+    mu[j] = gs[g[j]] * inv_n;
     s[j] = 0.0f;
   }
 #pragma unroll
@@ -503,23 +548,11 @@ __global__ __launch_bounds__(T) void groupnorm_one_kernel(GroupNormProblem a) {
       s[j] = __builtin_fmaf(d, d, s[j]);
     }
   }
-  __syncthreads();  // every thread has read its means
-  group_sum<T>(s, t, l, a.D);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) s[j] = l.gs[g[j]];
-  __syncthreads();
-  if (t.active) {  // the group's threads write equal values
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j < t.nv) {
-        l.gs[g[j]] = mu[j];
-        l.gr[g[j]] = 1.0f / sqrtf(s[j] * inv_n + a.eps);
-      }
-    }
-  }
-  __syncthreads();
+  group_sum<T>(s, t, buf, waves, gs, a.D);
   if (!t.active) return;
-  const GnAffine af = gn_affine<T, TAIL>(a, t, l, sample);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = __builtin_amdgcn_rsqf(gs[g[j]] * inv_n + a.eps);
+  const GnAffine af = gn_affine<TAIL>(a, t, mu, s, sample);
   float ip = 0.0f, in = 0.0f;
   if (a.out.q) seg_scales(a.out, t.c, ip, in);
 #pragma unroll
@@ -541,10 +574,46 @@ __device__ __forceinline__ int gn_chans(const GroupNormProblem &a, int g, int co
   return max(0, hi - lo);
 }
 
+// nb <= U more values of 8 channels to the running mean and squared
+// deviations of cnt values: their own mean and deviations from registers,
+// then the pairs joined (Chan, Golub, LeVeque 1979).
+template <int U>
+__device__ __forceinline__ void add_rows(const v4u v[U], int nb, float mean[8], float m2[8],
+                                         float &cnt) {
+  const float n = (float)nb, inv = 1.0f / n, w = n / (cnt + n), cw = cnt * w;
+  float s[8], f[8], q[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = q[j] = 0.0f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (u >= nb) break;
+    unpack8(v[u], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] += f[j];
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] *= inv;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (u >= nb) break;
+    unpack8(v[u], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float d = f[j] - s[j];
+      q[j] = __builtin_fmaf(d, d, q[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float d = s[j] - mean[j];
+    mean[j] = __builtin_fmaf(d, w, mean[j]);
+    m2[j] += __builtin_fmaf(d * d, cw, q[j]);
+  }
+  cnt += n;
+}
+
 // Launch 1 of 2: mean and squared deviations of every group over one block of
-// rows (and columns), to a.part[sample][row block][column block][group].
-// Eight rows at a time per thread: their mean from registers, then their
-// deviations from it, joined to the running pair (Chan, Golub, LeVeque 1979).
+// rows (and columns), to a.part[sample][column block][row block][group].
 template <int T, bool TAIL>
 __global__ __launch_bounds__(T) void groupnorm_stats_kernel(GroupNormProblem a) {
   constexpr int U = 8;
@@ -553,7 +622,8 @@ __global__ __launch_bounds__(T) void groupnorm_stats_kernel(GroupNormProblem a) 
   const int64_t sample = blockIdx.z;
   const int c0 = colblk * a.cols_per_block;
   const GnTile t = gn_tile<T, TAIL>(a, c0, min(c0 + a.cols_per_block, a.C));
-  const GnLds<T> l(smem, t.cb);
+  float2 *buf = reinterpret_cast<float2 *>(smem);  // [T][8] mean, squared deviations
+  float *waves = smem + 16 * T, *counts = waves + T / 64;  // [rs]: rows of a row step
   const int64_t p0 = (int64_t)blk * a.rows_per_block;
   const int rows = gn_rows(a, blk);
   const uint16_t *z = a.z + (sample * a.P + p0) * a.ld_z + t.c;
@@ -561,62 +631,49 @@ __global__ __launch_bounds__(T) void groupnorm_stats_kernel(GroupNormProblem a) 
 #pragma unroll
   for (int j = 0; j < 8; ++j) mean[j] = m2[j] = 0.0f;
   if (t.active) {
-    for (int p = t.rsub; p < rows; p += U * t.rs) {
-      const int nb = min(U, (rows - p + t.rs - 1) / t.rs);  // rows of this batch
+    v4u next[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      next[u] = load8<TAIL>(z + min(t.rsub + u * t.rs, rows - 1) * a.ld_z, t.nv);
+    int p = t.rsub;
+    for (; p + (U - 1) * t.rs < rows; p += U * t.rs) {
       v4u v[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        v[u] = load8<TAIL>(z + (int64_t)(p + min(u, nb - 1) * t.rs) * a.ld_z, t.nv);
-      const float n = (float)nb, inv = 1.0f / n, w = n / (cnt + n);
-      float s[8], f[8], q[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] = q[j] = 0.0f;
-#pragma unroll
       for (int u = 0; u < U; ++u) {
-        unpack8(v[u], f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] += u < nb ? f[j] : 0.0f;
+        v[u] = next[u];
+        if (p + U * t.rs < rows)
+          next[u] = load8<TAIL>(z + min(p + (U + u) * t.rs, rows - 1) * a.ld_z, t.nv);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] *= inv;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        unpack8(v[u], f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float d = u < nb ? f[j] - s[j] : 0.0f;
-          q[j] = __builtin_fmaf(d, d, q[j]);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float d = s[j] - mean[j];
-        mean[j] = __builtin_fmaf(d, w, mean[j]);
-        m2[j] += __builtin_fmaf(d * d, cnt * w, q[j]);
-      }
-      cnt += n;
+      add_rows<U>(v, U, mean, m2, cnt);
     }
+    if (p < rows) add_rows<U>(next, (rows - p + t.rs - 1) / t.rs, mean, m2, cnt);
   }
-  // the channels past C hold zeros: they count nowhere
-  float s[8];
+  if (t.active) {
+    v4f *p = reinterpret_cast<v4f *>(buf + threadIdx.x * 8);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) s[j] = j < t.nv ? cnt * mean[j] : 0.0f;
-  group_sum<T>(s, t, l, a.D);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int g = min((t.c + j) / a.D - t.g0, t.ng - 1);
-    const float mu = l.gs[g] / (float)(rows * (float)gn_chans(a, t.g0 + g, colblk));
-    const float d = mean[j] - mu;
-    s[j] = j < t.nv ? __builtin_fmaf(d * d, cnt, m2[j]) : 0.0f;
+    for (int j = 0; j < 4; ++j)
+      p[j] = v4f{mean[2 * j], m2[2 * j], mean[2 * j + 1], m2[2 * j + 1]};
+    if (t.col == 0) counts[t.rsub] = cnt;
   }
   __syncthreads();
-  for (int g = threadIdx.x; g < t.ng; g += T) l.gr[g] = l.gs[g];
-  __syncthreads();
-  group_sum<T>(s, t, l, a.D);
-  float *part = a.part + 2 * ((sample * a.n_row_blocks + blk) * gridDim.y + colblk) * a.G;
-  for (int g = threadIdx.x; g < t.ng; g += T) {
-    part[2 * (t.g0 + g)] = l.gr[g] / (float)(rows * (float)gn_chans(a, t.g0 + g, colblk));
-    part[2 * (t.g0 + g) + 1] = l.gs[g];
+  float2 *part = reinterpret_cast<float2 *>(a.part) +
+                 ((sample * gridDim.y + colblk) * a.n_row_blocks + blk) * a.G + t.g0;
+  const GroupShare<T> sh(t.ng);
+  for (int g0 = 0; g0 < t.ng; g0 += sh.step) {
+    const int g = g0 + (threadIdx.x >> sh.log2n);
+    float s = 0.0f;
+    if (g < t.ng)
+      each_value<T>(t, sh, g, a.D, [&](int r, int at) { s = __builtin_fmaf(counts[r], buf[at].x, s); });
+    const float mu = sh.total(s, waves) / ((float)rows * (float)gn_chans(a, t.g0 + g, colblk));
+    s = 0.0f;
+    if (g < t.ng)
+      each_value<T>(t, sh, g, a.D, [&](int r, int at) {
+        const float2 v = buf[at];
+        const float d = v.x - mu;
+        s += __builtin_fmaf(d * d, counts[r], v.y);
+      });
+    s = sh.total(s, waves);
+    if (g < t.ng && sh.first == 0) part[g] = make_float2(mu, s);
   }
 }
 
@@ -630,49 +687,98 @@ template <int T, int ACT, bool TAIL>
 __global__ __launch_bounds__(T) void groupnorm_apply_kernel(GroupNormProblem a) {
   constexpr int U = 4;
   extern __shared__ float smem[];
-  const int blk = blockIdx.x, colblk = blockIdx.y, ncb = gridDim.y;
+  // part `part` of the rows of statistics block blk, the last parts first:
+  // they were read last and the cache may still hold them
+  const int part_no = a.parts - 1 - (int)(blockIdx.x / a.n_row_blocks);
+  const int blk = blockIdx.x - (a.parts - 1 - part_no) * a.n_row_blocks;
+  const int colblk = blockIdx.y, ncb = gridDim.y;
   const int64_t sample = blockIdx.z;
   const int c0 = colblk * a.cols_per_block;
   const GnTile t = gn_tile<T, TAIL>(a, c0, min(c0 + a.cols_per_block, a.C));
-  const GnLds<T> l(smem, t.cb);
+  const int in_block = part_no * a.rows_per_part;
+  const int rows = min(a.rows_per_part, gn_rows(a, blk) - in_block);
+  if (rows <= 0) return;
+  const int64_t p0 = sample * a.P + (int64_t)blk * a.rows_per_block + in_block;
+  v4u z[U];  // the first rows are on their way while the statistics are joined
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    z[u] = load8<TAIL>(a.z + (p0 + min(t.rsub + u * t.rs, rows - 1)) * a.ld_z + t.c, t.nv);
+
+  const int width = max(T, 8 * t.cb);  // at most as many groups
+  float2 *sums = reinterpret_cast<float2 *>(smem);
+  float *mean = smem + 2 * width, *rstd = mean + width;
   const float2 *part =
-      reinterpret_cast<const float2 *>(a.part) + sample * a.n_row_blocks * ncb * a.G;
+      reinterpret_cast<const float2 *>(a.part) + sample * ncb * a.n_row_blocks * a.G;
   const float inv_n = 1.0f / ((float)a.P * (float)a.D);
-  const int n = threads_per_group<T>(t.ng);
-  for (int i = threadIdx.x / n; i < t.ng; i += T / n) {
-    const int g = t.g0 + i;
-    const float pivot = part[(int64_t)(g * a.D / a.cols_per_block) * a.G + g].x;
+  const int last = a.n_row_blocks - 1;
+  const int slices = max(1, div24(T, t.ng));  // threads that share a group, ng apart
+  for (int i = threadIdx.x; i < slices * t.ng; i += T) {
+    const int slice = div24(i, t.ng), g = i - slice * t.ng + t.g0;
+    int cb0 = 0, cb1 = 0;
+    if (ncb > 1) {
+      cb0 = g * a.D / a.cols_per_block;
+      cb1 = ((g + 1) * a.D - 1) / a.cols_per_block;
+    }
+    const float pivot = part[(int64_t)cb0 * a.n_row_blocks * a.G + g].x;
     float s1 = 0.0f, s2 = 0.0f;
-    for (int e = threadIdx.x % n; e < a.n_row_blocks * ncb; e += n) {
-      const float cnt = (float)gn_rows(a, e / ncb) * (float)gn_chans(a, g, e % ncb);
-      const float2 v = part[(int64_t)e * a.G + g];
-      const float d = cnt > 0.0f ? v.x - pivot : 0.0f;
-      s1 = __builtin_fmaf(cnt, d, s1);
-      s2 += cnt > 0.0f ? __builtin_fmaf(cnt * d, d, v.y) : 0.0f;
+    for (int cb = cb0; cb <= cb1; ++cb) {
+      const float chans = (float)gn_chans(a, g, cb);
+      const float full = chans * (float)a.rows_per_block, rest = chans * (float)gn_rows(a, last);
+      const float2 *q = part + (int64_t)cb * a.n_row_blocks * a.G + g;
+#pragma unroll 8
+      for (int e = slice; e < a.n_row_blocks; e += slices) {
+        const float2 v = q[(int64_t)e * a.G];
+        const float cnt = e < last ? full : rest, d = v.x - pivot;
+        s1 = __builtin_fmaf(cnt, d, s1);
+        s2 += __builtin_fmaf(cnt * d, d, v.y);
+      }
+    }
+    sums[i] = make_float2(s1, s2);
+    if (slice == 0) mean[i] = pivot;
+  }
+  __syncthreads();
+  int log2n = 0;  // now n neighbouring threads per group
+  while (log2n < 6 && (2 << log2n) <= slices) ++log2n;
+  const int n = 1 << log2n, first = threadIdx.x & (n - 1);
+  for (int i = threadIdx.x >> log2n; i < t.ng; i += T >> log2n) {
+    float s1 = 0.0f, s2 = 0.0f;
+    for (int k = first; k < slices; k += n) {
+      const float2 v = sums[k * t.ng + i];
+      s1 += v.x;
+      s2 += v.y;
     }
     s1 = part_sum(s1, n) * inv_n;
     s2 = part_sum(s2, n) * inv_n;
-    if (threadIdx.x % n == 0) {
-      l.gs[i] = pivot + s1;
-      l.gr[i] = 1.0f / sqrtf(fmaxf(s2 - s1 * s1, 0.0f) + a.eps);
+    if (first == 0) {
+      mean[i] += s1;
+      rstd[i] = __builtin_amdgcn_rsqf(fmaxf(s2 - s1 * s1, 0.0f) + a.eps);
     }
   }
   __syncthreads();
   if (!t.active) return;
-  const GnAffine af = gn_affine<T, TAIL>(a, t, l, sample);
+  int g[8];
+  float mu[8], rs[8];
+  gn_groups(t, a.D, g);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    mu[j] = mean[g[j]];
+    rs[j] = rstd[g[j]];
+  }
+  const GnAffine af = gn_affine<TAIL>(a, t, mu, rs, sample);
   float ip = 0.0f, in = 0.0f;
   if (a.out.q) seg_scales(a.out, t.c, ip, in);
-  const int64_t p0 = sample * a.P + (int64_t)blk * a.rows_per_block;
-  const int rows = gn_rows(a, blk);
   for (int p = t.rsub; p < rows; p += U * t.rs) {
-    v4u z[U];
+    v4u now[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      z[u] = load8<TAIL>(a.z + (p0 + min(p + u * t.rs, rows - 1)) * a.ld_z + t.c, t.nv);
+    for (int u = 0; u < U; ++u) {
+      now[u] = z[u];
+      if (p + U * t.rs < rows)
+        z[u] = load8<TAIL>(a.z + (p0 + min(p + (U + u) * t.rs, rows - 1)) * a.ld_z + t.c, t.nv);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (p + u * t.rs < rows)
-        emit8<TAIL>(a.out, p0 + p + u * t.rs, t.c, t.nv, gn_apply8<ACT>(z[u], af), ip, in);
+        emit8<TAIL>(a.out, p0 + p + u * t.rs, t.c, t.nv, gn_apply8<ACT>(now[u], af), ip, in);
   }
 }
 
@@ -731,8 +837,8 @@ hipError_t launch_adanorm(const AdaNormProblem &p, hipStream_t s) {
 
 namespace {
 
-constexpr int kGnT = 512;       // threads of a group-norm workgroup
-constexpr int kGnOneMaxU = 16;  // pieces per thread that stay in registers
+constexpr int kGnStatsT = 512, kGnApplyT = 256;  // threads of the two launches
+constexpr int kGnMaxCols = kGnApplyT;            // 16-byte columns of a workgroup
 
 // Smallest count of neighbouring groups whose channels start on a 16-byte
 // column wherever the block stands.
@@ -742,32 +848,45 @@ int gn_groups_per_block(int G, int D) {
   return g < G ? g : G;
 }
 
-// Pieces per thread of the one-launch kernel, or 0 where a group block does
-// not fit its registers.
-int gn_one_pieces(const GroupNormProblem &a, int gpb) {
+// Threads and pieces per thread of the one-launch kernel; u == 0 where a group
+// block does not fit its registers.
+struct GnOne {
+  int t, u;
+};
+
+GnOne gn_one(const GroupNormProblem &a, int gpb) {
   const int64_t cb = ((int64_t)gpb * a.D + 7) / 8;
-  if (cb > kGnT) return 0;
-  const int64_t rs = kGnT / cb;
-  const int64_t u = (a.P + rs - 1) / rs;
-  return u <= kGnOneMaxU ? (int)u : 0;
+  for (int t = 256; t <= 512; t *= 2) {
+    const int64_t most = t == 256 ? 8 : 16;
+    if (cb > t) continue;
+    const int64_t rs = t / cb, u = (a.P + rs - 1) / rs;
+    if (u <= most) return {t, (int)u};
+  }
+  return {0, 0};
 }
 
 void gn_plan(GroupNormProblem &a) {
   a.groups_per_block = gn_groups_per_block(a.G, a.D);
-  if (gn_one_pieces(a, a.groups_per_block)) {
+  if (gn_one(a, a.groups_per_block).u) {
     a.n_row_blocks = 0;
     return;
   }
-  const int64_t chunks = ((int64_t)a.C + 7) / 8, ncb = (chunks + kGnT - 1) / kGnT;
+  const int64_t chunks = ((int64_t)a.C + 7) / 8, ncb = (chunks + kGnMaxCols - 1) / kGnMaxCols;
   a.cols_per_block = (int)(8 * ((chunks + ncb - 1) / ncb));
-  // about 512 workgroups in all, at least one full batch of rows for each
-  const int64_t rs = kGnT / (a.cols_per_block / 8);
-  int64_t want = 512 / (a.B * ncb);
+  // statistics: about one workgroup per CU (every workgroup of the second
+  // launch reads all blocks of its sample), four rows or more per thread
+  const int64_t rs = kGnStatsT / (a.cols_per_block / 8);
+  int64_t want = 256 / (a.B * ncb);
   if (want < 1) want = 1;
   int64_t rows = (a.P + want - 1) / want;
   if (rows < 4 * rs) rows = 4 * rs;
   a.rows_per_block = (int)(rows < (1 << 20) ? rows : 1 << 20);
   a.n_row_blocks = (int)((a.P + a.rows_per_block - 1) / a.rows_per_block);
+  // apply: 1024 workgroups where that leaves eight rows per thread
+  const int64_t rs2 = kGnApplyT / (a.cols_per_block / 8);
+  a.parts = 4;
+  while (a.parts > 1 && a.rows_per_block < a.parts * 8 * rs2) a.parts /= 2;
+  a.rows_per_part = (a.rows_per_block + a.parts - 1) / a.parts;
 }
 
 }  // namespace
@@ -780,27 +899,32 @@ size_t groupnorm_workspace_bytes(const GroupNormProblem &p) {
   return sizeof(float) * 2 * (size_t)a.B * (size_t)a.n_row_blocks * (size_t)ncb * (size_t)a.G;
 }
 
+template <int T, int U, int ACT, bool TAIL>
+static void launch_groupnorm_one(const GroupNormProblem &a, hipStream_t s) {
+  const int gpb = a.groups_per_block;
+  const dim3 grid((unsigned)((a.G + gpb - 1) / gpb), (unsigned)a.B);
+  const size_t lds = sizeof(float) * (8 * T + T / 64 + 8 * (size_t)((gpb * a.D + 7) / 8));
+  hipLaunchKernelGGL((groupnorm_one_kernel<T, U, ACT, TAIL>), grid, dim3(T), lds, s, a);
+}
+
 template <int ACT, bool TAIL>
 static void launch_groupnorm_act(const GroupNormProblem &a, hipStream_t s) {
   if (!a.n_row_blocks) {
-    const int gpb = a.groups_per_block, u = gn_one_pieces(a, gpb);
-    const dim3 grid((unsigned)((a.G + gpb - 1) / gpb), (unsigned)a.B);
-    const size_t lds = gn_lds_bytes(kGnT, (gpb * a.D + 7) / 8);
-#define SQ_GN_ONE(U) \
-  hipLaunchKernelGGL((groupnorm_one_kernel<kGnT, U, ACT, TAIL>), grid, dim3(kGnT), lds, s, a)
-    if (u <= 1) SQ_GN_ONE(1);
-    else if (u <= 2) SQ_GN_ONE(2);
-    else if (u <= 4) SQ_GN_ONE(4);
-    else if (u <= 8) SQ_GN_ONE(8);
-    else SQ_GN_ONE(16);
-#undef SQ_GN_ONE
-    return;
+    const GnOne o = gn_one(a, a.groups_per_block);
+    if (o.t == 256 && o.u <= 2) return launch_groupnorm_one<256, 2, ACT, TAIL>(a, s);
+    if (o.t == 256 && o.u <= 4) return launch_groupnorm_one<256, 4, ACT, TAIL>(a, s);
+    if (o.t == 256) return launch_groupnorm_one<256, 8, ACT, TAIL>(a, s);
+    if (o.u <= 8) return launch_groupnorm_one<512, 8, ACT, TAIL>(a, s);
+    return launch_groupnorm_one<512, 16, ACT, TAIL>(a, s);
   }
   const unsigned ncb = (unsigned)((a.C + a.cols_per_block - 1) / a.cols_per_block);
-  const dim3 grid((unsigned)a.n_row_blocks, ncb, (unsigned)a.B);
-  const size_t lds = gn_lds_bytes(kGnT, a.cols_per_block / 8);
-  hipLaunchKernelGGL((groupnorm_stats_kernel<kGnT, TAIL>), grid, dim3(kGnT), lds, s, a);
-  hipLaunchKernelGGL((groupnorm_apply_kernel<kGnT, ACT, TAIL>), grid, dim3(kGnT), lds, s, a);
+  const int width = a.cols_per_block > kGnApplyT ? a.cols_per_block : kGnApplyT;
+  hipLaunchKernelGGL((groupnorm_stats_kernel<kGnStatsT, TAIL>),
+                     dim3((unsigned)a.n_row_blocks, ncb, (unsigned)a.B), dim3(kGnStatsT),
+                     sizeof(float) * (17 * kGnStatsT + kGnStatsT / 64), s, a);
+  hipLaunchKernelGGL((groupnorm_apply_kernel<kGnApplyT, ACT, TAIL>),
+                     dim3((unsigned)(a.n_row_blocks * a.parts), ncb, (unsigned)a.B),
+                     dim3(kGnApplyT), sizeof(float) * 4 * width, s, a);
 }
 
 hipError_t launch_groupnorm(const GroupNormProblem &p, hipStream_t s) {

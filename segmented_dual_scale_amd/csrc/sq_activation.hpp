@@ -58,16 +58,15 @@ __device__ __forceinline__ float silu_f32(float z) {
   return z * (z >= 0.0f ? r : ez * r);
 }
 
-// SiLU for a kernel that also normalises: e^-|z| and the reciprocal from the
-// hardware's one-ulp instructions, since the library expf and an IEEE divide
-// would make that kernel compute-bound.  Rounding the product |z| log2 e
-// costs 0.7 |z| 2^-24 of e^-|z|, so the result is within 2^-18 of the true
-// value, relative, down to z = -60 (and 2^-17 to -87, where it leaves the
-// normal range): bf16 rounds at 2^-9.
+// SiLU z / (1 + e^-z) for a kernel that also normalises, from the hardware's
+// one-ulp exp2 and reciprocal: eleven issue slots, where the library expf and
+// an IEEE divide would make that kernel compute-bound.  Rounding the product
+// z log2 e costs 0.7 |z| 2^-24 of e^-z, so the result is within 2^-18 of the
+// true value, relative, down to z = -60 and within 2^-17 to z = -87 (bf16
+// rounds at 2^-8); below -88.7, where e^-z overflows, it is -0 for a true
+// value smaller than 2^-121.
 __device__ __forceinline__ float silu_hw(float z) {
-  const float ez = __builtin_amdgcn_exp2f(fabsf(z) * -1.44269504f);
-  const float r = __builtin_amdgcn_rcpf(1.0f + ez);
-  return z * (z >= 0.0f ? r : ez * r);
+  return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));
 }
 
 }  // namespace sq

@@ -131,6 +131,23 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return f32_to_bf16_rne(lo) | (f32_to_bf16_rne(hi) << 16);
 }
 
+// The same rounding by the hardware's packed conversion (RNE; NaN stays NaN).
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo, hi}), v2bf));
+}
+
+// x / d for 0 <= x < 2^24 and d >= 1, from the reciprocal with a correction:
+// a quarter of the instructions of an integer division.
+__device__ __forceinline__ int div24(int x, int d) {
+  int q = (int)((float)x * __builtin_amdgcn_rcpf((float)d));
+  const int r = x - q * d;
+  q -= r < 0 ? 1 : 0;
+  q += r >= d ? 1 : 0;
+  return q;
+}
+
 // Non-negative floats order like their bit patterns: the reductions below
 // take atomic max over uint32 bits.
 __device__ __forceinline__ float pos_part(float x) { return x > 0.0f ? x : 0.0f; }

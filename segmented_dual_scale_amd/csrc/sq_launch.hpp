@@ -96,7 +96,7 @@ struct GroupNormProblem {
   NormOut out;
   float *part;  // workspace of the two-launch form
   // launch shape, filled in by the launch
-  int32_t groups_per_block, rows_per_block, n_row_blocks, cols_per_block;
+  int32_t groups_per_block, rows_per_block, n_row_blocks, cols_per_block, parts, rows_per_part;
 };
 
 hipError_t launch_groupnorm(const GroupNormProblem &p, hipStream_t s);

@@ -44,6 +44,7 @@ def groupnorm(B=2, Px=4, C=64, z=FAKE, ld_z=None, groups=8, eps=1e-5, gamma=FAKE
     (dict(groups=0), S.SEGQ_ERR_SHAPE),
     (dict(groups=7), S.SEGQ_ERR_SHAPE),
     (dict(eps=0.0), S.SEGQ_ERR_SHAPE),
+    (dict(eps=1e-39), S.SEGQ_ERR_SHAPE),
     (dict(eps=float("nan")), S.SEGQ_ERR_SHAPE),
     (dict(eps=float("inf")), S.SEGQ_ERR_SHAPE),
     (dict(gamma=ODD8), S.SEGQ_ERR_ALIGN),
