@@ -445,8 +445,11 @@ def _row_ld(t, name: str) -> int:
     spaced (any value fits a single row)."""
     if t is None:
         return 0
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     K = shape[-1]
+    if not K & 7 and t.is_contiguous():
+        return K
+    stride = t.stride()
     if stride[-1] != 1 and K > 1 and t.numel():
         raise ValueError(f"{name} must have unit stride in its last dimension")
     ld, below = None, 1  # rows inside one step of dimension d
@@ -465,10 +468,11 @@ def _on(device, fn, *args):
     import torch
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, got {device}")
+    stream = torch._C._cuda_getCurrentRawStream(device.index)  # current_stream() takes 2 us
     if device.index == torch.cuda.current_device():
-        return fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        return fn(*args, stream)
     with torch.cuda.device(device):
-        return fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        return fn(*args, stream)
 
 
 def _workspace(workspace, size, sizes, device):

@@ -54,9 +54,18 @@ __device__ __forceinline__ v4u load8(const uint16_t *p, int n) {
   return v;
 }
 
+// stream: past the caches (see kStreamBytes).
 template <bool TAIL>
-__device__ __forceinline__ void store8(uint16_t *p, v4u v, int n) {
-  if (n >= 8) *reinterpret_cast<v4u *>(p) = v;
+__device__ __forceinline__ void store8(uint16_t *p, v4u v, int n, bool stream) {
+  if (n >= 8) {
+    if (stream) {
+      asm volatile("" ::: "memory");  // between them, or the compiler makes the
+      __builtin_nontemporal_store(v, reinterpret_cast<v4u *>(p));  // two stores one
+      asm volatile("" ::: "memory");
+    } else {
+      *reinterpret_cast<v4u *>(p) = v;
+    }
+  }
   if (!TAIL || n >= 8) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -102,7 +111,7 @@ __device__ __forceinline__ void seg_scales(const NormOut &o, int64_t k, float &i
 template <bool TAIL>
 __device__ __forceinline__ void emit8(const NormOut &o, int64_t row, int64_t k, int n, v4u x,
                                       float ip, float in) {
-  if (o.x) store8<TAIL>(o.x + row * o.ld_x + k, x, n);
+  if (o.x) store8<TAIL>(o.x + row * o.ld_x + k, x, n, o.stream);
   if (o.q) {
     int8_t *q = o.q + row * o.ld_q + k;
     if (o.plane_stride) {
@@ -216,7 +225,8 @@ __global__ __launch_bounds__(256) void adanorm_kernel(AdaNormProblem a) {
         for (int j = 0; j < 8; ++j) f[j] = f[j] + (a.gate ? g[j] * b[j] : b[j]);
         h[c] = pack8(f);  // the norm reads the residual stream as it is stored
         if (a.h_out)
-          store8<TAIL>(a.h_out + r * a.ld_ho + 8 * (t + c * TPR), h[c], SQ_N(c));
+          store8<TAIL>(a.h_out + r * a.ld_ho + 8 * (t + c * TPR), h[c], SQ_N(c),
+                       a.out.stream);
       }
     }
     float s = 0.0f;
@@ -247,18 +257,22 @@ __global__ __launch_bounds__(256) void adanorm_kernel(AdaNormProblem a) {
       const int k = 8 * (t + c * TPR);
       float f[8], m[8], b[8];
       unpack8(h[c], f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = (f[j] - mean) * rstd;
       if (a.gamma || a.beta) {
         load8f<TAIL>(a.gamma ? a.gamma + k : nullptr, SQ_N(c), 1.0f, m);
         load8f<TAIL>(a.beta ? a.beta + k : nullptr, SQ_N(c), 0.0f, b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf(f[j], m[j], b[j]);
-      }
-      unpack8(sc[c], m);
-      unpack8(sh[c], b);
+        for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf((f[j] - mean) * rstd, m[j], b[j]);
+        unpack8(sc[c], m);
+        unpack8(sh[c], b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf(f[j], m[j], f[j]) + b[j];
+        for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf(f[j], m[j], f[j]) + b[j];
+      } else {
+        unpack8(sc[c], m);
+        unpack8(sh[c], b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          f[j] = __builtin_fmaf(f[j] - mean, __builtin_fmaf(m[j], rstd, rstd), b[j]);
+      }
       emit8<TAIL>(a.out, r, k, SQ_N(c), pack8(f), ip[c], in[c]);
     }
   }
@@ -318,7 +332,7 @@ __global__ __launch_bounds__(256) void adanorm_long_kernel(AdaNormProblem a) {
       // each thread reads its piece of h before it writes the same piece of
       // h_out, and no later pass reads either: h_out may be h itself
       const v4u v = piece(k, n, f);
-      if (a.branch && a.h_out) store8<true>(a.h_out + r * a.ld_ho + k, v, n);
+      if (a.branch && a.h_out) store8<true>(a.h_out + r * a.ld_ho + k, v, n, a.out.stream);
       load8f<true>(a.gamma ? a.gamma + k : nullptr, n, 1.0f, m);
       load8f<true>(a.beta ? a.beta + k : nullptr, n, 0.0f, b);
 #pragma unroll
@@ -787,6 +801,14 @@ __global__ __launch_bounds__(T) void groupnorm_apply_kernel(GroupNormProblem a) 
 // ------------------------------------------------------------- launches ----
 namespace {
 
+// Bf16 outputs above this many bytes are stored past the caches: the 256 MB
+// last-level cache could not hold them for their reader, and their lines
+// would be written back during the next pass instead.  Group norm
+// 1024x1024x128 (268 MB out): 50 + 90 us for the two launches, against 73 +
+// 87 us with cached stores, whose write-back the next call's statistics pass
+// then waits for.
+constexpr int64_t kStreamBytes = 128 << 20;
+
 template <int TPR, int NCH>
 void launch_adanorm_n(const AdaNormProblem &a, hipStream_t s) {
   const int64_t per = a.rows_per * (256 / TPR);
@@ -819,6 +841,7 @@ void launch_adanorm_t(const AdaNormProblem &a, hipStream_t s) {
 hipError_t launch_adanorm(const AdaNormProblem &p, hipStream_t s) {
   AdaNormProblem a = p;
   const int64_t chunks = (a.K + 7) / 8;
+  a.out.stream = 2 * a.M * a.K * ((a.out.x != nullptr) + (a.h_out != nullptr)) > kStreamBytes;
   // rows per row group: 8192 waves where that is at most 16 rows; beyond, a
   // grid of at most 2^20 workgroups
   a.rows_per = (a.M + (1 << 20) - 1) >> 20;
@@ -837,8 +860,8 @@ hipError_t launch_adanorm(const AdaNormProblem &p, hipStream_t s) {
 
 namespace {
 
-constexpr int kGnStatsT = 512, kGnApplyT = 256;  // threads of the two launches
-constexpr int kGnMaxCols = kGnApplyT;            // 16-byte columns of a workgroup
+constexpr int kGnT = 512;        // threads of the two launches
+constexpr int kGnMaxCols = 256;  // 16-byte columns of a workgroup
 
 // Smallest count of neighbouring groups whose channels start on a 16-byte
 // column wherever the block stands.
@@ -875,16 +898,16 @@ void gn_plan(GroupNormProblem &a) {
   a.cols_per_block = (int)(8 * ((chunks + ncb - 1) / ncb));
   // statistics: about one workgroup per CU (every workgroup of the second
   // launch reads all blocks of its sample), four rows or more per thread
-  const int64_t rs = kGnStatsT / (a.cols_per_block / 8);
+  const int64_t rs = kGnT / (a.cols_per_block / 8);
   int64_t want = 256 / (a.B * ncb);
   if (want < 1) want = 1;
   int64_t rows = (a.P + want - 1) / want;
   if (rows < 4 * rs) rows = 4 * rs;
   a.rows_per_block = (int)(rows < (1 << 20) ? rows : 1 << 20);
   a.n_row_blocks = (int)((a.P + a.rows_per_block - 1) / a.rows_per_block);
-  // apply: 1024 workgroups where that leaves eight rows per thread
-  const int64_t rs2 = kGnApplyT / (a.cols_per_block / 8);
-  a.parts = 4;
+  // apply: 2048 workgroups where that leaves eight rows per thread
+  const int64_t rs2 = kGnT / (a.cols_per_block / 8);
+  a.parts = 8;
   while (a.parts > 1 && a.rows_per_block < a.parts * 8 * rs2) a.parts /= 2;
   a.rows_per_part = (a.rows_per_block + a.parts - 1) / a.parts;
 }
@@ -918,18 +941,19 @@ static void launch_groupnorm_act(const GroupNormProblem &a, hipStream_t s) {
     return launch_groupnorm_one<512, 16, ACT, TAIL>(a, s);
   }
   const unsigned ncb = (unsigned)((a.C + a.cols_per_block - 1) / a.cols_per_block);
-  const int width = a.cols_per_block > kGnApplyT ? a.cols_per_block : kGnApplyT;
-  hipLaunchKernelGGL((groupnorm_stats_kernel<kGnStatsT, TAIL>),
-                     dim3((unsigned)a.n_row_blocks, ncb, (unsigned)a.B), dim3(kGnStatsT),
-                     sizeof(float) * (17 * kGnStatsT + kGnStatsT / 64), s, a);
-  hipLaunchKernelGGL((groupnorm_apply_kernel<kGnApplyT, ACT, TAIL>),
+  const int width = a.cols_per_block > kGnT ? a.cols_per_block : kGnT;
+  hipLaunchKernelGGL((groupnorm_stats_kernel<kGnT, TAIL>),
+                     dim3((unsigned)a.n_row_blocks, ncb, (unsigned)a.B), dim3(kGnT),
+                     sizeof(float) * (17 * kGnT + kGnT / 64), s, a);
+  hipLaunchKernelGGL((groupnorm_apply_kernel<kGnT, ACT, TAIL>),
                      dim3((unsigned)(a.n_row_blocks * a.parts), ncb, (unsigned)a.B),
-                     dim3(kGnApplyT), sizeof(float) * 4 * width, s, a);
+                     dim3(kGnT), sizeof(float) * 4 * width, s, a);
 }
 
 hipError_t launch_groupnorm(const GroupNormProblem &p, hipStream_t s) {
   GroupNormProblem a = p;
   gn_plan(a);
+  a.out.stream = 2 * a.B * a.P * a.C > kStreamBytes;
   const bool tail = a.C % 8 != 0;
 #define SQ_GN(ACT) tail ? launch_groupnorm_act<ACT, true>(a, s) : launch_groupnorm_act<ACT, false>(a, s)
   if (a.act == 1) SQ_GN(1);

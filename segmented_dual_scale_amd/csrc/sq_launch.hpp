@@ -82,6 +82,7 @@ struct NormOut {
   int64_t plane_stride;  // elements between the + and - planes (0: signed)
   const float *act;      // [4][n_kseg]
   SegTable ks;
+  bool stream;  // store x past the caches, filled in by the launch
 };
 
 struct GroupNormProblem {
@@ -141,7 +142,7 @@ struct AdapterProblem {
   int64_t ld_y;
   float *t;  // workspace [splits][M][ns.n * rank]
   // launch shape, filled in by the launch
-  int32_t splits;
+  int32_t splits, run_tiles;
   int64_t k_per_split;
 };
 
