@@ -108,17 +108,19 @@ __device__ __forceinline__ void wait_copies() {
 }
 
 // ------------------------------------------------------------- shrink ----
-// Grid: (row tile, block of 16 NT factor rows, part of K).  Four waves take
-// every fourth 64-wide piece of K, as two steps of 32, each with its own
-// rotating LDS buffers and no barrier; their sums meet in LDS.  A step is MT +
-// NT copies of 16 rows x 64 bytes: lane l copies chunk (l%4) ^ ((l/16)%4) of
-// row l/4, so operand row r finds chunk g at place g ^ ((r/4)%4) and 16 lanes
-// read 16 different groups of four banks.
-template <int MT, int NT, int NB>
-__global__ __launch_bounds__(256) void adapter_shrink_kernel(AdapterProblem p) {
-  constexpr int kStep = (MT + NT) * 1024;  // bytes of a wave's step
-  constexpr int kSums = 4 * MT * NT * 1024;
-  constexpr int kBytes = 4 * NB * kStep > kSums ? 4 * NB * kStep : kSums;
+// Grid: (row tile, block of 16 NT factor rows, part of K).  WV waves take every
+// WV-th 64-wide step of K, each with its own rotating pair of LDS buffers and
+// no barrier; their sums meet in LDS.  A copy is 8 rows x 128 bytes, whole
+// cache lines: copies of 64 bytes a row asked for each line twice, and the
+// second request waited on the first's (8192x6144, rank 64: 33 against NN us).
+// Lane l copies chunk (l%8) ^ ((row/2)%8) of its row, so operand row r finds
+// chunk c at place c ^ ((r/2)%8) and 16 lanes read 16 different groups of four
+// banks.
+template <int MT, int NT, int WV>
+__global__ __launch_bounds__(64 * WV) void adapter_shrink_kernel(AdapterProblem p) {
+  constexpr int kStep = (MT + NT) * 2048;  // bytes of a wave's step
+  constexpr int kSums = WV * MT * NT * 1024;
+  constexpr int kBytes = 2 * WV * kStep > kSums ? 2 * WV * kStep : kSums;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kBytes];
   const RowTile t = find_tile<16 * MT>(p, blockIdx.x);
   const int a = t.adapter;
@@ -129,25 +131,27 @@ __global__ __launch_bounds__(256) void adapter_shrink_kernel(AdapterProblem p) {
   const int64_t k0 = (int64_t)blockIdx.z * p.k_per_split;
   const int64_t k1 = min(k0 + p.k_per_split, p.K);
   const int pieces = k1 > k0 ? (int)((k1 - k0) / 64) : 0;
-  const int steps = wave < pieces ? 2 * ((pieces - wave + 3) / 4) : 0;
+  const int steps = wave < pieces ? (pieces - wave + WV - 1) / WV : 0;
 
-  const int chunk = 8 * ((lane & 3) ^ ((lane >> 4) & 3));
-  const uint16_t *xp[MT], *ap[NT];
+  const uint16_t *xp[2 * MT], *ap[2 * NT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-    xp[i] = p.x + (t.row0 + min(16 * i + (lane >> 2), t.rows - 1)) * p.ld_x + k0 + 64 * wave + chunk;
+  for (int i = 0; i < 2 * MT; ++i) {
+    const int row = 8 * i + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
+    xp[i] = p.x + (t.row0 + min(row, t.rows - 1)) * p.ld_x + k0 + 64 * wave + 8 * chunk;
+  }
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
-    ap[i] = p.a + ((int64_t)a * rt + min(c0 + 16 * i + (lane >> 2), rt - 1)) * p.K + k0 +
-            64 * wave + chunk;
-  uint8_t *mine = smem + wave * NB * kStep;
+  for (int i = 0; i < 2 * NT; ++i) {
+    const int row = 8 * i + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
+    ap[i] = p.a + ((int64_t)a * rt + min(c0 + row, rt - 1)) * p.K + k0 + 64 * wave + 8 * chunk;
+  }
+  uint8_t *mine = smem + wave * 2 * kStep;
   auto copy = [&](int step) {
-    uint8_t *to = mine + (step % NB) * kStep;
-    const int64_t k = 256 * (int64_t)(step >> 1) + 32 * (step & 1);
+    uint8_t *to = mine + (step & 1) * kStep;
+    const int64_t k = 64 * WV * (int64_t)step;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) copy_lds16(xp[i] + k, to + 1024 * i);
+    for (int i = 0; i < 2 * MT; ++i) copy_lds16(xp[i] + k, to + 1024 * i);
 #pragma unroll
-    for (int j = 0; j < NT; ++j) copy_lds16(ap[j] + k, to + 1024 * (MT + j));
+    for (int j = 0; j < 2 * NT; ++j) copy_lds16(ap[j] + k, to + 1024 * (2 * MT + j));
   };
 
   v4f acc[MT][NT];
@@ -155,28 +159,31 @@ __global__ __launch_bounds__(256) void adapter_shrink_kernel(AdapterProblem p) {
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  // this lane's 16 bytes of an operand block
-  const int at = 64 * (lane & 15) + 16 * ((lane >> 4) ^ ((lane >> 2) & 3));
-#pragma unroll
-  for (int s = 0; s < NB - 1; ++s)
-    if (s < steps) copy(s);
+  // this lane's 16 bytes of an operand block, for either half of the 64
+  const int r = lane & 15, g = lane >> 4, f = (r >> 1) & 7;
+  const int at[2] = {128 * r + 16 * (g ^ f), 128 * r + 16 * ((4 + g) ^ f)};
+  if (steps > 0) copy(0);
   for (int s = 0; s < steps; ++s) {
-    if (s + NB - 1 < steps) {
-      copy(s + NB - 1);
-      wait_copies<(NB - 1) * (MT + NT)>();
+    if (s + 1 < steps) {
+      copy(s + 1);
+      wait_copies<2 * (MT + NT)>();
     } else {
       wait_copies<0>();
     }
-    const uint8_t *from = mine + (s % NB) * kStep + at;
-    v4u x[MT], w[NT];
+    const uint8_t *from = mine + (s & 1) * kStep;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) x[i] = *reinterpret_cast<const v4u *>(from + 1024 * i);
+    for (int h = 0; h < 2; ++h) {
+      v4u x[MT], w[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) w[j] = *reinterpret_cast<const v4u *>(from + 1024 * (MT + j));
+      for (int i = 0; i < MT; ++i) x[i] = *reinterpret_cast<const v4u *>(from + 2048 * i + at[h]);
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+      for (int j = 0; j < NT; ++j)
+        w[j] = *reinterpret_cast<const v4u *>(from + 2048 * (MT + j) + at[h]);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = mfma(w[j], x[i], acc[i][j]);
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = mfma(w[j], x[i], acc[i][j]);
+    }
   }
 
   const float alpha = p.alpha ? p.alpha[a] : 1.0f;
@@ -190,9 +197,11 @@ __global__ __launch_bounds__(256) void adapter_shrink_kernel(AdapterProblem p) {
   __syncthreads();
   // stored row by row: lane l has row l/4, ranks 4 (l%4) .. +3 of a block
   const int from = 16 * (lane & 3) + (lane >> 2);
-  for (int u = wave; u < MT * NT; u += 4) {
+  for (int u = wave; u < MT * NT; u += WV) {
     const int m = 16 * (u / NT) + (lane >> 2), c = c0 + 16 * (u % NT);
-    v4f v = (sums[0][u][from] + sums[1][u][from]) + (sums[2][u][from] + sums[3][u][from]);
+    v4f v = sums[0][u][from];
+#pragma unroll
+    for (int w = 1; w < WV; ++w) v += sums[w][u][from];
     const int q = c - div24(c, p.rank) * p.rank + 4 * (lane & 3);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = q + i < rank ? v[i] * alpha : 0.0f;
@@ -307,16 +316,20 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(AdapterProblem p) {
       // lane l: row l/4, ranks 4 (l%4) .. +3 of the block
       const int m = min(16 * (f / RC) + (lane >> 2), t.rows - 1);
       const int block = (run.seg * p.rank) / 16 + f % RC;
-      v4f u[4];
+      v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int s0 = 0; s0 < p.splits; s0 += 4) {  // the parts of K that the shrink left
+        v4f u[4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {  // the parts of K that the shrink left
-        u[s] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        if (s < p.splits)
-          u[s] = *reinterpret_cast<const v4f *>(t_block(p, s, block) + (t.row0 + m) * 16 +
-                                                4 * (lane & 3));
+        for (int s = 0; s < 4; ++s) {
+          u[s] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+          if (s0 + s < p.splits)
+            u[s] = *reinterpret_cast<const v4f *>(t_block(p, s0 + s, block) + (t.row0 + m) * 16 +
+                                                  4 * (lane & 3));
+        }
+        sum += (u[0] + u[1]) + (u[2] + u[3]);
       }
       v2u hi, lo;
-      split4((u[0] + u[1]) + (u[2] + u[3]), hi, lo);
+      split4(sum, hi, lo);
       // operand lane 16 c + row holds ranks 8c .. +7 (lo: 32 lanes on)
       v2u *to = reinterpret_cast<v2u *>(lds.t[f]) +
                 2 * (16 * ((lane & 3) >> 1) + (lane >> 2)) + (lane & 1);
@@ -500,19 +513,13 @@ AdapterPlan adapter_plan(const AdapterProblem &p) {
     return tile_bound(p, 16 * l.mt) * ((rt + 16 * l.nt - 1) / (16 * l.nt));
   };
   while (few && l.nt > 1 && groups() < 256) l.nt /= 2;
-  // parts of K: the rounds of workgroups that the grid takes times the steps
-  // of one (256 of K, and about two for its start), and a read of t per part
-  const int64_t steps = (p.K + 255) / 256, at_once = l.mt * l.nt == 16 ? 512 : 1024;
-  int64_t best = -1;
-  for (int n = 1; n <= 4; ++n) {
-    const int64_t each = (steps + n - 1) / n;
-    const int64_t cost = (groups() * n + at_once - 1) / at_once * (each + 2) + n;
-    if (best < 0 || cost < best) {
-      best = cost;
-      l.splits = n;
-      l.k_per_split = 256 * each;
-    }
-  }
+  // parts of K: while the workgroups do not fill the chip (two to a CU at the
+  // largest LDS footprint) and each keeps four steps.  8192x6144, rank 64,
+  // 136 tiles: 40, 32, 28, 35, 32 us with 2, 3, 4, 6, 8 parts
+  const int64_t steps = (p.K + 255) / 256;
+  l.splits = 1;
+  while (l.splits < 4 && groups() * l.splits < 512 && steps >= 2 * (l.splits + 1)) ++l.splits;
+  l.k_per_split = 256 * ((steps + l.splits - 1) / l.splits);
   l.expand_mt = few ? 1 : 4;
   return l;
 }
@@ -566,7 +573,8 @@ hipError_t launch_adapter(const AdapterProblem &q, hipStream_t s) {
   const dim3 shrink((unsigned)tile_bound(p, 16 * l.mt),
                     (unsigned)((rt + 16 * l.nt - 1) / (16 * l.nt)), (unsigned)l.splits);
 #define SQ_SHRINK(MT, NT) \
-  hipLaunchKernelGGL((adapter_shrink_kernel<MT, NT, 2>), shrink, dim3(256), 0, s, p)
+  hipLaunchKernelGGL((adapter_shrink_kernel<MT, NT, (MT + NT > 5 ? 2 : 4)>), shrink, \
+                     dim3(MT + NT > 5 ? 128 : 256), 0, s, p)
 #define SQ_SHRINK_NT(MT)            \
   if (l.nt == 1) SQ_SHRINK(MT, 1);  \
   else if (l.nt == 2) SQ_SHRINK(MT, 2); \
