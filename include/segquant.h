@@ -256,7 +256,8 @@ size_t segquant_groupnorm_workspace_bytes(int64_t B, int64_t P, int64_t C, int32
  *               be given if h_out is
  * One launch, no workspace.  Tensor pointers 16-byte aligned (row_offset 4),
  * ld_h, ld_b, ld_ho, ld_xo and ld_mod multiples of 8, ld_q of 16; K needs no
- * alignment.  M may be 0.  Outputs other than h_out must not overlap inputs.
+ * alignment; K-segment boundaries up to 4194240.  M may be 0.  Outputs other
+ * than h_out must not overlap inputs.
  */
 int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int64_t ld_h,
                               const uint16_t *branch, int64_t ld_b, const uint16_t *gate,
@@ -306,7 +307,8 @@ int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
  *               one must be ordered
  * Two launches.  The order of every sum is fixed.  Requires K % 64 == 0,
  * N % 16 == 0, 16-byte aligned tensor pointers (int32 arrays and alpha 4),
- * ld_x, ld_base and ld_y multiples of 8, M <= 2^27.  M may be 0.
+ * ld_x, ld_base and ld_y multiples of 8, M <= 2^27, N <= 1048560,
+ * n_req <= 2^23.  M may be 0.
  */
 int segquant_adapter_add(int64_t M, int64_t N, int64_t K, const uint16_t *x_bf16, int64_t ld_x,
                          int32_t n_req, const int32_t *row_offset, const int32_t *adapter,

@@ -234,11 +234,11 @@ struct ColRun {
   int seg, n0, end;  // first column, end of the run
 };
 
-__device__ __forceinline__ ColRun find_run(const NSegTable &ns, int run, int per_run) {
+__device__ __forceinline__ ColRun find_run(const NSegEnds &ns, int run, int per_run) {
   ColRun c{0, 0, 0};
   const int width = 64 * per_run;
-  for (; c.seg < ns.n; ++c.seg) {
-    const int off = ns.off[c.seg], end = ns.end[c.seg];
+  for (int off = 0, end; c.seg < ns.n; ++c.seg, off = end) {
+    end = 16 * (int)ns.end16[c.seg];
     const int runs = (end - off + width - 1) / width;
     if (run < runs) {
       c.n0 = off + width * run;
@@ -539,8 +539,10 @@ void launch_expand(const AdapterProblem &q, hipStream_t s) {
   const int64_t rows = tile_bound(p, 16 * MT);
   auto runs = [&](int per_run) {
     int64_t n = 0;
-    for (int i = 0; i < p.ns.n; ++i)
-      n += (p.ns.end[i] - p.ns.off[i] + 64 * per_run - 1) / (64 * per_run);
+    for (int i = 0, off = 0, end; i < p.ns.n; ++i, off = end) {
+      end = 16 * (int)p.ns.end16[i];
+      n += (end - off + 64 * per_run - 1) / (64 * per_run);
+    }
     return n;
   };
   if (p.rank > 64) {

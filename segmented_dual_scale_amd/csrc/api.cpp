@@ -351,7 +351,17 @@ static int check_norm_out(int64_t M, int64_t K, int32_t n_kseg, const int32_t *k
   o.ld_q = ld_q;
   o.plane_stride = q_layout == SEGQ_Q_PLANES ? M * ld_q : 0;
   o.act = act_scales;
-  return read_kseg(n_kseg, kseg_offset, kseg_width, K, 0, o.ks);
+  sq::SegTable ks{};
+  const int st = read_kseg(n_kseg, kseg_offset, kseg_width, K, 0, ks);
+  if (st) return st;
+  o.ks.n = ks.n;
+  for (int32_t i = 0; i + 1 < ks.n; ++i) {
+    if (ks.end[i] / 64 > 0xffff)
+      return fail(SEGQ_ERR_UNSUPPORTED, "K-segment boundary %d is beyond %d", ks.end[i],
+                  64 * 0xffff);
+    o.ks.end64[i] = (uint16_t)(ks.end[i] / 64);
+  }
+  return SEGQ_OK;
 }
 
 // An optional bf16 matrix: pointer, leading dimension, row length.
@@ -506,8 +516,9 @@ static int adapter_sizes(int64_t M, int64_t N, int64_t K, int32_t n_req, int32_t
   if (K % 64 || N % 16)
     return fail(SEGQ_ERR_ALIGN, "adapters need K %% 64 == 0 and N %% 16 == 0 (K=%lld N=%lld)",
                 (long long)K, (long long)N);
-  if (M > (1 << 27) || n_req > (1 << 23))
-    return fail(SEGQ_ERR_UNSUPPORTED, "M %lld > 2^27 or n_req %d > 2^23", (long long)M, n_req);
+  if (M > (1 << 27) || n_req > (1 << 23) || N > 16 * 0xffff)
+    return fail(SEGQ_ERR_UNSUPPORTED, "M %lld > 2^27, n_req %d > 2^23 or N %lld > %d", (long long)M,
+                n_req, (long long)N, 16 * 0xffff);
   if (n_req < 1) return fail(SEGQ_ERR_SHAPE, "n_req %d < 1", n_req);
   if (rank < 1 || rank % SEGQ_ADAPTER_RANK_STEP)
     return fail(SEGQ_ERR_ALIGN, "rank %d is not a multiple of %d", rank, SEGQ_ADAPTER_RANK_STEP);
@@ -545,10 +556,13 @@ int segquant_adapter_add(int64_t M, int64_t N, int64_t K, const uint16_t *x_bf16
   if (st) return st;
   if (n_adapters < 1) return fail(SEGQ_ERR_SHAPE, "n_adapters %d < 1", n_adapters);
   if ((st = check_x(x_bf16, M, K, ld_x))) return st;
-  if ((st = read_nseg(n_nseg, nseg_offset, nseg_width, N, p.ns))) return st;
-  for (int32_t i = 0; i < p.ns.n; ++i)
-    if (p.ns.off[i] % 16)
-      return fail(SEGQ_ERR_ALIGN, "N-segment boundary %d is not a multiple of 16", p.ns.off[i]);
+  sq::NSegTable ns{};
+  if ((st = read_nseg(n_nseg, nseg_offset, nseg_width, N, ns))) return st;
+  for (int32_t i = 0; i < ns.n; ++i) {
+    if (ns.off[i] % 16)
+      return fail(SEGQ_ERR_ALIGN, "N-segment boundary %d is not a multiple of 16", ns.off[i]);
+    p.ns.end16[i] = (uint16_t)(ns.end[i] / 16);
+  }
   if (M == 0) return ok();
   if (!row_offset || !adapter || !a || !b || !y_bf16)
     return fail(SEGQ_ERR_NULL, "row_offset, adapter, a, b or y_bf16 is NULL");

@@ -102,7 +102,7 @@ __device__ __forceinline__ void load8f(const float *p, int n, float dflt, float 
 // multiple of 64, so an 8-element piece lies in one segment).
 __device__ __forceinline__ void seg_scales(const NormOut &o, int64_t k, float &ip, float &in) {
   int seg = 0;
-  while (seg + 1 < o.ks.n && k >= o.ks.end[seg]) ++seg;
+  while (seg + 1 < o.ks.n && k >= 64 * (int64_t)o.ks.end64[seg]) ++seg;
   ip = o.act[2 * o.ks.n + seg];
   in = o.act[3 * o.ks.n + seg];
 }
@@ -512,7 +512,7 @@ __device__ __forceinline__ v4u gn_apply8(v4u z, const GnAffine &f) {
   for (int j = 0; j < 8; ++j) {
     v[j] = __builtin_fmaf(v[j] - f.mu[j], f.a[j], f.b[j]);
     if (ACT == 1) v[j] = silu_hw(v[j]);
-    if (ACT == 2) v[j] = gelu_f32(v[j]);
+    if (ACT == 2) v[j] = gelu_hw(v[j]);
   }
   return pack8(v);
 }

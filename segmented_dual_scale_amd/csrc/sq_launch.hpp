@@ -72,6 +72,20 @@ hipError_t launch_gemm_smallm(const GemmProblem &p, hipStream_t s);
 // the large-M kernel with both operands staged through LDS
 hipError_t launch_gemm_lds(const GemmProblem &p, hipStream_t s);
 
+// Segment lists of the calls below, small enough to be cheap as kernel
+// arguments (a launch with 1.2 KB of them costs the host about 1 us more):
+// the ends of the K-segments before the last in steps of 64 columns, of all
+// N-segments in steps of 16.
+struct KSegEnds {
+  int32_t n;
+  uint16_t end64[kMaxKSeg];
+};
+
+struct NSegEnds {
+  int32_t n;
+  uint16_t end16[kMaxNSeg];
+};
+
 // Where a producer of the layer's input puts it: bf16 x, int8 codes q, or
 // both.
 struct NormOut {
@@ -81,7 +95,7 @@ struct NormOut {
   int64_t ld_q;
   int64_t plane_stride;  // elements between the + and - planes (0: signed)
   const float *act;      // [4][n_kseg]
-  SegTable ks;
+  KSegEnds ks;
   bool stream;  // store x past the caches, filled in by the launch
 };
 
@@ -135,7 +149,7 @@ struct AdapterProblem {
   const uint16_t *a;       // [n_adapters][ns.n * rank][K]
   const uint16_t *b;       // [n_adapters][N][rank]
   const float *alpha;      // device [n_adapters], optional
-  NSegTable ns;
+  NSegEnds ns;
   const uint16_t *base;  // optional; may be y
   int64_t ld_base;
   uint16_t *y;

@@ -146,6 +146,7 @@ def adapter(M=8, N=64, K=64, x=FAKE, ld_x=None, n_req=2, row_offset=FAKE, ids=FA
 
 @pytest.mark.parametrize("kw,status", [
     (dict(M=-1), S.SEGQ_ERR_SHAPE),
+    (dict(N=1 << 20, ld_base=1 << 20, ld_y=1 << 20), S.SEGQ_ERR_UNSUPPORTED),
     (dict(K=72, ld_x=72), S.SEGQ_ERR_ALIGN),
     (dict(N=40), S.SEGQ_ERR_ALIGN),
     (dict(M=(1 << 27) + 1), S.SEGQ_ERR_UNSUPPORTED),
