@@ -39,14 +39,15 @@ __device__ __forceinline__ v4u pack8(const float f[8]) {
   return v;
 }
 
-// Up to 8 bf16 at p, 16-byte aligned; the elements from n on read as 0 and
-// are not touched (a row's last piece may end with the allocation).  TAIL:
-// rows end inside a piece; without it n is 8 or 0, and the element-wise code
-// of every access (half of the kernel's registers) is not built.
+// A row's pieces.  TAIL: rows end inside a piece, whose n elements count (the
+// code for it is half of a kernel's registers, so it is built apart); without
+// TAIL n is 8, or 0 for no piece.  Rows stand a multiple of 8 elements apart,
+// so a whole piece may be read in every row but the array's last, which may
+// end with the allocation; what the padding holds is not used.
 template <bool TAIL>
-__device__ __forceinline__ v4u load8(const uint16_t *p, int n) {
+__device__ __forceinline__ v4u load8(const uint16_t *p, int n, bool last_row) {
   v4u v = {0u, 0u, 0u, 0u};
-  if (n >= 8) return *reinterpret_cast<const v4u *>(p);
+  if (n >= 8 || (TAIL && n > 0 && !last_row)) return *reinterpret_cast<const v4u *>(p);
   if (!TAIL) return v;
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -54,6 +55,17 @@ __device__ __forceinline__ v4u load8(const uint16_t *p, int n) {
   return v;
 }
 
+// v with the elements from n on zeroed.
+template <bool TAIL>
+__device__ __forceinline__ v4u keep8(v4u v, int n) {
+  if (TAIL) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = 2 * j + 1 < n ? v[j] : 2 * j < n ? v[j] & 0xffffu : 0u;
+  }
+  return v;
+}
+
+// The padding is not written: a short piece goes out as 4, 2 and 1 elements.
 // stream: past the caches (see kStreamBytes).
 template <bool TAIL>
 __device__ __forceinline__ void store8(uint16_t *p, v4u v, int n, bool stream) {
@@ -67,18 +79,20 @@ __device__ __forceinline__ void store8(uint16_t *p, v4u v, int n, bool stream) {
     }
   }
   if (!TAIL || n >= 8) return;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < n) p[j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+  const uint32_t a = n & 4 ? v[2] : v[0], b = n & 4 ? v[3] : v[1];
+  if (n & 4) *reinterpret_cast<v2u *>(p) = v2u{v[0], v[1]};
+  if (n & 2) *reinterpret_cast<uint32_t *>(p + (n & 4)) = a;
+  if (n & 1) p[n & 6] = (uint16_t)(n & 2 ? b : a);
 }
 
 template <bool TAIL>
 __device__ __forceinline__ void store8(int8_t *p, v2u v, int n) {
   if (n >= 8) *reinterpret_cast<v2u *>(p) = v;
   if (!TAIL || n >= 8) return;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < n) p[j] = (int8_t)(v[j >> 2] >> (8 * (j & 3)));
+  const uint32_t a = n & 4 ? v[1] : v[0];
+  if (n & 4) *reinterpret_cast<uint32_t *>(p) = v[0];
+  if (n & 2) *reinterpret_cast<uint16_t *>(p + (n & 4)) = (uint16_t)a;
+  if (n & 1) p[n & 6] = (int8_t)(n & 2 ? a >> 16 : a);
 }
 
 // 8 fp32 parameters at p (16-byte aligned), dflt where there are none.
@@ -183,8 +197,29 @@ __global__ __launch_bounds__(256) void adanorm_kernel(AdaNormProblem a) {
     if (a.out.q && SQ_N(c) > 0) seg_scales(a.out, 8 * (t + c * TPR), ip[c], in[c]);
   }
   v4u sc[NCH], sh[NCH], ga[NCH];
+  // a row's h and branch are loaded while the row before it is worked on, the
+  // first row's while its request is looked up
+  v4u h[NCH], y[NCH], next_h[NCH], next_y[NCH];
+  auto load_row = [&](int64_t r) {
+    const bool last_row = r == a.M - 1;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      next_h[c] = load8<TAIL>(a.h + r * a.ld_h + 8 * (t + c * TPR), SQ_N(c), last_row);
+      if (a.branch)
+        next_y[c] = load8<TAIL>(a.branch + r * a.ld_b + 8 * (t + c * TPR), SQ_N(c), last_row);
+    }
+  };
+  constexpr bool kAhead = NCH <= 4;  // beyond, the registers cost more waves than this gains
+  if (kAhead && first < last) load_row(first);
   int64_t until = first;  // sc, sh and ga hold for the rows before this one
   for (int64_t r = first; r < last; ++r) {
+    if (!kAhead) load_row(r);
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      h[c] = next_h[c];
+      y[c] = next_y[c];
+    }
+    if (kAhead && r + 1 < last) load_row(r + 1);
     if (r >= until) {
       int64_t req;
       if (a.row_offset) {
@@ -197,24 +232,17 @@ __global__ __launch_bounds__(256) void adanorm_kernel(AdaNormProblem a) {
         req = r / a.rows_per_req;
         until = (req + 1) * a.rows_per_req;
       }
+      const bool last_row = req == a.n_req - 1;
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
         const int64_t at = req * a.ld_mod + 8 * (t + c * TPR);
         sc[c] = sh[c] = ga[c] = v4u{0u, 0u, 0u, 0u};
-        if (a.scale) sc[c] = load8<TAIL>(a.scale + at, SQ_N(c));
-        if (a.shift) sh[c] = load8<TAIL>(a.shift + at, SQ_N(c));
-        if (a.gate) ga[c] = load8<TAIL>(a.gate + at, SQ_N(c));
+        if (a.scale) sc[c] = load8<TAIL>(a.scale + at, SQ_N(c), last_row);
+        if (a.shift) sh[c] = load8<TAIL>(a.shift + at, SQ_N(c), last_row);
+        if (a.gate) ga[c] = load8<TAIL>(a.gate + at, SQ_N(c), last_row);
       }
     }
-    v4u h[NCH];
-    const uint16_t *hr = a.h + r * a.ld_h + 8 * t;
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) h[c] = load8<TAIL>(hr + 8 * c * TPR, SQ_N(c));
     if (a.branch) {
-      v4u y[NCH];
-      const uint16_t *br = a.branch + r * a.ld_b + 8 * t;
-#pragma unroll
-      for (int c = 0; c < NCH; ++c) y[c] = load8<TAIL>(br + 8 * c * TPR, SQ_N(c));
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
         float f[8], g[8], b[8];
@@ -229,6 +257,7 @@ __global__ __launch_bounds__(256) void adanorm_kernel(AdaNormProblem a) {
                        a.out.stream);
       }
     }
+    h[NCH - 1] = keep8<TAIL>(h[NCH - 1], n_last);
     float s = 0.0f;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
@@ -296,16 +325,17 @@ __global__ __launch_bounds__(256) void adanorm_long_kernel(AdaNormProblem a) {
     const uint16_t *ga = a.gate ? a.gate + req * a.ld_mod : nullptr;
     // h' of piece k, recomputed in each pass
     auto piece = [&](int64_t k, int n, float f[8]) -> v4u {
-      v4u v = load8<true>(h + k, n);
+      v4u v = load8<true>(h + k, n, r == a.M - 1);
       if (a.branch) {
         float g[8], b[8];
         unpack8(v, f);
-        unpack8(load8<true>(a.branch + r * a.ld_b + k, n), b);
-        if (ga) unpack8(load8<true>(ga + k, n), g);
+        unpack8(load8<true>(a.branch + r * a.ld_b + k, n, r == a.M - 1), b);
+        if (ga) unpack8(load8<true>(ga + k, n, req == a.n_req - 1), g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = f[j] + (ga ? g[j] * b[j] : b[j]);
         v = pack8(f);
       }
+      v = keep8<true>(v, n);
       unpack8(v, f);
       return v;
     };
@@ -338,8 +368,8 @@ __global__ __launch_bounds__(256) void adanorm_long_kernel(AdaNormProblem a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf((f[j] - mean) * rstd, m[j], b[j]);
       v4u sc = {0u, 0u, 0u, 0u}, sh = sc;
-      if (a.scale) sc = load8<true>(a.scale + req * a.ld_mod + k, n);
-      if (a.shift) sh = load8<true>(a.shift + req * a.ld_mod + k, n);
+      if (a.scale) sc = load8<true>(a.scale + req * a.ld_mod + k, n, req == a.n_req - 1);
+      if (a.shift) sh = load8<true>(a.shift + req * a.ld_mod + k, n, req == a.n_req - 1);
       unpack8(sc, m);
       unpack8(sh, b);
 #pragma unroll
@@ -489,7 +519,7 @@ __device__ __forceinline__ GnAffine gn_affine(const GroupNormProblem &a, const G
     f.a[j] = rstd[j] * m[j];
   }
   if (a.scale) {
-    unpack8(load8<TAIL>(a.scale + sample * a.ld_mod + t.c, t.nv), m);
+    unpack8(load8<TAIL>(a.scale + sample * a.ld_mod + t.c, t.nv, sample == a.B - 1), m);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       f.a[j] = __builtin_fmaf(f.a[j], m[j], f.a[j]);
@@ -497,7 +527,7 @@ __device__ __forceinline__ GnAffine gn_affine(const GroupNormProblem &a, const G
     }
   }
   if (a.shift) {
-    unpack8(load8<TAIL>(a.shift + sample * a.ld_mod + t.c, t.nv), s);
+    unpack8(load8<TAIL>(a.shift + sample * a.ld_mod + t.c, t.nv, sample == a.B - 1), s);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f.b[j] += s[j];
   }
@@ -532,7 +562,8 @@ __global__ __launch_bounds__(T) void groupnorm_one_kernel(GroupNormProblem a) {
   for (int u = 0; u < U; ++u) {
     const int p = t.rsub + u * t.rs;
     z[u] = v4u{0u, 0u, 0u, 0u};
-    if (t.active && p < a.P) z[u] = load8<TAIL>(a.z + (row0 + p) * a.ld_z + t.c, t.nv);
+    if (t.active && p < a.P)
+      z[u] = load8<TAIL>(a.z + (row0 + p) * a.ld_z + t.c, t.nv, row0 + p == a.B * a.P - 1);
   }
   float s[8], f[8], mu[8];
 #pragma unroll
@@ -640,23 +671,25 @@ __global__ __launch_bounds__(T) void groupnorm_stats_kernel(GroupNormProblem a) 
   float *waves = smem + 16 * T, *counts = waves + T / 64;  // [rs]: rows of a row step
   const int64_t p0 = (int64_t)blk * a.rows_per_block;
   const int rows = gn_rows(a, blk);
-  const uint16_t *z = a.z + (sample * a.P + p0) * a.ld_z + t.c;
+  const int64_t row0 = sample * a.P + p0;
+  auto load_z = [&](int p) {  // past the block: its last row again
+    p = min(p, rows - 1);
+    return load8<TAIL>(a.z + (row0 + p) * a.ld_z + t.c, t.nv, row0 + p == a.B * a.P - 1);
+  };
   float mean[8], m2[8], cnt = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) mean[j] = m2[j] = 0.0f;
   if (t.active) {
     v4u next[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      next[u] = load8<TAIL>(z + min(t.rsub + u * t.rs, rows - 1) * a.ld_z, t.nv);
+    for (int u = 0; u < U; ++u) next[u] = load_z(t.rsub + u * t.rs);
     int p = t.rsub;
     for (; p + (U - 1) * t.rs < rows; p += U * t.rs) {
       v4u v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         v[u] = next[u];
-        if (p + U * t.rs < rows)
-          next[u] = load8<TAIL>(z + min(p + (U + u) * t.rs, rows - 1) * a.ld_z, t.nv);
+        if (p + U * t.rs < rows) next[u] = load_z(p + (U + u) * t.rs);
       }
       add_rows<U>(v, U, mean, m2, cnt);
     }
@@ -713,10 +746,13 @@ __global__ __launch_bounds__(T) void groupnorm_apply_kernel(GroupNormProblem a) 
   const int rows = min(a.rows_per_part, gn_rows(a, blk) - in_block);
   if (rows <= 0) return;
   const int64_t p0 = sample * a.P + (int64_t)blk * a.rows_per_block + in_block;
+  auto load_z = [&](int p) {  // past the block: its last row again
+    p = min(p, rows - 1);
+    return load8<TAIL>(a.z + (p0 + p) * a.ld_z + t.c, t.nv, p0 + p == a.B * a.P - 1);
+  };
   v4u z[U];  // the first rows are on their way while the statistics are joined
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    z[u] = load8<TAIL>(a.z + (p0 + min(t.rsub + u * t.rs, rows - 1)) * a.ld_z + t.c, t.nv);
+  for (int u = 0; u < U; ++u) z[u] = load_z(t.rsub + u * t.rs);
 
   const int width = max(T, 8 * t.cb);  // at most as many groups
   float2 *sums = reinterpret_cast<float2 *>(smem);
@@ -786,8 +822,7 @@ __global__ __launch_bounds__(T) void groupnorm_apply_kernel(GroupNormProblem a) 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       now[u] = z[u];
-      if (p + U * t.rs < rows)
-        z[u] = load8<TAIL>(a.z + (p0 + min(p + (U + u) * t.rs, rows - 1)) * a.ld_z + t.c, t.nv);
+      if (p + U * t.rs < rows) z[u] = load_z(p + (U + u) * t.rs);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
