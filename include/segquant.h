@@ -304,8 +304,9 @@ int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
  *   workspace   device scratch, 16-byte aligned, of at least
  *               segquant_adapter_workspace_bytes() bytes (SEGQ_ERR_UNSUPPORTED
  *               with fewer), contents undefined afterwards; calls that share
- *               one must be ordered
- * Two launches.  The order of every sum is fixed.  Requires K % 64 == 0,
+ *               one must be ordered.  NULL where that size is 0.
+ * One launch, or two through the workspace.  The order of every sum is fixed.
+ * Requires K % 64 == 0,
  * N % 16 == 0, 16-byte aligned tensor pointers (int32 arrays and alpha 4),
  * ld_x, ld_base and ld_y multiples of 8, M <= 2^27, N <= 1048560,
  * n_req <= 2^23.  M may be 0.
@@ -318,10 +319,11 @@ int segquant_adapter_add(int64_t M, int64_t N, int64_t K, const uint16_t *x_bf16
                          const uint16_t *base_bf16, int64_t ld_base, uint16_t *y_bf16,
                          int64_t ld_y, void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace of segquant_adapter_add for these sizes.  On invalid sizes
- * returns 0 and sets segquant_last_error(). */
+/* Workspace of segquant_adapter_add for these sizes (0: none).  On invalid
+ * sizes returns 0 and sets segquant_last_error(). */
 size_t segquant_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t n_req,
-                                        int32_t rank, int32_t n_nseg);
+                                        int32_t rank, int32_t n_nseg, const int32_t *nseg_offset,
+                                        const int32_t *nseg_width);
 
 /*
  * segquant_weight_packed_bytes -- size of the packed int8 weight for a

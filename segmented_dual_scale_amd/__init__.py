@@ -118,7 +118,7 @@ def load_library():
                                       I32, P, I32, P, P, P, P, I64, I32, P, I64, P],
         "segquant_adapter_add": [I64, I64, I64, P, I64, I32, P, P, I32, I32, P, P, P, P, I32, P, P,
                                  P, I64, P, I64, P, ctypes.c_size_t, P],
-        "segquant_adapter_workspace_bytes": [I64, I64, I64, I32, I32, I32],
+        "segquant_adapter_workspace_bytes": [I64, I64, I64, I32, I32, I32, P, P],
         "segquant_gemm_halves": [P, I32],
         "segquant_version": [],
         "segquant_status_string": [ctypes.c_int],
@@ -524,14 +524,12 @@ def _codes_out(out, M: int, K: int, layout: int, device, new):
     return out, out.data_ptr(), ld
 
 
-@functools.lru_cache(maxsize=1024)
-def _sizes_of(name: str, *sizes: int) -> int:
-    """A workspace size; it depends on the sizes alone."""
-    return int(getattr(load_library(), name)(*sizes))
-
-
 def segquant_groupnorm_workspace_bytes(B: int, P: int, C: int, groups: int) -> int:
     return int(load_library().segquant_groupnorm_workspace_bytes(B, P, C, groups))
+
+
+# workspace sizes depend on the sizes alone
+_groupnorm_bytes = functools.lru_cache(maxsize=256)(segquant_groupnorm_workspace_bytes)
 
 
 def segquant_groupnorm_quantize(z, groups: int, eps: float = 1e-5, gamma=None, beta=None,
@@ -568,7 +566,7 @@ def segquant_groupnorm_quantize(z, groups: int, eps: float = 1e-5, gamma=None, b
     if scale is not None and shift is not None and B > 1 and scale.stride(0) != shift.stride(0):
         raise ValueError("scale and shift must have the same row stride")
     workspace, ws, ws_bytes = _workspace(
-        workspace, _sizes_of, ("segquant_groupnorm_workspace_bytes", B, P, C, groups), dev)
+        workspace, _groupnorm_bytes, (B, P, C, groups), dev)
     _check(_on(dev, fn, z.data_ptr(), B, P, C, _row_ld(z, "z"), groups, eps,
                _want_array(gamma, "gamma", f32, (C,), dev),
                _want_array(beta, "beta", f32, (C,), dev),
@@ -638,8 +636,12 @@ def segquant_adanorm_quantize(h, eps: float = 1e-6, gamma=None, beta=None, scale
 
 
 def segquant_adapter_workspace_bytes(M: int, N: int, K: int, n_req: int, rank: int,
-                                     n_nseg: int = 1) -> int:
-    return int(load_library().segquant_adapter_workspace_bytes(M, N, K, n_req, rank, n_nseg))
+                                     nseg: Optional[Sequence[int]] = None) -> int:
+    n, off, wid, _ = _segments(nseg, N)
+    return int(load_library().segquant_adapter_workspace_bytes(M, N, K, n_req, rank, n, off, wid))
+
+
+_adapter_bytes = functools.lru_cache(maxsize=256)(segquant_adapter_workspace_bytes)
 
 
 def segquant_adapter_add(x, a, b, adapter, row_offset, base=None, alpha=None, rank=None,
@@ -654,8 +656,8 @@ def segquant_adapter_add(x, a, b, adapter, row_offset, base=None, alpha=None, ra
     [n_adapters]; rank: int32 [n_adapters], the true ranks; nseg: the layer's
     N-segments.  Everything but nseg is on the device.  Returns bf16 y [M][N];
     out may be base.  Rows of no request are left as they are, zeros in a
-    tensor allocated here.  workspace: a device tensor, or "auto" (from
-    torch's allocator)."""
+    tensor allocated here.  workspace: a device tensor, None, or "auto" (from
+    torch's allocator when the library asks for one)."""
     import torch
     fn = load_library().segquant_adapter_add
     bf, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, x.device
@@ -669,7 +671,7 @@ def segquant_adapter_add(x, a, b, adapter, row_offset, base=None, alpha=None, ra
     if out is None:
         out = torch.zeros(y_shape, dtype=bf, device=dev)
     workspace, ws, ws_bytes = _workspace(
-        workspace, _sizes_of, ("segquant_adapter_workspace_bytes", M, N, K, n_req, r, n), dev)
+        workspace, _adapter_bytes, (M, N, K, n_req, r, None if nseg is None else tuple(nseg)), dev)
     _check(_on(dev, fn, M, N, K, x.data_ptr(), _row_ld(x, "x"), n_req,
                _want_array(row_offset, "row_offset", i32, (n_req + 1,), dev),
                _want_array(adapter, "adapter", i32, (n_req,), dev), n_adapters, r,

@@ -112,99 +112,121 @@ __device__ __forceinline__ void wait_copies() {
 // WV-th 64-wide step of K, each with its own rotating pair of LDS buffers and
 // no barrier; their sums meet in LDS.  A copy is 8 rows x 128 bytes, whole
 // cache lines: copies of 64 bytes a row asked for each line twice, and the
-// second request waited on the first's (8192x6144, rank 64: 33 against NN us).
+// second request waited on the first's (8192x6144, rank 64: 33 against 28 us).
 // Lane l copies chunk (l%8) ^ ((row/2)%8) of its row, so operand row r finds
 // chunk c at place c ^ ((r/2)%8) and 16 lanes read 16 different groups of four
 // banks.
 template <int MT, int NT, int WV>
+struct Shrink {
+  static constexpr int kStep = (MT + NT) * 2048;  // bytes of a wave's step
+  static constexpr int kSums = WV * MT * NT * 1024;
+  static constexpr int kBytes = 2 * WV * kStep > kSums ? 2 * WV * kStep : kSums;
+
+  // Sums of the tile's rows against factor rows c0 .. over k0 <= k < k1, a
+  // wave's share in acc.
+  static __device__ __forceinline__ void products(const AdapterProblem &p, const RowTile &t,
+                                                  int c0, int64_t k0, int64_t k1, uint8_t *smem,
+                                                  v4f acc[MT][NT]) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rt = p.ns.n * p.rank;
+    const int pieces = k1 > k0 ? (int)((k1 - k0) / 64) : 0;
+    const int steps = wave < pieces ? (pieces - wave + WV - 1) / WV : 0;
+    const uint16_t *xp[2 * MT], *ap[2 * NT];
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) {
+      const int row = 8 * i + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
+      xp[i] = p.x + (t.row0 + min(row, t.rows - 1)) * p.ld_x + k0 + 64 * wave + 8 * chunk;
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) {
+      const int row = 8 * i + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
+      ap[i] = p.a + ((int64_t)t.adapter * rt + min(c0 + row, rt - 1)) * p.K + k0 + 64 * wave +
+              8 * chunk;
+    }
+    uint8_t *mine = smem + wave * 2 * kStep;
+    auto copy = [&](int step) {
+      uint8_t *to = mine + (step & 1) * kStep;
+      const int64_t k = 64 * WV * (int64_t)step;
+#pragma unroll
+      for (int i = 0; i < 2 * MT; ++i) copy_lds16(xp[i] + k, to + 1024 * i);
+#pragma unroll
+      for (int j = 0; j < 2 * NT; ++j) copy_lds16(ap[j] + k, to + 1024 * (2 * MT + j));
+    };
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    // this lane's 16 bytes of an operand block, for either half of the 64
+    const int r = lane & 15, g = lane >> 4, f = (r >> 1) & 7;
+    const int at[2] = {128 * r + 16 * (g ^ f), 128 * r + 16 * ((4 + g) ^ f)};
+    if (steps > 0) copy(0);
+    for (int s = 0; s < steps; ++s) {
+      if (s + 1 < steps) {
+        copy(s + 1);
+        wait_copies<2 * (MT + NT)>();
+      } else {
+        wait_copies<0>();
+      }
+      const uint8_t *from = mine + (s & 1) * kStep;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        v4u x[MT], w[NT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) x[i] = *reinterpret_cast<const v4u *>(from + 2048 * i + at[h]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          w[j] = *reinterpret_cast<const v4u *>(from + 2048 * (MT + j) + at[h]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) acc[i][j] = mfma(w[j], x[i], acc[i][j]);
+      }
+    }
+  }
+
+  // The waves' shares to LDS (the copies' buffers, once every wave is done).
+  static __device__ __forceinline__ void gather(const v4f acc[MT][NT], uint8_t *smem) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < MT * NT; ++u)
+      reinterpret_cast<v4f *>(smem)[(wave * MT * NT + u) * 64 + lane] = acc[u / NT][u % NT];
+    __syncthreads();
+  }
+
+  // Block u = NT * (block of rows) + (block of ranks) of the sum, row by row:
+  // lane l has row l/4, ranks 4 (l%4) .. +3; q0 is the block's first rank.
+  static __device__ __forceinline__ v4f block(const uint8_t *smem, int u, int q0, int rank,
+                                              float alpha) {
+    const int lane = threadIdx.x & 63, from = 16 * (lane & 3) + (lane >> 2);
+    v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < WV; ++w)
+      v += reinterpret_cast<const v4f *>(smem)[(w * MT * NT + u) * 64 + from];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = q0 + 4 * (lane & 3) + i < rank ? v[i] * alpha : 0.0f;
+    return v;
+  }
+};
+
+template <int MT, int NT, int WV>
 __global__ __launch_bounds__(64 * WV) void adapter_shrink_kernel(AdapterProblem p) {
-  constexpr int kStep = (MT + NT) * 2048;  // bytes of a wave's step
-  constexpr int kSums = WV * MT * NT * 1024;
-  constexpr int kBytes = 2 * WV * kStep > kSums ? 2 * WV * kStep : kSums;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kBytes];
+  using Sh = Shrink<MT, NT, WV>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[Sh::kBytes];
   const RowTile t = find_tile<16 * MT>(p, blockIdx.x);
-  const int a = t.adapter;
-  if (t.rows == 0 || a < 0) return;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t.rows == 0 || t.adapter < 0) return;
   const int rt = p.ns.n * p.rank, c0 = blockIdx.y * 16 * NT;
   const int64_t k0 = (int64_t)blockIdx.z * p.k_per_split;
-  const int64_t k1 = min(k0 + p.k_per_split, p.K);
-  const int pieces = k1 > k0 ? (int)((k1 - k0) / 64) : 0;
-  const int steps = wave < pieces ? (pieces - wave + WV - 1) / WV : 0;
-
-  const uint16_t *xp[2 * MT], *ap[2 * NT];
-#pragma unroll
-  for (int i = 0; i < 2 * MT; ++i) {
-    const int row = 8 * i + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
-    xp[i] = p.x + (t.row0 + min(row, t.rows - 1)) * p.ld_x + k0 + 64 * wave + 8 * chunk;
-  }
-#pragma unroll
-  for (int i = 0; i < 2 * NT; ++i) {
-    const int row = 8 * i + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
-    ap[i] = p.a + ((int64_t)a * rt + min(c0 + row, rt - 1)) * p.K + k0 + 64 * wave + 8 * chunk;
-  }
-  uint8_t *mine = smem + wave * 2 * kStep;
-  auto copy = [&](int step) {
-    uint8_t *to = mine + (step & 1) * kStep;
-    const int64_t k = 64 * WV * (int64_t)step;
-#pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) copy_lds16(xp[i] + k, to + 1024 * i);
-#pragma unroll
-    for (int j = 0; j < 2 * NT; ++j) copy_lds16(ap[j] + k, to + 1024 * (2 * MT + j));
-  };
-
   v4f acc[MT][NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  // this lane's 16 bytes of an operand block, for either half of the 64
-  const int r = lane & 15, g = lane >> 4, f = (r >> 1) & 7;
-  const int at[2] = {128 * r + 16 * (g ^ f), 128 * r + 16 * ((4 + g) ^ f)};
-  if (steps > 0) copy(0);
-  for (int s = 0; s < steps; ++s) {
-    if (s + 1 < steps) {
-      copy(s + 1);
-      wait_copies<2 * (MT + NT)>();
-    } else {
-      wait_copies<0>();
-    }
-    const uint8_t *from = mine + (s & 1) * kStep;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      v4u x[MT], w[NT];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) x[i] = *reinterpret_cast<const v4u *>(from + 2048 * i + at[h]);
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        w[j] = *reinterpret_cast<const v4u *>(from + 2048 * (MT + j) + at[h]);
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = mfma(w[j], x[i], acc[i][j]);
-    }
-  }
-
-  const float alpha = p.alpha ? p.alpha[a] : 1.0f;
-  const int rank = rank_of(p, a);
-  __syncthreads();  // the buffers become the sums
-  v4f(*sums)[MT * NT][64] = reinterpret_cast<v4f(*)[MT * NT][64]>(smem);
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) sums[wave][i * NT + j][lane] = acc[i][j];
-  __syncthreads();
-  // stored row by row: lane l has row l/4, ranks 4 (l%4) .. +3 of a block
-  const int from = 16 * (lane & 3) + (lane >> 2);
-  for (int u = wave; u < MT * NT; u += WV) {
+  Sh::products(p, t, c0, k0, min(k0 + p.k_per_split, p.K), smem, acc);
+  const float alpha = p.alpha ? p.alpha[t.adapter] : 1.0f;
+  const int rank = rank_of(p, t.adapter);
+  Sh::gather(acc, smem);
+  const int lane = threadIdx.x & 63;
+  for (int u = threadIdx.x >> 6; u < MT * NT; u += WV) {
     const int m = 16 * (u / NT) + (lane >> 2), c = c0 + 16 * (u % NT);
-    v4f v = sums[0][u][from];
-#pragma unroll
-    for (int w = 1; w < WV; ++w) v += sums[w][u][from];
-    const int q = c - div24(c, p.rank) * p.rank + 4 * (lane & 3);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = q + i < rank ? v[i] * alpha : 0.0f;
+    const v4f v = Sh::block(smem, u, c - div24(c, p.rank) * p.rank, rank, alpha);
     if (m < t.rows && c < rt)
       *reinterpret_cast<v4f *>(t_block(p, blockIdx.z, c / 16) + (t.row0 + m) * 16 +
                                4 * (lane & 3)) = v;
@@ -250,21 +272,26 @@ __device__ __forceinline__ ColRun find_run(const NSegEnds &ns, int run, int per_
   return c;
 }
 
-// Grid: (row tile, run of column blocks of one segment).  A workgroup keeps
-// its rows' t in LDS as matrix-core operands, made once by its four waves; the
-// waves take the run's blocks of 64 columns in turn.  16 ranks fill one
-// instruction: its 32 contracted values are t's hi then lo halves against the
-// 16 values of B twice.  A block's B (RC blocks of 16 ranks) is 2 RC KiB of
-// contiguous memory, copied to LDS with chunk c of column n at place c ^
-// f(n), and held in registers for all rows, so the next block's copy runs
-// under this one's products; its base is loaded a block ahead too.
-template <int MT, int RC>
-struct ExpandLds {
-  v4u t[MT * RC][64];
-  uint8_t b[4][2048 * RC];
-  float out[4][16][68];  // a row of 64 columns, padded
-};
+// Four ranks of a row of t (lane l of a wave: row l/4, ranks 4 (l%4) .. +3 of a
+// 16 x 16 block) as the matrix-core operand of the block: lane 16 c + row holds
+// the hi halves of ranks 8c .. +7, and the lo halves 32 lanes on.
+__device__ __forceinline__ void store_operand(v4u *op, v4f v) {
+  const int lane = threadIdx.x & 63;
+  v2u hi, lo;
+  split4(v, hi, lo);
+  v2u *to = reinterpret_cast<v2u *>(op) + 2 * (16 * ((lane & 3) >> 1) + (lane >> 2)) + (lane & 1);
+  to[0] = hi;
+  to[64] = lo;
+}
 
+// The second product for a workgroup's rows and a run of columns.  t stands in
+// LDS as matrix-core operands; the four waves take the run's blocks of 64
+// columns in turn.  16 ranks fill one instruction: its 32 contracted values
+// are t's hi then lo halves against the 16 values of B twice.  A block's B (RC
+// blocks of 16 ranks) is 2 RC KiB of contiguous memory, copied to LDS with
+// chunk c of column n at place c ^ f(n), and held in registers for all rows,
+// so the next block's copy runs under this one's products; its base is loaded
+// a block ahead too.
 template <int RC>
 __device__ __forceinline__ int b_place(int chunk, int col) {
   return RC == 4 ? chunk ^ ((col >> 1) & 7) : RC == 2 ? chunk ^ ((col >> 2) & 3)
@@ -272,137 +299,196 @@ __device__ __forceinline__ int b_place(int chunk, int col) {
 }
 
 template <int MT, int RC>
-__global__ __launch_bounds__(256) void adapter_expand_kernel(AdapterProblem p) {
-  __shared__ __attribute__((aligned(1024))) ExpandLds<MT, RC> lds;
-  const ColRun run = find_run(p.ns, blockIdx.y, p.run_tiles);
-  const RowTile t = find_tile<16 * MT>(p, blockIdx.x);
-  const int a = t.adapter;
-  if (t.rows == 0 || run.seg == p.ns.n || (a < 0 && p.base == p.y)) return;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  const int orow = lane >> 3, ocol = 8 * (lane & 7);  // this lane's place in a row of the output
-  v4u base[MT][2], b[RC][4];
+struct Expand {
+  static constexpr int kB = 2048 * RC;        // bytes of a block's B, per wave
+  static constexpr int kOut = 16 * 68 * 4;    // 16 rows of 64 columns, padded, per wave
+  static constexpr int kBytes = 4 * (kB + kOut);
 
-  auto load_base = [&](int i, int n0) {
+  const AdapterProblem &p;
+  const RowTile &t;
+  const ColRun &run;
+  uint8_t *b_lds;
+  float (*out)[68];
+  int n0;  // this wave's next block of columns
+  v4u base[MT][2];
+
+  __device__ __forceinline__ Expand(const AdapterProblem &p, const RowTile &t, const ColRun &run,
+                                    uint8_t *lds)
+      : p(p), t(t), run(run) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    b_lds = lds + wave * kB;
+    out = reinterpret_cast<float(*)[68]>(lds + 4 * kB + wave * kOut);
+    n0 = run.n0 + 64 * wave;
+  }
+
+  __device__ __forceinline__ void load_base(int i, int n) {
+    const int lane = threadIdx.x & 63;
+    const int64_t col = n + 8 * (lane & 7);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int m = 16 * i + 8 * h + orow;
+      const int m = 16 * i + 8 * h + (lane >> 3);
       base[i][h] = v4u{0u, 0u, 0u, 0u};
-      if (p.base && m < t.rows && n0 + ocol < run.end)
-        base[i][h] = *reinterpret_cast<const v4u *>(p.base + (t.row0 + m) * p.ld_base + n0 + ocol);
+      if (p.base && m < t.rows && col < run.end)
+        base[i][h] = *reinterpret_cast<const v4u *>(p.base + (t.row0 + m) * p.ld_base + col);
     }
-  };
-  auto copy_b = [&](int n0) {
+  }
+
+  __device__ __forceinline__ void first_base() {
+    if (n0 < run.end) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) load_base(i, n0);
+    }
+  }
+
+  __device__ __forceinline__ void copy_b(int n) {
+    if (t.adapter < 0 || n >= run.end) return;
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int q = 0; q < 2 * RC; ++q) {
-      const int flat = 64 * q + lane, n = flat / (2 * RC), place = flat % (2 * RC);
-      copy_lds16(p.b + ((int64_t)a * p.N + min(n0 + n, run.end - 1)) * p.rank +
-                     8 * b_place<RC>(place, n),
-                 lds.b[wave] + 1024 * q);
+      const int flat = 64 * q + lane, col = flat / (2 * RC), place = flat % (2 * RC);
+      copy_lds16(p.b + ((int64_t)t.adapter * p.N + min(n + col, run.end - 1)) * p.rank +
+                     8 * b_place<RC>(place, col),
+                 b_lds + 1024 * q);
     }
-  };
-
-  int n0 = run.n0 + 64 * wave;
-  if (n0 < run.end) {
-    if (a >= 0) copy_b(n0);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) load_base(i, n0);
   }
-  int rank = 0;
-  if (a >= 0) {
-    rank = rank_of(p, a);
-    for (int f = wave; f < MT * RC; f += 4) {
-      // lane l: row l/4, ranks 4 (l%4) .. +3 of the block
-      const int m = min(16 * (f / RC) + (lane >> 2), t.rows - 1);
-      const int block = (run.seg * p.rank) / 16 + f % RC;
-      v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int s0 = 0; s0 < p.splits; s0 += 4) {  // the parts of K that the shrink left
-        v4f u[4];
+
+  __device__ __forceinline__ void columns(const v4u *tv, int rank) {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int orow = lane >> 3, ocol = 8 * (lane & 7);  // this lane's place in a row of y
+    for (; n0 < run.end; n0 += 256) {
+      const bool more = n0 + 256 < run.end;
+      v4u b[RC][4];
+      if (t.adapter >= 0) {
+        wait_copies<0>();
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          u[s] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-          if (s0 + s < p.splits)
-            u[s] = *reinterpret_cast<const v4f *>(t_block(p, s0 + s, block) + (t.row0 + m) * 16 +
-                                                  4 * (lane & 3));
+        for (int e = 0; e < RC; ++e)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int n = 16 * j + r;
+            b[e][j] = *reinterpret_cast<const v4u *>(b_lds + 32 * RC * n +
+                                                     16 * b_place<RC>(2 * e + (g & 1), n));
+          }
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // the reads are done: the buffer is free
+        __builtin_amdgcn_sched_barrier(0);
+        copy_b(n0 + 256);
+#pragma unroll
+        for (int e = 0; e < RC; ++e) {
+          if (16 * e + 16 > rank) {  // what is stored past an adapter's rank is not used
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int at = 16 * e + 8 * (g & 1) + 2 * q;
+                b[e][j][q] = at + 1 < rank ? b[e][j][q] : at < rank ? b[e][j][q] & 0xffffu : 0u;
+              }
+          }
         }
-        sum += (u[0] + u[1]) + (u[2] + u[3]);
       }
-      v2u hi, lo;
-      split4(sum, hi, lo);
-      // operand lane 16 c + row holds ranks 8c .. +7 (lo: 32 lanes on)
-      v2u *to = reinterpret_cast<v2u *>(lds.t[f]) +
-                2 * (16 * ((lane & 3) >> 1) + (lane >> 2)) + (lane & 1);
-      to[0] = hi;
-      to[64] = lo;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        v4u y[2] = {base[i][0], base[i][1]};
+        if (more) load_base(i, n0 + 256);
+        if (t.adapter >= 0) {
+          v4f acc[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int e = 0; e < RC; ++e) {
+            const v4u tf = tv[(i * RC + e) * 64 + lane];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] = mfma(b[e][j], tf, acc[j]);
+          }
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<v4f *>(&out[r][16 * j + 4 * g]) = acc[j];
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const v4f *d = reinterpret_cast<const v4f *>(&out[8 * h + orow][ocol]);
+            const v4f u = d[0], v = d[1];
+            y[h][0] = cvt_bf16x2(bf16_lo(y[h][0]) + u[0], bf16_hi(y[h][0]) + u[1]);
+            y[h][1] = cvt_bf16x2(bf16_lo(y[h][1]) + u[2], bf16_hi(y[h][1]) + u[3]);
+            y[h][2] = cvt_bf16x2(bf16_lo(y[h][2]) + v[0], bf16_hi(y[h][2]) + v[1]);
+            y[h][3] = cvt_bf16x2(bf16_lo(y[h][3]) + v[2], bf16_hi(y[h][3]) + v[3]);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int m = 16 * i + 8 * h + orow;
+          if (m < t.rows && n0 + ocol < run.end)
+            *reinterpret_cast<v4u *>(p.y + (t.row0 + m) * p.ld_y + n0 + ocol) = y[h];
+        }
+      }
+    }
+  }
+};
+
+// Grid: (row tile, run of column blocks of one segment).
+template <int MT, int RC>
+__global__ __launch_bounds__(256) void adapter_expand_kernel(AdapterProblem p) {
+  using Ex = Expand<MT, RC>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[MT * RC * 1024 + Ex::kBytes];
+  const ColRun run = find_run(p.ns, blockIdx.y, p.run_tiles);
+  const RowTile t = find_tile<16 * MT>(p, blockIdx.x);
+  if (t.rows == 0 || run.seg == p.ns.n || (t.adapter < 0 && p.base == p.y)) return;
+  v4u *tv = reinterpret_cast<v4u *>(smem);
+  Ex ex(p, t, run, smem + MT * RC * 1024);
+  ex.copy_b(ex.n0);
+  ex.first_base();
+  int rank = 0;
+  if (t.adapter >= 0) {
+    rank = rank_of(p, t.adapter);
+    const int lane = threadIdx.x & 63;
+    for (int f = threadIdx.x >> 6; f < MT * RC; f += 4) {
+      const int64_t row = t.row0 + min(16 * (f / RC) + (lane >> 2), t.rows - 1);
+      const int block = (run.seg * p.rank) / 16 + f % RC;
+      v4f u[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {  // the parts of K that the shrink left
+        u[s] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        if (s < p.splits)
+          u[s] = *reinterpret_cast<const v4f *>(t_block(p, s, block) + row * 16 + 4 * (lane & 3));
+      }
+      store_operand(tv + 64 * f, (u[0] + u[1]) + (u[2] + u[3]));
     }
   }
   __syncthreads();
-  for (; n0 < run.end; n0 += 256) {
-    const bool more = n0 + 256 < run.end;
-    if (a >= 0) {
-      wait_copies<0>();
-#pragma unroll
-      for (int e = 0; e < RC; ++e)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = 16 * j + r;
-          b[e][j] = *reinterpret_cast<const v4u *>(
-              lds.b[wave] + 32 * RC * n + 16 * b_place<RC>(2 * e + (g & 1), n));
-        }
-      __builtin_amdgcn_s_waitcnt(0xc07f);  // the reads are done: the buffer is free
-      __builtin_amdgcn_sched_barrier(0);
-      if (more) copy_b(n0 + 256);
-#pragma unroll
-      for (int e = 0; e < RC; ++e) {
-        if (16 * e + 16 > rank) {  // what is stored past an adapter's rank is not used
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int at = 16 * e + 8 * (g & 1) + 2 * q;
-              b[e][j][q] = at + 1 < rank ? b[e][j][q] : at < rank ? b[e][j][q] & 0xffffu : 0u;
-            }
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      v4u y[2] = {base[i][0], base[i][1]};
-      if (more) load_base(i, n0 + 256);
-      if (a >= 0) {
-        v4f acc[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int e = 0; e < RC; ++e) {
-          const v4u tf = lds.t[i * RC + e][lane];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j] = mfma(b[e][j], tf, acc[j]);
-        }
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<v4f *>(&lds.out[wave][r][16 * j + 4 * g]) = acc[j];
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const v4f *d = reinterpret_cast<const v4f *>(&lds.out[wave][8 * h + orow][ocol]);
-          const v4f u = d[0], v = d[1];
-          y[h][0] = cvt_bf16x2(bf16_lo(y[h][0]) + u[0], bf16_hi(y[h][0]) + u[1]);
-          y[h][1] = cvt_bf16x2(bf16_lo(y[h][1]) + u[2], bf16_hi(y[h][1]) + u[3]);
-          y[h][2] = cvt_bf16x2(bf16_lo(y[h][2]) + v[0], bf16_hi(y[h][2]) + v[1]);
-          y[h][3] = cvt_bf16x2(bf16_lo(y[h][3]) + v[2], bf16_hi(y[h][3]) + v[3]);
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int m = 16 * i + 8 * h + orow;
-        if (m < t.rows && n0 + ocol < run.end)
-          *reinterpret_cast<v4u *>(p.y + (t.row0 + m) * p.ld_y + n0 + ocol) = y[h];
-      }
-    }
+  ex.columns(tv, rank);
+}
+
+// ------------------------------------------------------- in one launch ----
+// Grid: (row tile, run of column blocks of one segment), each workgroup making
+// its rows' t for that segment over the whole of K and then its columns.  The
+// factor a is read by every row tile and x by every run, from the caches, in
+// return for a launch and t's way through memory.
+template <int MT, int RC>
+__global__ __launch_bounds__(256) void adapter_one_kernel(AdapterProblem p) {
+  using Sh = Shrink<MT, RC, 4>;
+  using Ex = Expand<MT, RC>;
+  // the copies' buffers become the sums, B and the output rows, the operands
+  constexpr int kOperands = Sh::kSums + Ex::kBytes, kAfter = kOperands + MT * RC * 1024;
+  __shared__ __attribute__((aligned(1024))) uint8_t
+      smem[Sh::kBytes > kAfter ? Sh::kBytes : kAfter];
+  const ColRun run = find_run(p.ns, blockIdx.y, p.run_tiles);
+  const RowTile t = find_tile<16 * MT>(p, blockIdx.x);
+  if (t.rows == 0 || run.seg == p.ns.n || (t.adapter < 0 && p.base == p.y)) return;
+  v4u *tv = reinterpret_cast<v4u *>(smem + kOperands);
+  Ex ex(p, t, run, smem + Sh::kSums);
+  ex.first_base();
+  int rank = 0;
+  if (t.adapter >= 0) {
+    v4f acc[MT][RC];
+    Sh::products(p, t, run.seg * p.rank, 0, p.K, smem, acc);
+    const float alpha = p.alpha ? p.alpha[t.adapter] : 1.0f;
+    rank = rank_of(p, t.adapter);
+    Sh::gather(acc, smem);
+    ex.copy_b(ex.n0);  // behind the sums, under the making of the operands
+    for (int f = threadIdx.x >> 6; f < MT * RC; f += 4)
+      store_operand(tv + 64 * f, Sh::block(smem, f, 16 * (f % RC), rank, alpha));
+    __syncthreads();
   }
+  ex.columns(tv, rank);
 }
 
 // The same for ranks above 64: t and B pass through the registers 16 ranks at
@@ -488,13 +574,6 @@ __global__ __launch_bounds__(256) void adapter_expand_wide_kernel(AdapterProblem
   }
 }
 
-// Launch shape from the sizes the host knows.
-struct AdapterPlan {
-  int mt, nt, splits;  // shrink
-  int64_t k_per_split;
-  int expand_mt;
-};
-
 // Tiles of at most bm rows: every request that has rows adds at most one
 // that is not full.
 int64_t tile_bound(const AdapterProblem &p, int bm) {
@@ -502,59 +581,79 @@ int64_t tile_bound(const AdapterProblem &p, int bm) {
   return n < p.M ? n : p.M;
 }
 
-AdapterPlan adapter_plan(const AdapterProblem &p) {
-  AdapterPlan l;
-  const int64_t rt = (int64_t)p.ns.n * p.rank;
-  const bool few = p.M <= 16 * (int64_t)p.n_req;  // at most 16 rows per request
-  // shrink: a tile of BM rows reads BM K values of x and, from L2, rt K of a
-  l.mt = few || rt <= 16 ? 1 : rt <= 32 ? 2 : 4;
-  l.nt = rt <= 16 ? 1 : rt <= 32 ? 2 : 4;
-  auto groups = [&] {
-    return tile_bound(p, 16 * l.mt) * ((rt + 16 * l.nt - 1) / (16 * l.nt));
-  };
-  while (few && l.nt > 1 && groups() < 256) l.nt /= 2;
-  // parts of K: while the workgroups do not fill the chip (two to a CU at the
-  // largest LDS footprint) and each keeps four steps.  8192x6144, rank 64,
-  // 136 tiles: 40, 32, 28, 35, 32 us with 2, 3, 4, 6, 8 parts
-  const int64_t steps = (p.K + 255) / 256;
-  l.splits = 1;
-  while (l.splits < 4 && groups() * l.splits < 512 && steps >= 2 * (l.splits + 1)) ++l.splits;
-  l.k_per_split = 256 * ((steps + l.splits - 1) / l.splits);
-  l.expand_mt = few ? 1 : 4;
-  return l;
+// Column blocks of 64 in runs of at most per_run, no run across a segment.
+int64_t column_runs(const AdapterProblem &p, int per_run) {
+  int64_t n = 0;
+  for (int i = 0, off = 0, end; i < p.ns.n; ++i, off = end) {
+    end = 16 * (int)p.ns.end16[i];
+    n += (end - off + 64 * per_run - 1) / (64 * per_run);
+  }
+  return n;
+}
+
+// Whether the form in one launch is taken.  It saves a launch and t's way
+// through memory, and pays with one workgroup walking the whole of K and with
+// reading x and a once per run of columns.  Against two launches (us, MI355X,
+// N = 1536; N = 4608 in 3 segments; rank 16, 32, 64):
+//   K 1536   64 requests of a row   6.2 7.7 10.3 | 8.5 10.9 17.3   one
+//                                   7.8 8.5  9.2 | 10.1 10.9 16.3  two
+//            4096 rows              12.7 14.9 22.1 | 20.6 23.0 35.3  one
+//                                   14.3 17.3 22.7 | 25.5 29.8 45.7  two
+//   K 3584   64 requests of a row   8.1 10.6 15.2 | 11.6 15.5 23.8  one
+//                                   8.3  9.2 10.1 | 11.0 12.5 18.6  two
+//            4096 rows              20.3 23.2 32.6 | 27.7 31.6 45.8  one
+//                                   18.2 20.9 27.3 | 30.3 36.2 54.3  two
+//   K 6144   4096 rows              29.7 34.1 45.8 | 37.6 43.1 59.5  one
+//                                   21.7 23.9 32.7 | 34.8 43.6 68.8  two
+bool in_one_launch(const AdapterProblem &p, bool few) {
+  return p.rank <= 64 && p.K <= (few && p.rank > 16 ? 2048 : 4096);
+}
+
+// Column blocks of a run: one per wave, and more until the workgroups of all
+// row tiles fit the chip at once.
+int run_tiles_for(const AdapterProblem &p, int64_t rows, int64_t at_once) {
+  int n = 4;
+  while (n < 64 && rows * column_runs(p, n) > at_once) n += 4;
+  return n;
 }
 
 }  // namespace
 
-size_t adapter_workspace_bytes(const AdapterProblem &p) {
-  return sizeof(float) * (size_t)adapter_plan(p).splits * (size_t)p.M * (size_t)p.ns.n *
-         (size_t)p.rank;
+size_t adapter_plan(AdapterProblem &p) {
+  const int64_t rt = (int64_t)p.ns.n * p.rank;
+  const bool few = p.M <= 16 * (int64_t)p.n_req;  // at most 16 rows per request
+  // shrink: a tile of BM rows reads BM K values of x and, from L2, rt K of a
+  p.mt = few || rt <= 16 ? 1 : rt <= 32 ? 2 : 4;
+  p.nt = rt <= 16 ? 1 : rt <= 32 ? 2 : 4;
+  auto groups = [&] {
+    return tile_bound(p, 16 * p.mt) * ((rt + 16 * p.nt - 1) / (16 * p.nt));
+  };
+  while (few && p.nt > 1 && groups() < 256) p.nt /= 2;
+  // parts of K: while the workgroups do not fill the chip (two to a CU at the
+  // largest LDS footprint) and each keeps two steps of 256.  8192x6144, rank
+  // 64, 136 tiles: 40, 32, 28, 35, 32 us with 2, 3, 4, 6, 8 parts
+  const int64_t steps = (p.K + 255) / 256;
+  p.splits = 1;
+  while (p.splits < 4 && groups() * p.splits < 512 && steps >= 2 * (p.splits + 1)) ++p.splits;
+  p.k_per_split = 256 * ((steps + p.splits - 1) / p.splits);
+  p.expand_mt = few ? 1 : 4;
+  p.one = in_one_launch(p, few);
+  p.run_tiles = run_tiles_for(p, tile_bound(p, p.one ? 16 : 16 * p.expand_mt),
+                              p.one || few ? 1024 : 768);
+  return p.one ? 0 : sizeof(float) * (size_t)p.splits * (size_t)p.M * (size_t)rt;
 }
 
 namespace {
 
 template <int MT>
-void launch_expand(const AdapterProblem &q, hipStream_t s) {
-  AdapterProblem p = q;
-  const int64_t rows = tile_bound(p, 16 * MT);
-  auto runs = [&](int per_run) {
-    int64_t n = 0;
-    for (int i = 0, off = 0, end; i < p.ns.n; ++i, off = end) {
-      end = 16 * (int)p.ns.end16[i];
-      n += (end - off + 64 * per_run - 1) / (64 * per_run);
-    }
-    return n;
-  };
+void launch_expand(const AdapterProblem &p, hipStream_t s) {
+  const unsigned rows = (unsigned)tile_bound(p, 16 * MT);
   if (p.rank > 64) {
     hipLaunchKernelGGL((adapter_expand_wide_kernel<MT>),
-                       dim3((unsigned)rows, (unsigned)((runs(1) + 3) / 4)), dim3(256), 0, s, p);
+                       dim3(rows, (unsigned)((column_runs(p, 1) + 3) / 4)), dim3(256), 0, s, p);
     return;
   }
-  // column blocks per workgroup: one per wave, and more until the workgroups
-  // all fit the chip at once
-  p.run_tiles = 4;
-  while (p.run_tiles < 64 && rows * runs(p.run_tiles) > (MT == 1 ? 1024 : 768)) p.run_tiles += 4;
-  const dim3 grid((unsigned)rows, (unsigned)runs(p.run_tiles));
+  const dim3 grid(rows, (unsigned)column_runs(p, p.run_tiles));
 #define SQ_EXPAND(RC) \
   hipLaunchKernelGGL((adapter_expand_kernel<MT, RC>), grid, dim3(256), 0, s, p)
   if (p.rank == 16) SQ_EXPAND(1);
@@ -566,31 +665,37 @@ void launch_expand(const AdapterProblem &q, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_adapter(const AdapterProblem &q, hipStream_t s) {
-  AdapterProblem p = q;
-  const AdapterPlan l = adapter_plan(p);
-  p.splits = l.splits;
-  p.k_per_split = l.k_per_split;
+hipError_t launch_adapter(const AdapterProblem &p, hipStream_t s) {
+  if (p.one) {
+    const dim3 grid((unsigned)tile_bound(p, 16), (unsigned)column_runs(p, p.run_tiles));
+#define SQ_ONE(RC) hipLaunchKernelGGL((adapter_one_kernel<1, RC>), grid, dim3(256), 0, s, p)
+    if (p.rank == 16) SQ_ONE(1);
+    else if (p.rank == 32) SQ_ONE(2);
+    else if (p.rank == 48) SQ_ONE(3);
+    else SQ_ONE(4);
+#undef SQ_ONE
+    return hipGetLastError();
+  }
   const int64_t rt = (int64_t)p.ns.n * p.rank;
-  const dim3 shrink((unsigned)tile_bound(p, 16 * l.mt),
-                    (unsigned)((rt + 16 * l.nt - 1) / (16 * l.nt)), (unsigned)l.splits);
-#define SQ_SHRINK(MT, NT) \
+  const dim3 shrink((unsigned)tile_bound(p, 16 * p.mt),
+                    (unsigned)((rt + 16 * p.nt - 1) / (16 * p.nt)), (unsigned)p.splits);
+#define SQ_SHRINK(MT, NT)                                                            \
   hipLaunchKernelGGL((adapter_shrink_kernel<MT, NT, (MT + NT > 5 ? 2 : 4)>), shrink, \
                      dim3(MT + NT > 5 ? 128 : 256), 0, s, p)
-#define SQ_SHRINK_NT(MT)            \
-  if (l.nt == 1) SQ_SHRINK(MT, 1);  \
-  else if (l.nt == 2) SQ_SHRINK(MT, 2); \
+#define SQ_SHRINK_NT(MT)                \
+  if (p.nt == 1) SQ_SHRINK(MT, 1);      \
+  else if (p.nt == 2) SQ_SHRINK(MT, 2); \
   else SQ_SHRINK(MT, 4);
-  if (l.mt == 1) {
+  if (p.mt == 1) {
     SQ_SHRINK_NT(1)
-  } else if (l.mt == 2) {
-    SQ_SHRINK_NT(2)
+  } else if (p.mt == 2) {
+    SQ_SHRINK(2, 2);
   } else {
-    SQ_SHRINK_NT(4)
+    SQ_SHRINK(4, 4);
   }
 #undef SQ_SHRINK_NT
 #undef SQ_SHRINK
-  if (l.expand_mt == 1) launch_expand<1>(p, s);
+  if (p.expand_mt == 1) launch_expand<1>(p, s);
   else launch_expand<4>(p, s);
   return hipGetLastError();
 }

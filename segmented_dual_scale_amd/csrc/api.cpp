@@ -536,12 +536,28 @@ static int adapter_sizes(int64_t M, int64_t N, int64_t K, int32_t n_req, int32_t
   return SEGQ_OK;
 }
 
+static int adapter_segments(int32_t n_nseg, const int32_t *nseg_offset, const int32_t *nseg_width,
+                            int64_t N, sq::AdapterProblem &p) {
+  sq::NSegTable ns{};
+  const int st = read_nseg(n_nseg, nseg_offset, nseg_width, N, ns);
+  if (st) return st;
+  for (int32_t i = 0; i < ns.n; ++i) {
+    if (ns.off[i] % 16)
+      return fail(SEGQ_ERR_ALIGN, "N-segment boundary %d is not a multiple of 16", ns.off[i]);
+    p.ns.end16[i] = (uint16_t)(ns.end[i] / 16);
+  }
+  return SEGQ_OK;
+}
+
 size_t segquant_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t n_req,
-                                        int32_t rank, int32_t n_nseg) {
+                                        int32_t rank, int32_t n_nseg, const int32_t *nseg_offset,
+                                        const int32_t *nseg_width) {
   sq::AdapterProblem p{};
-  if (adapter_sizes(M, N, K, n_req, rank, n_nseg, p)) return 0;
+  if (adapter_sizes(M, N, K, n_req, rank, n_nseg, p) ||
+      adapter_segments(n_nseg, nseg_offset, nseg_width, N, p))
+    return 0;
   ok();
-  return M ? sq::adapter_workspace_bytes(p) : 0;
+  return M ? sq::adapter_plan(p) : 0;
 }
 
 int segquant_adapter_add(int64_t M, int64_t N, int64_t K, const uint16_t *x_bf16, int64_t ld_x,
@@ -556,13 +572,7 @@ int segquant_adapter_add(int64_t M, int64_t N, int64_t K, const uint16_t *x_bf16
   if (st) return st;
   if (n_adapters < 1) return fail(SEGQ_ERR_SHAPE, "n_adapters %d < 1", n_adapters);
   if ((st = check_x(x_bf16, M, K, ld_x))) return st;
-  sq::NSegTable ns{};
-  if ((st = read_nseg(n_nseg, nseg_offset, nseg_width, N, ns))) return st;
-  for (int32_t i = 0; i < ns.n; ++i) {
-    if (ns.off[i] % 16)
-      return fail(SEGQ_ERR_ALIGN, "N-segment boundary %d is not a multiple of 16", ns.off[i]);
-    p.ns.end16[i] = (uint16_t)(ns.end[i] / 16);
-  }
+  if ((st = adapter_segments(n_nseg, nseg_offset, nseg_width, N, p))) return st;
   if (M == 0) return ok();
   if (!row_offset || !adapter || !a || !b || !y_bf16)
     return fail(SEGQ_ERR_NULL, "row_offset, adapter, a, b or y_bf16 is NULL");
@@ -574,10 +584,10 @@ int segquant_adapter_add(int64_t M, int64_t N, int64_t K, const uint16_t *x_bf16
   if ((st = check_rows(y_bf16, ld_y, N, "y_bf16"))) return st;
   if (base_bf16 == y_bf16 && ld_base != ld_y)
     return fail(SEGQ_ERR_SHAPE, "base_bf16 on y_bf16 needs ld_base = ld_y");
-  const size_t need = sq::adapter_workspace_bytes(p);
-  if (!workspace || workspace_bytes < need)
+  const size_t need = sq::adapter_plan(p);
+  if (need && (!workspace || workspace_bytes < need))
     return fail(SEGQ_ERR_UNSUPPORTED,
-                "adapters need a workspace of at least %zu bytes "
+                "adapters of this shape need a workspace of at least %zu bytes "
                 "(segquant_adapter_workspace_bytes)", need);
   if (!aligned16(workspace)) return fail(SEGQ_ERR_ALIGN, "workspace is not 16-byte aligned");
   p.x = x_bf16;

@@ -154,15 +154,19 @@ struct AdapterProblem {
   int64_t ld_base;
   uint16_t *y;
   int64_t ld_y;
-  float *t;  // workspace [splits][M][ns.n * rank]
-  // launch shape, filled in by the launch
-  int32_t splits, run_tiles;
+  float *t;  // workspace [splits][ns.n * rank / 16][M][16]
+  // launch shape, filled in by adapter_plan
+  bool one;                // one launch, no t in memory
+  int32_t mt, nt, splits;  // shrink: blocks of 16 rows, of 16 ranks, parts of K
   int64_t k_per_split;
+  int32_t expand_mt, run_tiles;  // second product: blocks of 16 rows, of 64 columns
 };
 
+// Choose the launch shape from the sizes (M, N, K, n_req, rank and the
+// segments) and return the bytes of `t` it needs.
+size_t adapter_plan(AdapterProblem &p);
+// Launch a planned problem.
 hipError_t launch_adapter(const AdapterProblem &p, hipStream_t s);
-// Bytes of `t` (M, K, n_req, rank and ns.n of the problem decide).
-size_t adapter_workspace_bytes(const AdapterProblem &p);
 
 constexpr int kSmallMMax = 16;
 

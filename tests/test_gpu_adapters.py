@@ -100,6 +100,13 @@ CASES = [
     ([31, 2], 320, 64, [64], 256, [1, 0], [256, 200]),
     ([16, 16, 16], 64, 2048, [16] * 128, 16, [0, 1, 0], None),
     ([2000], 64, 48, [48], 16, [-1], None),
+    # two launches
+    ([1] * 5, 8192, 160, [80, 80], 16, [0, 1, -1, 2, 0], [16, 7, 16]),
+    ([1, 0, 3, 16, 2], 4160, 336, [336], 32, [0, 2, 1, 0, -1], [32, 30, 5]),
+    ([90, 200, 17], 4224, 208, [208], 16, [1, 0, -1], [11, 16]),
+    ([500, 33], 4096 + 64, 400, [64, 336], 48, [1, 0], [48, 20]),
+    ([5, 40], 128, 320, [16] * 20, 64, [1, 0], None),
+    ([7] * 9, 64, 32, [32], 128, [i % 2 for i in range(9)], [128, 1]),
 ]
 
 
@@ -169,9 +176,10 @@ def test_offsets_out_of_order_stay_in_bounds(off):
 
 
 def test_workspace_of_the_exact_size_is_kept_to():
-    for lens, K, rank in (([1] * 3, 1536, 16), ([700, 20], 256, 64)):
+    for lens, K, rank in (([1] * 3, 8192, 16), ([700, 20], 5120, 64), ([9], 64, 80)):
         c = Case(lens, K, 64, [64], rank, [0] * len(lens))
         nb = S.segquant_adapter_workspace_bytes(sum(lens), 64, K, len(lens), rank)
+        assert nb > 0
         ws = torch.full((nb + 4096,), 77, dtype=torch.uint8, device=DEV)
         c.check(c.run(workspace=ws[:nb]))
         assert (ws[nb:] == 77).all()
@@ -206,10 +214,12 @@ def test_adapters_beyond_32_bit_offsets():
 def test_on_another_stream_and_in_graphs_that_share_a_workspace():
     """Two captured calls with one workspace, replayed in turn between eager
     calls on new inputs and new request tables."""
-    cs = [Case([1] * 20, 512, 192, [96, 96], 16, [i % 3 for i in range(20)], tail=4),
-          Case([100, 200, 40], 256, 64, [64], 32, [0, 1, -1])]
+    cs = [Case([1] * 20, 4224, 192, [96, 96], 16, [i % 3 for i in range(20)], tail=4),
+          Case([100, 200, 40], 4160, 64, [64], 32, [0, 1, -1]),
+          Case([70, 30], 256, 64, [64], 32, [0, 1])]
     nb = max(S.segquant_adapter_workspace_bytes(len(c.x), c.b.shape[1], c.x.shape[1],
-                                                len(c.ids), c.b.shape[2], len(c.nseg)) for c in cs)
+                                                len(c.ids), c.b.shape[2], c.nseg) for c in cs)
+    assert nb > 0
     ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
     outs = [torch.zeros_like(c.base) for c in cs]
     side = torch.cuda.Stream()

@@ -178,9 +178,9 @@ def adapter(M=8, N=64, K=64, x=FAKE, ld_x=None, n_req=2, row_offset=FAKE, ids=FA
     (dict(widths=[24, 40]), S.SEGQ_ERR_ALIGN),
     (dict(n_nseg=0), S.SEGQ_ERR_SEGMENTS),
     (dict(N=16 * 129, widths=[16] * 129), S.SEGQ_ERR_UNSUPPORTED),
-    (dict(work=None), S.SEGQ_ERR_UNSUPPORTED),
-    (dict(work_bytes=8 * 16 * 4 - 1), S.SEGQ_ERR_UNSUPPORTED),
-    (dict(work=ODD8), S.SEGQ_ERR_ALIGN),
+    (dict(M=64, rank=256, work=None), S.SEGQ_ERR_UNSUPPORTED),  # two launches
+    (dict(M=64, rank=256, work_bytes=64 * 256 * 4 - 1), S.SEGQ_ERR_UNSUPPORTED),
+    (dict(M=64, rank=256, work=ODD8), S.SEGQ_ERR_ALIGN),
 ])
 def test_adapter_refusals(kw, status):
     assert adapter(**kw) == status
@@ -193,7 +193,9 @@ def test_adapter_of_no_rows_is_ok():
 
 
 def test_adapter_workspace_bytes():
-    assert S.segquant_adapter_workspace_bytes(100, 64, 64, 3, 16, 2) % (100 * 2 * 16 * 4) == 0
+    assert S.segquant_adapter_workspace_bytes(100, 64, 64, 3, 16, [16, 48]) == 0  # one launch
+    two = S.segquant_adapter_workspace_bytes(4096, 64, 65536, 3, 16, [16, 48])
+    assert two > 0 and two % (4096 * 2 * 16 * 4) == 0
     assert S.segquant_adapter_workspace_bytes(100, 64, 60, 3, 16) == 0
     assert "K" in S.segquant_last_error()
 
