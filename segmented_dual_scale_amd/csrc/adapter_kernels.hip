@@ -591,30 +591,62 @@ int64_t column_runs(const AdapterProblem &p, int per_run) {
   return n;
 }
 
-// Whether the form in one launch is taken.  It saves a launch and t's way
-// through memory, and pays with one workgroup walking the whole of K and with
-// reading x and a once per run of columns.  Against two launches (us, MI355X,
-// N = 1536; N = 4608 in 3 segments; rank 16, 32, 64):
-//   K 1536   64 requests of a row   6.2 7.7 10.3 | 8.5 10.9 17.3   one
-//                                   7.8 8.5  9.2 | 10.1 10.9 16.3  two
-//            4096 rows              12.7 14.9 22.1 | 20.6 23.0 35.3  one
-//                                   14.3 17.3 22.7 | 25.5 29.8 45.7  two
-//   K 3584   64 requests of a row   8.1 10.6 15.2 | 11.6 15.5 23.8  one
-//                                   8.3  9.2 10.1 | 11.0 12.5 18.6  two
-//            4096 rows              20.3 23.2 32.6 | 27.7 31.6 45.8  one
-//                                   18.2 20.9 27.3 | 30.3 36.2 54.3  two
-//   K 6144   4096 rows              29.7 34.1 45.8 | 37.6 43.1 59.5  one
-//                                   21.7 23.9 32.7 | 34.8 43.6 68.8  two
-bool in_one_launch(const AdapterProblem &p, bool few) {
-  return p.rank <= 64 && p.K <= (few && p.rank > 16 ? 2048 : 4096);
-}
-
-// Column blocks of a run: one per wave, and more until the workgroups of all
-// row tiles fit the chip at once.
+// Column blocks of a run in the second of two launches: one per wave, and more
+// until the workgroups of all row tiles fit the chip at once.
 int run_tiles_for(const AdapterProblem &p, int64_t rows, int64_t at_once) {
   int n = 4;
   while (n < 64 && rows * column_runs(p, n) > at_once) n += 4;
   return n;
+}
+
+// Whether the form in one launch is taken.  It saves a launch and t's way
+// through memory, and pays with one workgroup walking the whole of K and with
+// reading x and a once per run of columns.  One launch | two (us, MI355X, rank
+// 16, 32, 64):
+//   N 1536               K 1536                  K 3584                  K 6144
+//   64 requests of a row  6.1  7.5 10.2           8.2 10.7 15.4          10.5 14.2 21.1
+//                       | 7.8  8.6  9.1         | 8.4  9.2 10.2         | 8.7  9.7 11.3
+//   1024 rows             6.7  8.2 11.4           8.6 12.4 18.9          14.0 19.1 27.5
+//                      | 10.3 11.4 16.3        | 10.9 12.3 19.0        | 12.0 14.3 21.7
+//   4096 rows            12.8 14.4 17.6          15.9 17.5 21.1          19.1 21.1 25.6
+//                      | 14.4 17.5 22.6        | 18.5 20.7 27.1        | 21.8 23.8 32.9
+//   N 4608, 3 segments
+//   8192 rows            38.8 42.2 59.6          54.0 59.5 80.1          78.6 84.5 112.9
+//                      | 41.1 45.0 59.2        | 47.2 52.9 73.4        | 60.9 70.3  99.5
+// So: K up to 4096, less for few rows of high rank, and x no more than the
+// caches hold: above, x comes from memory, which many short copies per
+// workgroup use less well (8192 rows, K 6144, rank 64, x from memory: 58
+// against 48 us, though 41 against 45 with x in the last-level cache).
+bool in_one_launch(const AdapterProblem &p, bool few) {
+  if (p.rank > 64) return false;
+  if (few) return p.K <= (p.rank > 16 ? 2048 : 4096);
+  return p.K <= 4096 && 2 * p.M * p.K <= (48 << 20);
+}
+
+// Column blocks of a run in one launch: a longer run walks K fewer times, a
+// shorter one spreads better.  Estimated in us: a workgroup's start, steps of K
+// and blocks of a wave, two or three of them side by side on a CU at hardly
+// more than the time of one, or what all read of x and a from the caches at 13
+// TB/s, whichever is more.  64 requests, K 1536, six segments of 24 blocks,
+// rank 32: 15.6 us with runs of 12 (3 workgroups a CU), 17.9 with runs of 24;
+// 4096 rows, K 3584, N 1536, rank 64: 25.3 with runs of 12, 21.0 with one of 24.
+int one_run_tiles(const AdapterProblem &p, bool few) {
+  const int64_t tiles = tile_bound(p, 16) - (few ? 0 : p.n_req / 2);
+  const double start = 3.0 + (p.K / 256.0) * (0.1 + 0.004 * p.rank);
+  double best = 0.0;
+  int take = 4;
+  for (int n = 4; n <= 64; n += n < 16 ? 4 : 8) {
+    const int64_t groups = tiles * column_runs(p, n);
+    const double per_cu = (double)((groups + 255) / 256);
+    const double walk = (per_cu > 2.5 ? 0.4 * per_cu : 1.0) * (start + 0.8 * ((n + 3) / 4));
+    const double bytes = 2.0 * groups * p.K * (16 + p.rank) / 13e6;
+    const double cost = walk > bytes ? walk : bytes;
+    if (n == 4 || cost < best) {
+      best = cost;
+      take = n;
+    }
+  }
+  return take;
 }
 
 }  // namespace
@@ -638,8 +670,8 @@ size_t adapter_plan(AdapterProblem &p) {
   p.k_per_split = 256 * ((steps + p.splits - 1) / p.splits);
   p.expand_mt = few ? 1 : 4;
   p.one = in_one_launch(p, few);
-  p.run_tiles = run_tiles_for(p, tile_bound(p, p.one ? 16 : 16 * p.expand_mt),
-                              p.one || few ? 1024 : 768);
+  p.run_tiles = p.one ? one_run_tiles(p, few)
+                      : run_tiles_for(p, tile_bound(p, 16 * p.expand_mt), few ? 1024 : 768);
   return p.one ? 0 : sizeof(float) * (size_t)p.splits * (size_t)p.M * (size_t)rt;
 }
 
