@@ -498,41 +498,33 @@ __device__ __forceinline__ void group_sum(const float v[8], const GnTile &t, flo
   __syncthreads();
 }
 
-// This thread's per-channel normalisation t = (z - mu) a + b from its
-// groups' means and 1/sqrt(var + eps), the weight and the sample's modulation
-// folded into a and b.
+// This thread's per-channel normalisation t = (z - mu) a + b.  a starts as the
+// weight and b as the bias, the sample's modulation folded into both: loaded
+// while the statistics are on their way, a then gets 1/sqrt(var + eps).
 struct GnAffine {
   float mu[8], a[8], b[8];
-};
 
-template <bool TAIL>
-__device__ __forceinline__ GnAffine gn_affine(const GroupNormProblem &a, const GnTile &t,
-                                              const float mu[8], const float rstd[8],
-                                              int64_t sample) {
-  GnAffine f;
-  float m[8], s[8];
-  load8f<TAIL>(a.gamma ? a.gamma + t.c : nullptr, t.nv, 1.0f, m);
-  load8f<TAIL>(a.beta ? a.beta + t.c : nullptr, t.nv, 0.0f, f.b);
+  template <bool TAIL>
+  __device__ __forceinline__ void load(const GroupNormProblem &p, const GnTile &t,
+                                       int64_t sample) {
+    float m[8];
+    load8f<TAIL>(p.gamma ? p.gamma + t.c : nullptr, t.nv, 1.0f, a);
+    load8f<TAIL>(p.beta ? p.beta + t.c : nullptr, t.nv, 0.0f, b);
+    if (p.scale) {
+      unpack8(load8<TAIL>(p.scale + sample * p.ld_mod + t.c, t.nv, sample == p.B - 1), m);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    f.mu[j] = mu[j];
-    f.a[j] = rstd[j] * m[j];
-  }
-  if (a.scale) {
-    unpack8(load8<TAIL>(a.scale + sample * a.ld_mod + t.c, t.nv, sample == a.B - 1), m);
+      for (int j = 0; j < 8; ++j) {
+        a[j] = __builtin_fmaf(a[j], m[j], a[j]);
+        b[j] = __builtin_fmaf(b[j], m[j], b[j]);
+      }
+    }
+    if (p.shift) {
+      unpack8(load8<TAIL>(p.shift + sample * p.ld_mod + t.c, t.nv, sample == p.B - 1), m);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      f.a[j] = __builtin_fmaf(f.a[j], m[j], f.a[j]);
-      f.b[j] = __builtin_fmaf(f.b[j], m[j], f.b[j]);
+      for (int j = 0; j < 8; ++j) b[j] += m[j];
     }
   }
-  if (a.shift) {
-    unpack8(load8<TAIL>(a.shift + sample * a.ld_mod + t.c, t.nv, sample == a.B - 1), s);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f.b[j] += s[j];
-  }
-  return f;
-}
+};
 
 template <int ACT>
 __device__ __forceinline__ v4u gn_apply8(v4u z, const GnAffine &f) {
@@ -565,7 +557,9 @@ __global__ __launch_bounds__(T) void groupnorm_one_kernel(GroupNormProblem a) {
     if (t.active && p < a.P)
       z[u] = load8<TAIL>(a.z + (row0 + p) * a.ld_z + t.c, t.nv, row0 + p == a.B * a.P - 1);
   }
-  float s[8], f[8], mu[8];
+  GnAffine af;
+  if (t.active) af.load<TAIL>(a, t, sample);
+  float s[8], f[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) s[j] = 0.0f;
 #pragma unroll
@@ -580,7 +574,7 @@ __global__ __launch_bounds__(T) void groupnorm_one_kernel(GroupNormProblem a) {
   group_sum<T>(s, t, buf, waves, gs, a.D);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    mu[j] = gs[g[j]] * inv_n;
+    af.mu[j] = gs[g[j]] * inv_n;
     s[j] = 0.0f;
   }
 #pragma unroll
@@ -589,15 +583,14 @@ __global__ __launch_bounds__(T) void groupnorm_one_kernel(GroupNormProblem a) {
     unpack8(z[u], f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float d = in && j < t.nv ? f[j] - mu[j] : 0.0f;
+      const float d = in && j < t.nv ? f[j] - af.mu[j] : 0.0f;
       s[j] = __builtin_fmaf(d, d, s[j]);
     }
   }
   group_sum<T>(s, t, buf, waves, gs, a.D);
   if (!t.active) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) s[j] = __builtin_amdgcn_rsqf(gs[g[j]] * inv_n + a.eps);
-  const GnAffine af = gn_affine<TAIL>(a, t, mu, s, sample);
+  for (int j = 0; j < 8; ++j) af.a[j] *= __builtin_amdgcn_rsqf(gs[g[j]] * inv_n + a.eps);
   float ip = 0.0f, in = 0.0f;
   if (a.out.q) seg_scales(a.out, t.c, ip, in);
 #pragma unroll
@@ -753,6 +746,8 @@ __global__ __launch_bounds__(T) void groupnorm_apply_kernel(GroupNormProblem a) 
   v4u z[U];  // the first rows are on their way while the statistics are joined
 #pragma unroll
   for (int u = 0; u < U; ++u) z[u] = load_z(t.rsub + u * t.rs);
+  GnAffine af;
+  if (t.active) af.load<TAIL>(a, t, sample);
 
   const int width = max(T, 8 * t.cb);  // at most as many groups
   float2 *sums = reinterpret_cast<float2 *>(smem);
@@ -807,14 +802,12 @@ __global__ __launch_bounds__(T) void groupnorm_apply_kernel(GroupNormProblem a) 
   __syncthreads();
   if (!t.active) return;
   int g[8];
-  float mu[8], rs[8];
   gn_groups(t, a.D, g);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    mu[j] = mean[g[j]];
-    rs[j] = rstd[g[j]];
+    af.mu[j] = mean[g[j]];
+    af.a[j] *= rstd[g[j]];
   }
-  const GnAffine af = gn_affine<TAIL>(a, t, mu, rs, sample);
   float ip = 0.0f, in = 0.0f;
   if (a.out.q) seg_scales(a.out, t.c, ip, in);
   for (int p = t.rsub; p < rows; p += U * t.rs) {
