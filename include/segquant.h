@@ -299,7 +299,7 @@ int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
  *   n_nseg, nseg_offset, nseg_width
  *               N-segments (host), boundaries multiples of 16
  *   base_bf16   optional device bf16 [M][ld_base]: the layer's output (NULL:
- *               0); may be y_bf16 when ld_base = ld_y
+ *               0); may be y_bf16 when ld_base = ld_y, else apart from it
  *   y_bf16      device bf16 [M][ld_y]; must not overlap x, a or b
  *   workspace   device scratch, 16-byte aligned, of at least
  *               segquant_adapter_workspace_bytes() bytes (SEGQ_ERR_UNSUPPORTED
@@ -309,7 +309,7 @@ int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
  * Requires K % 64 == 0,
  * N % 16 == 0, 16-byte aligned tensor pointers (int32 arrays and alpha 4),
  * ld_x, ld_base and ld_y multiples of 8, M <= 2^27, N <= 1048560,
- * n_req <= 2^23.  M may be 0.
+ * n_req <= 2^22.  M may be 0.
  */
 int segquant_adapter_add(int64_t M, int64_t N, int64_t K, const uint16_t *x_bf16, int64_t ld_x,
                          int32_t n_req, const int32_t *row_offset, const int32_t *adapter,

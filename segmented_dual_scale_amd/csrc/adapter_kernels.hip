@@ -38,12 +38,17 @@ __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
                                                  __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
-// Tile `tile` of a batch cut into tiles of at most BM rows of one request, and
-// that request's adapter (-1: none, or an index outside the table).  Offsets
-// outside [0, M] are clamped, so no row outside the batch is named whatever
-// they hold; rows == 0: no such tile.  One wave asks; the adapter indices are
-// loaded beside the offsets, since a kernel of a few microseconds is a chain
-// of dependent loads before its first useful one.
+// The batch in tiles of at most BM rows of one request: request r has the tile
+// numbers from off[r]/BM + r up to the next request's, which is at least as
+// many as it needs (a last one may be empty), so a tile's request is found by a
+// search over the offsets alone and M/BM + n_req tiles are enough.  Where M
+// numbers are fewer (a row or so per request: by_row), a tile's number is its
+// first row's, and the numbers between a request's tiles are empty.  adapter is
+// the request's (-1: none, or an index outside the table); rows == 0: no such
+// tile.  Offsets outside [0, M] are clamped, so no row outside the batch is
+// named whatever they hold.  One wave asks; up to 64 requests take one step,
+// with the adapter indices loaded beside the offsets, since a kernel of a few
+// microseconds is a chain of dependent loads before its first useful one.
 struct RowTile {
   int32_t rows, adapter;
   int64_t row0;
@@ -51,34 +56,46 @@ struct RowTile {
 
 template <int BM>
 __device__ __forceinline__ RowTile find_tile(const AdapterProblem &p, int tile) {
-  const int lane = threadIdx.x & 63;
-  for (int i0 = 0; i0 < p.n_req; i0 += 64) {
-    const int i = min(i0 + lane, p.n_req - 1);
-    const int id = p.adapter[i];
-    const int lo = (int)min(max((int64_t)p.row_offset[i], (int64_t)0), p.M);
-    const int hi = (int)min(max((int64_t)p.row_offset[i + 1], (int64_t)0), p.M);
-    const int mine = i0 + lane < p.n_req && hi > lo ? (hi - lo + BM - 1) / BM : 0;
-    int upto = mine;  // tiles of the requests i0 .. i0 + lane
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(upto, o, 64);
-      upto += lane >= o ? v : 0;
+  const int lane = threadIdx.x & 63, n = p.n_req;
+  auto offset = [&](int i) { return (int)min(max((int64_t)p.row_offset[i], (int64_t)0), p.M); };
+  auto first_of = [&](int off, int r) { return p.by_row ? off : off / BM + r; };
+  int r, lo, hi, id;  // the last request whose first tile is not past this one
+  if (n <= 64) {
+    const int i = min(lane, n - 1);
+    const int mine = offset(i), next = offset(i + 1), a = p.adapter[i];
+    r = __popcll(__ballot(lane < n && first_of(mine, i) <= tile)) - 1;
+    if (r < 0) return {0, -1, 0};
+    r = __builtin_amdgcn_readfirstlane(r);
+    lo = __builtin_amdgcn_readlane(mine, r);
+    hi = __builtin_amdgcn_readlane(next, r);
+    id = __builtin_amdgcn_readlane(a, r);
+  } else {
+    const int step = (n + 63) / 64;  // every step'th request, then those from there
+    int i = min(lane * step, n - 1);
+    const int before =
+        __popcll(__ballot(lane * step < n && first_of(offset(i), i) <= tile)) - 1;
+    if (before < 0) return {0, -1, 0};
+    const int base = before * step;
+    r = base - 1;
+    for (int k = 0; k < step; k += 64) {
+      i = min(base + k + lane, n - 1);
+      r += __popcll(
+          __ballot(k + lane < step && base + k + lane < n && first_of(offset(i), i) <= tile));
     }
-    const uint64_t holds = __ballot(tile < upto);
-    if (holds) {
-      const int l = __ffsll((unsigned long long)holds) - 1;
-      const int at = (tile - (__builtin_amdgcn_readlane(upto, l) -
-                              __builtin_amdgcn_readlane(mine, l))) * BM;
-      const int a = __builtin_amdgcn_readlane(id, l);
-      RowTile t;
-      t.row0 = (int64_t)__builtin_amdgcn_readlane(lo, l) + at;
-      t.rows = min(BM, __builtin_amdgcn_readlane(hi, l) - __builtin_amdgcn_readlane(lo, l) - at);
-      t.adapter = a >= 0 && a < p.n_adapters ? a : -1;
-      return t;
-    }
-    tile -= __builtin_amdgcn_readlane(upto, 63);
+    r = min(max(__builtin_amdgcn_readfirstlane(r), 0), n - 1);
+    lo = offset(r);
+    hi = offset(r + 1);
+    id = p.adapter[r];
   }
-  return {0, -1, 0};
+  RowTile t;
+  const int past = tile - first_of(lo, r);  // tiles (by_row: rows) into the request
+  const int64_t first = lo + (int64_t)past * (p.by_row ? 1 : BM);
+  // past < 0: offsets that decrease, where the count above is no search
+  t.rows = past < 0 || (p.by_row && past % BM) ? 0
+           : (int)min((int64_t)BM, max((int64_t)0, hi - first));
+  t.row0 = first;
+  t.adapter = __builtin_amdgcn_readfirstlane(id >= 0 && id < p.n_adapters ? id : -1);
+  return t;
 }
 
 __device__ __forceinline__ int rank_of(const AdapterProblem &p, int a) {
@@ -574,11 +591,9 @@ __global__ __launch_bounds__(256) void adapter_expand_wide_kernel(AdapterProblem
   }
 }
 
-// Tiles of at most bm rows: every request that has rows adds at most one
-// that is not full.
+// Tile numbers of the batch (find_tile).
 int64_t tile_bound(const AdapterProblem &p, int bm) {
-  const int64_t n = p.M / bm + p.n_req;
-  return n < p.M ? n : p.M;
+  return p.by_row ? p.M : p.M / bm + p.n_req;
 }
 
 // Column blocks of 64 in runs of at most per_run, no run across a segment.
@@ -631,7 +646,7 @@ bool in_one_launch(const AdapterProblem &p, bool few) {
 // rank 32: 15.6 us with runs of 12 (3 workgroups a CU), 17.9 with runs of 24;
 // 4096 rows, K 3584, N 1536, rank 64: 25.3 with runs of 12, 21.0 with one of 24.
 int one_run_tiles(const AdapterProblem &p, bool few) {
-  const int64_t tiles = tile_bound(p, 16) - (few ? 0 : p.n_req / 2);
+  const int64_t tiles = few ? p.M : tile_bound(p, 16) - p.n_req / 2;  // about, not empty
   const double start = 3.0 + (p.K / 256.0) * (0.1 + 0.004 * p.rank);
   double best = 0.0;
   int take = 4;
@@ -654,6 +669,7 @@ int one_run_tiles(const AdapterProblem &p, bool few) {
 size_t adapter_plan(AdapterProblem &p) {
   const int64_t rt = (int64_t)p.ns.n * p.rank;
   const bool few = p.M <= 16 * (int64_t)p.n_req;  // at most 16 rows per request
+  p.by_row = p.M <= p.M / 16 + p.n_req;           // implies few: all tiles have 16 rows
   // shrink: a tile of BM rows reads BM K values of x and, from L2, rt K of a
   p.mt = few || rt <= 16 ? 1 : rt <= 32 ? 2 : 4;
   p.nt = rt <= 16 ? 1 : rt <= 32 ? 2 : 4;

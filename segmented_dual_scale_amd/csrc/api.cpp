@@ -516,8 +516,8 @@ static int adapter_sizes(int64_t M, int64_t N, int64_t K, int32_t n_req, int32_t
   if (K % 64 || N % 16)
     return fail(SEGQ_ERR_ALIGN, "adapters need K %% 64 == 0 and N %% 16 == 0 (K=%lld N=%lld)",
                 (long long)K, (long long)N);
-  if (M > (1 << 27) || n_req > (1 << 23) || N > 16 * 0xffff)
-    return fail(SEGQ_ERR_UNSUPPORTED, "M %lld > 2^27, n_req %d > 2^23 or N %lld > %d", (long long)M,
+  if (M > (1 << 27) || n_req > (1 << 22) || N > 16 * 0xffff)
+    return fail(SEGQ_ERR_UNSUPPORTED, "M %lld > 2^27, n_req %d > 2^22 or N %lld > %d", (long long)M,
                 n_req, (long long)N, 16 * 0xffff);
   if (n_req < 1) return fail(SEGQ_ERR_SHAPE, "n_req %d < 1", n_req);
   if (rank < 1 || rank % SEGQ_ADAPTER_RANK_STEP)

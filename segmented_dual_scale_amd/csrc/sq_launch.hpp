@@ -157,6 +157,7 @@ struct AdapterProblem {
   float *t;  // workspace [splits][ns.n * rank / 16][M][16]
   // launch shape, filled in by adapter_plan
   bool one;                // one launch, no t in memory
+  bool by_row;             // tiles numbered by their first rows
   int32_t mt, nt, splits;  // shrink: blocks of 16 rows, of 16 ranks, parts of K
   int64_t k_per_split;
   int32_t expand_mt, run_tiles;  // second product: blocks of 16 rows, of 64 columns

@@ -100,7 +100,11 @@ CASES = [
     ([31, 2], 320, 64, [64], 256, [1, 0], [256, 200]),
     ([16, 16, 16], 64, 2048, [16] * 128, 16, [0, 1, 0], None),
     ([2000], 64, 48, [48], 16, [-1], None),
+    ([i % 5 for i in range(5000)], 64, 32, [32], 16, [i % 3 - 1 for i in range(5000)], None),
+    ([0] * 100 + [40] + [0] * 29 + [1], 64, 32, [32], 16, [i % 2 for i in range(131)], [3, 16]),
+    ([1] * 60 + [0, 0, 17, 1, 35] + [1] * 60, 64, 32, [32], 16, [i % 3 - 1 for i in range(125)], None),
     # two launches
+    ([3] * 150, 4160, 96, [96], 48, [i % 4 - 1 for i in range(150)], None),
     ([1] * 5, 8192, 160, [80, 80], 16, [0, 1, -1, 2, 0], [16, 7, 16]),
     ([1, 0, 3, 16, 2], 4160, 336, [336], 32, [0, 2, 1, 0, -1], [32, 30, 5]),
     ([90, 200, 17], 4224, 208, [208], 16, [1, 0, -1], [11, 16]),

@@ -150,7 +150,7 @@ def adapter(M=8, N=64, K=64, x=FAKE, ld_x=None, n_req=2, row_offset=FAKE, ids=FA
     (dict(K=72, ld_x=72), S.SEGQ_ERR_ALIGN),
     (dict(N=40), S.SEGQ_ERR_ALIGN),
     (dict(M=(1 << 27) + 1), S.SEGQ_ERR_UNSUPPORTED),
-    (dict(n_req=(1 << 23) + 1), S.SEGQ_ERR_UNSUPPORTED),
+    (dict(n_req=(1 << 22) + 1), S.SEGQ_ERR_UNSUPPORTED),
     (dict(n_req=0), S.SEGQ_ERR_SHAPE),
     (dict(n_adapters=0), S.SEGQ_ERR_SHAPE),
     (dict(rank=8), S.SEGQ_ERR_ALIGN),
