@@ -24,8 +24,7 @@
 //
 // t stands between the launches as fp32 blocks of 16 ranks, [part of K][block]
 // [row][16]: a tile's rows of a block are contiguous.
-#include "sq_device.hpp"
-#include "sq_launch.hpp"
+#include "sq_rows.hpp"
 
 namespace sq {
 

@@ -15,6 +15,7 @@
 #include "../../include/segquant.h"
 #include "sq_api.hpp"
 #include "sq_launch.hpp"
+#include "sq_rows.hpp"
 
 namespace {
 

@@ -16,8 +16,7 @@
 // over a few values in registers, before squares are summed, and pieces are
 // joined as (count, mean, sum of squared deviations).
 #include "sq_activation.hpp"
-#include "sq_device.hpp"
-#include "sq_launch.hpp"
+#include "sq_rows.hpp"
 
 namespace sq {
 

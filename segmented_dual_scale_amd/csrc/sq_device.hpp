@@ -131,23 +131,6 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return f32_to_bf16_rne(lo) | (f32_to_bf16_rne(hi) << 16);
 }
 
-// The same rounding by the hardware's packed conversion (RNE; NaN stays NaN).
-__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
-  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-  typedef float v2f __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo, hi}), v2bf));
-}
-
-// x / d for 0 <= x < 2^24 and d >= 1, from the reciprocal with a correction:
-// a quarter of the instructions of an integer division.
-__device__ __forceinline__ int div24(int x, int d) {
-  int q = (int)((float)x * __builtin_amdgcn_rcpf((float)d));
-  const int r = x - q * d;
-  q -= r < 0 ? 1 : 0;
-  q += r >= d ? 1 : 0;
-  return q;
-}
-
 // Non-negative floats order like their bit patterns: the reductions below
 // take atomic max over uint32 bits.
 __device__ __forceinline__ float pos_part(float x) { return x > 0.0f ? x : 0.0f; }
@@ -167,39 +150,6 @@ __device__ __forceinline__ void scale_pair(float a, double q, float &s, float &i
   if (iv > 3.40282346638528859812e38f) iv = 0.0f;  // +inf
   s = iv == 0.0f ? 0.0f : (float)((double)a / q);
   inv = iv;
-}
-
-// Request of a row in a packed batch: off[0..n] are row offsets, request i
-// holds rows off[i] .. off[i+1]-1.  req is the number of off[1..n] that are
-// <= row: -1 for a row before off[0], n behind off[n]; end is the first row
-// after the request.  One wave asks about one row: 64 offsets a step, after
-// one step over every (n/64)th where there are more.  Whatever off holds, only
-// off[0..n] is read.
-struct RowRequest {
-  int32_t req;
-  int64_t end;
-};
-
-__device__ __forceinline__ RowRequest find_request(const int32_t *off, int32_t n, int64_t row) {
-  const int lane = threadIdx.x & 63;
-  int base = 0, limit = n;  // off[1..base] <= row; off beyond limit > row
-  if (n > 64) {
-    const int step = (n + 63) / 64;
-    const int32_t v = off[min((lane + 1) * step, n)];
-    base = min(__popcll(__ballot(v <= row)) * step, n);
-    limit = min(base + step, n);
-  }
-  int req = base;
-  for (int i = base; i < limit; i += 64) {
-    const int at = i + 1 + lane;
-    const int32_t v = off[min(at, n)];
-    req += __popcll(__ballot(at <= limit && v <= row));
-  }
-  req = __builtin_amdgcn_readfirstlane(req);
-  RowRequest r;
-  r.end = off[min(req + 1, n)];
-  r.req = off[0] <= row ? req : -1;
-  return r;
 }
 
 }  // namespace sq
