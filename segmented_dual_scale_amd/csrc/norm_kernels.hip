@@ -717,11 +717,13 @@ __global__ __launch_bounds__(T) void groupnorm_stats_kernel(GroupNormProblem a) 
 }
 
 // Launch 2 of 2: join the blocks' statistics, normalise, activate, store.
-// The blocks are joined around the first one's mean p: with n_i values of
-// mean m_i, S1 = sum n_i (m_i - p) and S2 = sum M2_i + n_i (m_i - p)^2 give
-// mean p + S1/N and variance S2/N - (S1/N)^2.  The first block is part of the
-// whole, so (mean - p)^2 <= (N/n_0) variance and the subtraction loses at
-// most log2 (N/n_0) <= 10 bits of fp32.
+// The blocks are joined around one block's mean p: with n_i values of mean
+// m_i, S1 = sum n_i (m_i - p) and S2 = sum M2_i + n_i (m_i - p)^2 give mean p +
+// S1/N and variance S2/N - (S1/N)^2.  That block, of n_0 values, is part of the
+// whole, so (mean - p)^2 <= (N/n_0) variance and the subtraction loses at most
+// log2 (N/n_0) bits of fp32.  It is a full one: the first rows, and of the
+// group's first two column blocks the one with more of its channels (the first
+// may hold a single one), so with 256 blocks a sample N/n_0 <= 2^9.
 template <int T, int ACT, bool TAIL>
 __global__ __launch_bounds__(T) void groupnorm_apply_kernel(GroupNormProblem a) {
   constexpr int U = 4;
@@ -763,7 +765,8 @@ __global__ __launch_bounds__(T) void groupnorm_apply_kernel(GroupNormProblem a) 
       cb0 = g * a.D / a.cols_per_block;
       cb1 = ((g + 1) * a.D - 1) / a.cols_per_block;
     }
-    const float pivot = part[(int64_t)cb0 * a.n_row_blocks * a.G + g].x;
+    const int pb = cb0 + (cb1 > cb0 && gn_chans(a, g, cb0) < gn_chans(a, g, cb0 + 1));
+    const float pivot = part[(int64_t)pb * a.n_row_blocks * a.G + g].x;
     float s1 = 0.0f, s2 = 0.0f;
     for (int cb = cb0; cb <= cb1; ++cb) {
       const float chans = (float)gn_chans(a, g, cb);

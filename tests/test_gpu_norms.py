@@ -173,6 +173,19 @@ def test_groupnorm_hard_values(P):
     assert (x[1].double() - ref[1]).abs().max() < 2.0 ** -7
 
 
+@pytest.mark.parametrize("value", [37.0, 255.0, 300.0, 1000.0])
+def test_groupnorm_a_group_that_starts_in_the_last_channel_of_a_column_block(value):
+    """Group 1 has one of its 2047 channels in the first block of 2048, whose
+    first rows are unlike the rest: 8 of its 1.4 million values carry all the
+    variance, so statistics joined around those 8 would lose 17 bits."""
+    z = torch.zeros(1, 680, 3 * 2047, device=DEV, dtype=BF)
+    _, z = padded(z, 6144, 0.0)
+    z[0, :8, 2047] = value
+    x = S.segquant_groupnorm_quantize(z, 3, 1e-5, x_out=True)[1]
+    ref, A, zmax, t = groupnorm_ref(z, 3, 1e-5, None, None, None, None, "none")
+    close(x, ref, A, zmax, t)
+
+
 def test_groupnorm_rows_beyond_32_bit_offsets():
     B, P, C = 3, 700_000, 1032
     assert B * P * C > 2 ** 31
