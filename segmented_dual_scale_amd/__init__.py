@@ -142,7 +142,7 @@ def load_library():
 
 # ----------------------------------------------------------------- helpers --
 def _segs(widths: Optional[Sequence[int]], total: int):
-    return _seg_lists((total,) if widths is None else tuple(widths))
+    return _seg_lists((total,) if widths is None else tuple(map(int, widths)))
 
 
 @functools.lru_cache(maxsize=256)
@@ -167,6 +167,8 @@ def _ptr(t):
 
 def _stream(t):
     import torch
+    if t.device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {t.device}")
     # torch.cuda.current_stream() takes 2 us
     return torch._C._cuda_getCurrentRawStream(t.device.index)
 
@@ -428,7 +430,7 @@ def _seg_arrays(widths: Tuple[int, ...]):
 
 
 def _segments(widths, total: int):
-    return _seg_arrays((total,) if widths is None else tuple(widths))
+    return _seg_arrays((total,) if widths is None else tuple(map(int, widths)))
 
 
 def _want(t, name: str, dtype, shape, device):
@@ -469,6 +471,20 @@ def _row_ld(t, name: str) -> int:
                 raise ValueError(f"{name}: its rows are not evenly spaced")
             below *= shape[d]
     return -(-K // 8) * 8 if ld is None else ld
+
+
+def _mod_ld(rows: int, params, names: str) -> int:
+    """The row distance that a request's parameters share."""
+    ld = None
+    for t in params:
+        if t is not None:
+            if ld is None:
+                ld, first = _row_ld(t, names), t
+            elif t.shape[-1] > 1 and t.stride(-1) != 1:
+                raise ValueError(f"{names} must have unit stride in their last dimension")
+            elif rows > 1 and t.stride(0) != first.stride(0):
+                raise ValueError(f"{names} must have the same row stride")
+    return ld or 0
 
 
 def _on(device, fn, *args):
@@ -515,9 +531,8 @@ def _codes_out(out, M: int, K: int, layout: int, device, new):
         raise ValueError(f"out must be an int8 tensor of {'2 planes of ' if planes else ''}{M} rows "
                          f"of at least {K} codes on {device}, got {out.dtype} {tuple(out.shape)} on "
                          f"{out.device}")
-    if M > 1:
-        ld = _row_ld(out[0] if planes else out, "out")
-    else:
+    ld = _row_ld(out[0] if planes else out, "out")
+    if M <= 1:
         ld = out.stride(0) if planes else (out.shape[-1] + 15) // 16 * 16
     if planes and out.stride(0) != M * ld:
         raise ValueError("out: the second plane must follow the first")
@@ -562,16 +577,13 @@ def segquant_groupnorm_quantize(z, groups: int, eps: float = 1e-5, gamma=None, b
         out, q, ld_q = _codes_out(out, B * P, C, layout, dev, torch.empty)
     else:
         out = None
-    mod = scale if scale is not None else shift
-    if scale is not None and shift is not None and B > 1 and scale.stride(0) != shift.stride(0):
-        raise ValueError("scale and shift must have the same row stride")
     workspace, ws, ws_bytes = _workspace(
         workspace, _groupnorm_bytes, (B, P, C, groups), dev)
     _check(_on(dev, fn, z.data_ptr(), B, P, C, _row_ld(z, "z"), groups, eps,
                _want_array(gamma, "gamma", f32, (C,), dev),
                _want_array(beta, "beta", f32, (C,), dev),
                _want(scale, "scale", bf, (B, C), dev), _want(shift, "shift", bf, (B, C), dev),
-               _row_ld(mod, "scale or shift"), act_kind, n, off, wid, act, q, ld_q, layout,
+               _mod_ld(B, (scale, shift), "scale and shift"), act_kind, n, off, wid, act, q, ld_q, layout,
                _want(x_out, "x_out", bf, shape, dev), _row_ld(x_out, "x_out"), ws, ws_bytes),
            "segquant_groupnorm_quantize")
     return out, x_out
@@ -601,6 +613,8 @@ def segquant_adanorm_quantize(h, eps: float = 1e-6, gamma=None, beta=None, scale
     M, K = shape
     mod = scale if scale is not None else shift if shift is not None else gate
     if row_offset is not None:
+        if n_req is not None and n_req != row_offset.numel() - 1:
+            raise ValueError(f"n_req {n_req} with row_offset of {row_offset.numel()} offsets")
         n_req = row_offset.numel() - 1
     elif n_req is None:
         n_req = mod.shape[0] if mod is not None else 1
@@ -617,10 +631,6 @@ def segquant_adanorm_quantize(h, eps: float = 1e-6, gamma=None, beta=None, scale
         out, q, ld_q = _codes_out(out, M, K, layout, dev, new)
     else:
         out = None
-    if n_req > 1:
-        for t in (scale, shift, gate):
-            if t is not None and t.stride(0) != mod.stride(0):
-                raise ValueError("scale, shift and gate must have the same row stride")
     params = (n_req, K)
     _check(_on(dev, fn, h.data_ptr(), M, K, _row_ld(h, "h"), _want(branch, "branch", bf, shape, dev),
                _row_ld(branch, "branch"), _want(gate, "gate", bf, params, dev),
@@ -628,7 +638,7 @@ def segquant_adanorm_quantize(h, eps: float = 1e-6, gamma=None, beta=None, scale
                _want_array(gamma, "gamma", f32, (K,), dev),
                _want_array(beta, "beta", f32, (K,), dev),
                _want(scale, "scale", bf, params, dev), _want(shift, "shift", bf, params, dev),
-               _row_ld(mod, "scale, shift or gate"), n_req,
+               _mod_ld(n_req, (scale, shift, gate), "scale, shift and gate"), n_req,
                _want_array(row_offset, "row_offset", torch.int32, (n_req + 1,), dev), n, off, wid,
                act, q, ld_q, layout, _want(x_out, "x_out", bf, shape, dev),
                _row_ld(x_out, "x_out")), "segquant_adanorm_quantize")

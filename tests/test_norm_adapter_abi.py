@@ -219,6 +219,8 @@ def bf(*shape):
     (dict(z=bf(1, 64, 4).transpose(1, 2)), "unit stride"),
     (dict(z=bf(2, 9, 64)[:, :4]), "evenly spaced"),
     (dict(workspace="mine"), "workspace"),
+    (dict(x_out=True, scale=bf(1, 64), shift=bf(1, 128)[:, ::2]), "unit stride"),
+    (dict(x_out=True, z=bf(2, 4, 64), scale=bf(2, 64), shift=bf(2, 72)[:, :64]), "row stride"),
     (dict(x_out=True), "on a GPU"),
 ])
 def test_groupnorm_binding_refusals(kw, text):
@@ -230,6 +232,15 @@ def test_groupnorm_binding_refusals(kw, text):
     (dict(h=bf(1, 4, 64)), r"\[M\]\[K\]"),
     (dict(scale=bf(2, 64), row_offset=torch.zeros(2, dtype=torch.int32)), "scale"),
     (dict(scale=bf(2, 64), shift=bf(2, 128)[:, :64]), "row stride"),
+    # a request alone has no row stride, its columns have one all the same
+    (dict(x_out=True, scale=bf(1, 64), shift=bf(64, 1).t(), gate=bf(1, 128)[:, ::2],
+          branch=bf(4, 64)), "unit stride"),
+    (dict(x_out=True, shift=bf(2, 64), gate=bf(2, 128)[:, ::2], branch=bf(4, 64)), "unit stride"),
+    (dict(act_scales=torch.zeros(4, 1), h=bf(1, 64),
+          out=torch.zeros(1, 128, dtype=torch.int8)[:, ::2]), "unit stride"),
+    (dict(act_scales=torch.zeros(4, 1), h=bf(1, 64), layout=S.SEGQ_Q_PLANES,
+          out=torch.zeros(2, 1, 128, dtype=torch.int8)[:, :, ::2]), "unit stride"),
+    (dict(x_out=True, n_req=2, row_offset=torch.zeros(2, dtype=torch.int32)), "n_req"),
     (dict(branch=bf(4, 32)), "branch"),
     (dict(row_offset=torch.zeros(3, dtype=torch.int64)), "row_offset"),
     (dict(branch=bf(4, 64), h_out=torch.zeros(4, 64)), "h_out"),
@@ -269,3 +280,16 @@ def test_row_distance_of_views():
     assert S._row_ld(bf(1, 1, 61), "t") == 64             # a single row: any distance
     assert S._row_ld(bf(8, 64)[::2], "t") == 128
     assert np.int64(S._row_ld(None, "t")) == 0
+
+
+def test_segment_widths_are_read_at_every_call():
+    w = [torch.tensor(64), torch.tensor(64)]
+    assert S._segs(w, 128)[1].tolist() == [64, 64]
+    w[0] += 64
+    assert S._segs(w, 192)[1].tolist() == [128, 64]
+    assert S._segs(w, 192)[0].tolist() == [0, 128]
+
+
+def test_the_layer_s_calls_on_a_cpu_tensor():
+    with pytest.raises(ValueError, match="on a GPU"):
+        S.segquant_quantize_dualscale(bf(4, 64), torch.zeros(4, 1), [64])
