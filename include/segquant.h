@@ -199,7 +199,8 @@ int segquant_activate_quantize(const uint16_t *z_bf16, int64_t M, int64_t K, int
  *   act_kind    SEGQ_ACT_NONE, SEGQ_ACT_SILU or SEGQ_ACT_GELU
  *   act_scales, q_out, ld_q, q_layout, x_out, ld_xo
  *               the outputs of segquant_activate_quantize, K-segments over
- *               the C channels.  x_out may be z_bf16 when ld_xo = ld_z.
+ *               the C channels.  x_out may be z_bf16 when ld_xo = ld_z
+ *               (SEGQ_ERR_SHAPE where their rows overlap otherwise).
  *   workspace   device scratch, 16-byte aligned, of at least
  *               segquant_groupnorm_workspace_bytes() bytes (SEGQ_ERR_UNSUPPORTED
  *               with fewer), contents undefined afterwards; calls that share
@@ -239,7 +240,7 @@ size_t segquant_groupnorm_workspace_bytes(int64_t B, int64_t P, int64_t C, int32
  *   gate        optional, only with branch: device bf16 [n_req][ld_mod]
  *               (NULL: 1)
  *   h_out       optional, only with branch: device bf16 [M][ld_ho], h';
- *               may be h_bf16 when ld_ho = ld_h
+ *               may be h_bf16 when ld_ho = ld_h, or branch when ld_ho = ld_b
  *   gamma, beta device fp32 [K], each optional (NULL: 1 and 0)
  *   scale, shift  device bf16 [n_req][ld_mod], each optional (NULL: 0); scale,
  *               shift and gate share ld_mod: chunks of one layer's output
@@ -256,8 +257,9 @@ size_t segquant_groupnorm_workspace_bytes(int64_t B, int64_t P, int64_t C, int32
  *               be given if h_out is
  * One launch, no workspace.  Tensor pointers 16-byte aligned (row_offset 4),
  * ld_h, ld_b, ld_ho, ld_xo and ld_mod multiples of 8, ld_q of 16; K needs no
- * alignment; K-segment boundaries up to 4194240.  M may be 0.  Outputs other
- * than h_out must not overlap inputs.
+ * alignment; K-segment boundaries up to 4194240.  M may be 0.  Outputs must
+ * not overlap each other or, but for h_out as above, inputs: SEGQ_ERR_SHAPE
+ * where x_out or h_out does.
  */
 int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int64_t ld_h,
                               const uint16_t *branch, int64_t ld_b, const uint16_t *gate,
@@ -300,7 +302,9 @@ int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
  *               N-segments (host), boundaries multiples of 16
  *   base_bf16   optional device bf16 [M][ld_base]: the layer's output (NULL:
  *               0); may be y_bf16 when ld_base = ld_y, else apart from it
- *   y_bf16      device bf16 [M][ld_y]; must not overlap x, a or b
+ *               (SEGQ_ERR_SHAPE)
+ *   y_bf16      device bf16 [M][ld_y]; must not overlap x (SEGQ_ERR_SHAPE), a
+ *               or b
  *   workspace   device scratch, 16-byte aligned, of at least
  *               segquant_adapter_workspace_bytes() bytes (SEGQ_ERR_UNSUPPORTED
  *               with fewer), contents undefined afterwards; calls that share

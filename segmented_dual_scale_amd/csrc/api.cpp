@@ -377,6 +377,26 @@ static int check_rows(const uint16_t *p, int64_t ld, int64_t len, const char *wh
   return SEGQ_OK;
 }
 
+// Whether an output's rows share elements with another matrix's, M rows each.
+// Two matrices may stand side by side in one buffer, or be the same one where
+// `in_place` allows it: every element is then read before it is written.
+static bool rows_meet(const uint16_t *p, int64_t ld_p, int64_t w_p, const uint16_t *q, int64_t ld_q,
+                      int64_t w_q, int64_t M, bool in_place) {
+  if (!p || !q || (in_place && p == q && ld_p == ld_q)) return false;
+  typedef __int128 I;  // leading dimensions have no upper limit
+  const I d = (reinterpret_cast<intptr_t>(q) - reinterpret_cast<intptr_t>(p)) / 2;
+  if (d >= (I)(M - 1) * ld_p + w_p || d + (I)(M - 1) * ld_q + w_q <= 0) return false;
+  if (ld_p == ld_q) {
+    const I r = (d % ld_p + ld_p) % ld_p;
+    if (r >= w_p && r + w_q <= ld_p) return false;
+  }
+  for (int64_t i = 0; i < M; ++i) {  // the first row of q that ends behind row i's start
+    const I past = (I)i * ld_p - d - w_q, j = past < 0 ? 0 : past / ld_q + 1;
+    if (j < M && d + j * ld_q < (I)i * ld_p + w_p) return true;
+  }
+  return false;
+}
+
 static int check_norm_params(const float *gamma, const float *beta, float eps) {
   if (!(eps >= 1.17549435e-38f) || eps > 3.0e38f)
     return fail(SEGQ_ERR_SHAPE, "eps must be positive, finite and at least 2^-126");
@@ -443,6 +463,8 @@ int segquant_groupnorm_quantize(const uint16_t *z_bf16, int64_t B, int64_t P, in
                 "(segquant_groupnorm_workspace_bytes)", need);
   if (workspace && !aligned16(workspace))
     return fail(SEGQ_ERR_ALIGN, "workspace is not 16-byte aligned");
+  if (rows_meet(x_out, ld_xo, C, z_bf16, ld_z, C, M, true))
+    return fail(SEGQ_ERR_SHAPE, "x_out overlaps z_bf16");
   p.z = z_bf16;
   p.ld_z = ld_z;
   p.eps = eps;
@@ -488,6 +510,13 @@ int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
                            x_out, ld_xo, p.out)))
     return st;
   if (M == 0) return ok();
+  if (rows_meet(h_out, ld_ho, K, h_bf16, ld_h, K, M, true) ||
+      rows_meet(h_out, ld_ho, K, branch, ld_b, K, M, true))
+    return fail(SEGQ_ERR_SHAPE, "h_out overlaps h_bf16 or branch");
+  if (rows_meet(x_out, ld_xo, K, h_bf16, ld_h, K, M, false) ||
+      rows_meet(x_out, ld_xo, K, branch, ld_b, K, M, false) ||
+      rows_meet(x_out, ld_xo, K, h_out, ld_ho, K, M, false))
+    return fail(SEGQ_ERR_SHAPE, "x_out overlaps h_bf16, branch or h_out");
   p.h = h_bf16;
   p.M = M;
   p.K = K;
@@ -591,6 +620,10 @@ int segquant_adapter_add(int64_t M, int64_t N, int64_t K, const uint16_t *x_bf16
                 "adapters of this shape need a workspace of at least %zu bytes "
                 "(segquant_adapter_workspace_bytes)", need);
   if (!aligned16(workspace)) return fail(SEGQ_ERR_ALIGN, "workspace is not 16-byte aligned");
+  if (rows_meet(y_bf16, ld_y, N, x_bf16, ld_x, K, M, false))
+    return fail(SEGQ_ERR_SHAPE, "y_bf16 overlaps x_bf16");
+  if (rows_meet(y_bf16, ld_y, N, base_bf16, ld_base, N, M, true))
+    return fail(SEGQ_ERR_SHAPE, "y_bf16 overlaps base_bf16");
   p.x = x_bf16;
   p.ld_x = ld_x;
   p.row_offset = row_offset;

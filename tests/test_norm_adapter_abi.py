@@ -200,6 +200,50 @@ def test_adapter_workspace_bytes():
     assert "K" in S.segquant_last_error()
 
 
+B2 = 2  # bytes of a bf16 element
+ADANORM_APART = dict(M=8, K=64, q=None, h_out=0x30000, x=0x40000)
+
+
+@pytest.mark.parametrize("kw,status", [
+    # x_out one row, one 16-byte step, or one row's end into z
+    (dict(x=FAKE + 64 * B2, q=None), S.SEGQ_ERR_SHAPE),
+    (dict(x=FAKE + 8 * B2, q=None), S.SEGQ_ERR_SHAPE),
+    (dict(x=FAKE - 7 * 64 * B2, q=None), S.SEGQ_ERR_SHAPE),
+    (dict(x=FAKE + 64 * B2, ld_z=120, ld_xo=120, q=None), S.SEGQ_ERR_SHAPE),
+    (dict(x=FAKE + 7 * 64 * B2, ld_xo=1 << 40, q=None), S.SEGQ_ERR_SHAPE),
+])
+def test_groupnorm_outputs_that_overlap(kw, status):
+    assert groupnorm(**kw) == status and "overlaps" in S.segquant_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(h_out=FAKE + 64 * B2), dict(h_out=FAKE - 64 * B2), dict(x=FAKE), dict(x=0x30000),
+    dict(branch=0x50000, h_out=0x50000 + 64 * B2), dict(branch=0x50000, x=0x50000),
+    dict(branch=0x50000, h_out=0x50000, ld_ho=72),
+])
+def test_adanorm_outputs_that_overlap(kw):
+    assert adanorm(**{**ADANORM_APART, **kw}) == S.SEGQ_ERR_SHAPE
+    assert "overlaps" in S.segquant_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x=FAKE2), dict(x=FAKE2 + 7 * 64 * B2), dict(base=FAKE2 + 64 * B2),
+    dict(base=FAKE2 - 63 * 64 * B2, M=64), dict(x=FAKE2 + 64 * B2, ld_x=72, ld_y=128),
+    dict(x=FAKE2 + 64 * B2, ld_x=120, ld_y=120),
+])
+def test_adapter_outputs_that_overlap(kw):
+    assert adapter(**kw) == S.SEGQ_ERR_SHAPE and "overlaps" in S.segquant_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x=FAKE2 + 64 * B2, ld_x=128, ld_y=128),   # side by side in one buffer
+    dict(x=FAKE2 + 64 * B2, ld_x=72, ld_y=1024),   # between two rows
+    dict(x=FAKE2 + 8 * 64 * B2), dict(base=FAKE2), dict(x=FAKE2 - 8 * 64 * B2),
+])
+def test_outputs_beside_inputs_reach_the_launch(kw):
+    assert adapter(**kw) == S.SEGQ_ERR_HIP
+
+
 # The binding looks at its operands before it calls: these never reach a GPU.
 def bf(*shape):
     return torch.zeros(shape, dtype=torch.bfloat16)
