@@ -426,28 +426,34 @@ def segquant_gemm_w8a8_seg_noalloc(x, w_packed, w_scale, act_scales, out,
 @functools.lru_cache(maxsize=256)
 def _seg_arrays(widths: Tuple[int, ...]):
     off, wid = _seg_lists(widths)
-    return len(wid), off.ctypes.data, wid.ctypes.data, (off, wid)  # kept with their addresses
+    # the widths as a key, and the arrays that the addresses belong to
+    return len(wid), off.ctypes.data, wid.ctypes.data, widths, (off, wid)
 
 
 def _segments(widths, total: int):
     return _seg_arrays((total,) if widths is None else tuple(map(int, widths)))
 
 
-def _want(t, name: str, dtype, shape, device):
-    """Check an operand (None: not given) and return its address."""
+def _want(t, name: str, dtype, shape, at: int):
+    """Check an operand (None: not given; at: the GPU's index) and return its
+    address."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or t.device != device:
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.get_device() == at and t.shape == shape:
+        return t.data_ptr()
+    raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on the GPU of the first "
+                     f"operand ({at}), got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _want_array(t, name: str, dtype, shape, device):
+def _want_array(t, name: str, dtype, shape, at: int):
     """_want for an operand without a leading dimension of its own."""
-    if t is not None and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return _want(t, name, dtype, shape, device)
+    if t is None:
+        return None
+    if (t.dtype is dtype and t.get_device() == at and t.shape == shape and
+            t.is_contiguous()):
+        return t.data_ptr()
+    _want(t, name, dtype, shape, at)
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _row_ld(t, name: str) -> int:
@@ -487,15 +493,15 @@ def _mod_ld(rows: int, params, names: str) -> int:
     return ld or 0
 
 
-def _on(device, fn, *args):
-    """fn(*args, stream) on `device`'s current stream, with it current."""
+def _on(at: int, fn, *args):
+    """fn(*args, stream) on the current stream of GPU `at`, with it current."""
     import torch
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a GPU, got {device}")
-    stream = torch._C._cuda_getCurrentRawStream(device.index)  # current_stream() takes 2 us
-    if device.index == torch.cuda.current_device():
+    if at < 0:
+        raise ValueError("tensors must be on a GPU")
+    stream = torch._C._cuda_getCurrentRawStream(at)  # current_stream() takes 2 us
+    if at == torch._C._cuda_getDevice():
         return fn(*args, stream)
-    with torch.cuda.device(device):
+    with torch.cuda.device(at):
         return fn(*args, stream)
 
 
@@ -565,26 +571,26 @@ def segquant_groupnorm_quantize(z, groups: int, eps: float = 1e-5, gamma=None, b
     bf, f32 = torch.bfloat16, torch.float32
     if z.dim() != 3 or z.dtype is not bf:
         raise ValueError(f"z must be bfloat16 [B][P][C], got {z.dtype} {tuple(z.shape)}")
-    shape, dev = z.shape, z.device
+    shape, dev, at = z.shape, z.device, z.get_device()
     B, P, C = shape
     if x_out is True:
         x_out = torch.empty((B, P, -(-C // 8) * 8), dtype=bf, device=dev)[:, :, :C]
-    n, off, wid, _ = _segments(kseg, C)
+    n, off, wid, *_ = _segments(kseg, C)
     act = q = None
     ld_q = 0
     if act_scales is not None and want_codes:
-        act = _want_array(act_scales, "act_scales", f32, (4, n), dev)
+        act = _want_array(act_scales, "act_scales", f32, (4, n), at)
         out, q, ld_q = _codes_out(out, B * P, C, layout, dev, torch.empty)
     else:
         out = None
     workspace, ws, ws_bytes = _workspace(
         workspace, _groupnorm_bytes, (B, P, C, groups), dev)
-    _check(_on(dev, fn, z.data_ptr(), B, P, C, _row_ld(z, "z"), groups, eps,
-               _want_array(gamma, "gamma", f32, (C,), dev),
-               _want_array(beta, "beta", f32, (C,), dev),
-               _want(scale, "scale", bf, (B, C), dev), _want(shift, "shift", bf, (B, C), dev),
+    _check(_on(at, fn, z.data_ptr(), B, P, C, _row_ld(z, "z"), groups, eps,
+               _want_array(gamma, "gamma", f32, (C,), at),
+               _want_array(beta, "beta", f32, (C,), at),
+               _want(scale, "scale", bf, (B, C), at), _want(shift, "shift", bf, (B, C), at),
                _mod_ld(B, (scale, shift), "scale and shift"), act_kind, n, off, wid, act, q, ld_q, layout,
-               _want(x_out, "x_out", bf, shape, dev), _row_ld(x_out, "x_out"), ws, ws_bytes),
+               _want(x_out, "x_out", bf, shape, at), _row_ld(x_out, "x_out"), ws, ws_bytes),
            "segquant_groupnorm_quantize")
     return out, x_out
 
@@ -609,7 +615,7 @@ def segquant_adanorm_quantize(h, eps: float = 1e-6, gamma=None, beta=None, scale
     bf, f32 = torch.bfloat16, torch.float32
     if h.dim() != 2 or h.dtype is not bf:
         raise ValueError(f"h must be bfloat16 [M][K], got {h.dtype} {tuple(h.shape)}")
-    shape, dev = h.shape, h.device
+    shape, dev, at = h.shape, h.device, h.get_device()
     M, K = shape
     mod = scale if scale is not None else shift if shift is not None else gate
     if row_offset is not None:
@@ -623,31 +629,31 @@ def segquant_adanorm_quantize(h, eps: float = 1e-6, gamma=None, beta=None, scale
         x_out = new((M, -(-K // 8) * 8), dtype=bf, device=dev)[:, :K]
     if h_out is True:
         h_out = new((M, -(-K // 8) * 8), dtype=bf, device=dev)[:, :K]
-    n, off, wid, _ = _segments(kseg, K)
+    n, off, wid, *_ = _segments(kseg, K)
     act = q = None
     ld_q = 0
     if act_scales is not None and want_codes:
-        act = _want_array(act_scales, "act_scales", f32, (4, n), dev)
+        act = _want_array(act_scales, "act_scales", f32, (4, n), at)
         out, q, ld_q = _codes_out(out, M, K, layout, dev, new)
     else:
         out = None
     params = (n_req, K)
-    _check(_on(dev, fn, h.data_ptr(), M, K, _row_ld(h, "h"), _want(branch, "branch", bf, shape, dev),
-               _row_ld(branch, "branch"), _want(gate, "gate", bf, params, dev),
-               _want(h_out, "h_out", bf, shape, dev), _row_ld(h_out, "h_out"), eps,
-               _want_array(gamma, "gamma", f32, (K,), dev),
-               _want_array(beta, "beta", f32, (K,), dev),
-               _want(scale, "scale", bf, params, dev), _want(shift, "shift", bf, params, dev),
+    _check(_on(at, fn, h.data_ptr(), M, K, _row_ld(h, "h"), _want(branch, "branch", bf, shape, at),
+               _row_ld(branch, "branch"), _want(gate, "gate", bf, params, at),
+               _want(h_out, "h_out", bf, shape, at), _row_ld(h_out, "h_out"), eps,
+               _want_array(gamma, "gamma", f32, (K,), at),
+               _want_array(beta, "beta", f32, (K,), at),
+               _want(scale, "scale", bf, params, at), _want(shift, "shift", bf, params, at),
                _mod_ld(n_req, (scale, shift, gate), "scale, shift and gate"), n_req,
-               _want_array(row_offset, "row_offset", torch.int32, (n_req + 1,), dev), n, off, wid,
-               act, q, ld_q, layout, _want(x_out, "x_out", bf, shape, dev),
+               _want_array(row_offset, "row_offset", torch.int32, (n_req + 1,), at), n, off, wid,
+               act, q, ld_q, layout, _want(x_out, "x_out", bf, shape, at),
                _row_ld(x_out, "x_out")), "segquant_adanorm_quantize")
     return out, x_out, h_out
 
 
 def segquant_adapter_workspace_bytes(M: int, N: int, K: int, n_req: int, rank: int,
                                      nseg: Optional[Sequence[int]] = None) -> int:
-    n, off, wid, _ = _segments(nseg, N)
+    n, off, wid, *_ = _segments(nseg, N)
     return int(load_library().segquant_adapter_workspace_bytes(M, N, K, n_req, rank, n, off, wid))
 
 
@@ -673,23 +679,24 @@ def segquant_adapter_add(x, a, b, adapter, row_offset, base=None, alpha=None, ra
     bf, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, x.device
     if x.dim() != 2 or x.dtype is not bf or a.dim() != 3 or b.dim() != 3:
         raise ValueError("x must be bfloat16 [M][K], a and b 3-D")
+    at = x.get_device()
     M, K = x.shape
     n_adapters, N, r = b.shape
     n_req = adapter.numel()
-    n, off, wid, _ = _segments(nseg, N)
+    n, off, wid, widths, _ = _segments(nseg, N)
     y_shape = (M, N)
     if out is None:
         out = torch.zeros(y_shape, dtype=bf, device=dev)
     workspace, ws, ws_bytes = _workspace(
-        workspace, _adapter_bytes, (M, N, K, n_req, r, None if nseg is None else tuple(nseg)), dev)
-    _check(_on(dev, fn, M, N, K, x.data_ptr(), _row_ld(x, "x"), n_req,
-               _want_array(row_offset, "row_offset", i32, (n_req + 1,), dev),
-               _want_array(adapter, "adapter", i32, (n_req,), dev), n_adapters, r,
-               _want_array(rank, "rank", i32, (n_adapters,), dev),
-               _want_array(a, "a", bf, (n_adapters, n * r, K), dev),
-               _want_array(b, "b", bf, (n_adapters, N, r), dev),
-               _want_array(alpha, "alpha", f32, (n_adapters,), dev), n, off, wid,
-               _want(base, "base", bf, y_shape, dev), _row_ld(base, "base"),
-               _want(out, "out", bf, y_shape, dev), _row_ld(out, "out"), ws, ws_bytes),
+        workspace, _adapter_bytes, (M, N, K, n_req, r, widths), dev)
+    _check(_on(at, fn, M, N, K, x.data_ptr(), _row_ld(x, "x"), n_req,
+               _want_array(row_offset, "row_offset", i32, (n_req + 1,), at),
+               _want_array(adapter, "adapter", i32, (n_req,), at), n_adapters, r,
+               _want_array(rank, "rank", i32, (n_adapters,), at),
+               _want_array(a, "a", bf, (n_adapters, n * r, K), at),
+               _want_array(b, "b", bf, (n_adapters, N, r), at),
+               _want_array(alpha, "alpha", f32, (n_adapters,), at), n, off, wid,
+               _want(base, "base", bf, y_shape, at), _row_ld(base, "base"),
+               _want(out, "out", bf, y_shape, at), _row_ld(out, "out"), ws, ws_bytes),
            "segquant_adapter_add")
     return out
