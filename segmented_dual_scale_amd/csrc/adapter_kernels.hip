@@ -450,24 +450,37 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(AdapterProblem p) {
   if (t.rows == 0 || run.seg == p.ns.n || (t.adapter < 0 && p.base == p.y)) return;
   v4u *tv = reinterpret_cast<v4u *>(smem);
   Ex ex(p, t, run, smem + MT * RC * 1024);
-  ex.copy_b(ex.n0);
-  ex.first_base();
   int rank = 0;
   if (t.adapter >= 0) {
-    rank = rank_of(p, t.adapter);
+    // t first and all of it at once, then what is needed after it: loads come
+    // back in the order of their issue
+    constexpr int F = (MT * RC + 3) / 4;
     const int lane = threadIdx.x & 63;
-    for (int f = threadIdx.x >> 6; f < MT * RC; f += 4) {
-      const int64_t row = t.row0 + min(16 * (f / RC) + (lane >> 2), t.rows - 1);
-      const int block = (run.seg * p.rank) / 16 + f % RC;
-      v4f u[4];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    v4f u[F][4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {  // the parts of K that the shrink left
-        u[s] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        if (s < p.splits)
-          u[s] = *reinterpret_cast<const v4f *>(t_block(p, s, block) + row * 16 + 4 * (lane & 3));
+    for (int s = 0; s < 4; ++s) {  // the parts of K that the shrink left
+#pragma unroll
+      for (int i = 0; i < F; ++i) u[i][s] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      if (s < p.splits) {
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+          const int f = min(wave + 4 * i, MT * RC - 1);
+          const int64_t row = t.row0 + min(16 * (f / RC) + (lane >> 2), t.rows - 1);
+          u[i][s] = *reinterpret_cast<const v4f *>(
+              t_block(p, s, (run.seg * p.rank) / 16 + f % RC) + row * 16 + 4 * (lane & 3));
+        }
       }
-      store_operand(tv + 64 * f, (u[0] + u[1]) + (u[2] + u[3]));
     }
+    ex.copy_b(ex.n0);
+    ex.first_base();
+    rank = rank_of(p, t.adapter);
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+      if (wave + 4 * i < MT * RC)
+        store_operand(tv + 64 * (wave + 4 * i), (u[i][0] + u[i][1]) + (u[i][2] + u[i][3]));
+  } else {
+    ex.first_base();
   }
   __syncthreads();
   ex.columns(tv, rank);
