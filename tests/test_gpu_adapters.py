@@ -111,6 +111,9 @@ CASES = [
     ([500, 33], 4096 + 64, 400, [64, 336], 48, [1, 0], [48, 20]),
     ([5, 40], 128, 320, [16] * 20, 64, [1, 0], None),
     ([7] * 9, 64, 32, [32], 128, [i % 2 for i in range(9)], [128, 1]),
+    # whole tiles of rows and columns, several blocks of columns to a wave
+    *[([4000, 33, 64], 1536, 1536, [1536], r, [0, 1, -1], [r, r - 9]) for r in (16, 32, 48, 64)],
+    *[([8000, 70, 128], 4160, 1600, [64, 1536], r, [0, 1, -1], [r - 7, r]) for r in (16, 32, 48, 64)],
 ]
 
 
