@@ -69,19 +69,18 @@ __device__ __forceinline__ RowTile find_tile(const AdapterProblem &p, int tile) 
     hi = __builtin_amdgcn_readlane(next, r);
     id = __builtin_amdgcn_readlane(a, r);
   } else {
-    const int step = (n + 63) / 64;  // every step'th request, then those from there
-    int i = min(lane * step, n - 1);
-    const int before =
-        __popcll(__ballot(lane * step < n && first_of(offset(i), i) <= tile)) - 1;
-    if (before < 0) return {0, -1, 0};
-    const int base = before * step;
-    r = base - 1;
-    for (int k = 0; k < step; k += 64) {
-      i = min(base + k + lane, n - 1);
-      r += __popcll(
-          __ballot(k + lane < step && base + k + lane < n && first_of(offset(i), i) <= tile));
+    int base = 0, width = n, count;  // the request is one of base .. base + width - 1
+    for (;;) {  // every step'th of them, then those from the last that fits
+      const int step = (width + 63) / 64, i = base + min(lane * step, width - 1);
+      count = __popcll(__ballot(lane * step < width && first_of(offset(i), i) <= tile));
+      count = __builtin_amdgcn_readfirstlane(count);
+      if (count == 0) break;
+      base += (count - 1) * step;
+      width = min(step, width - (count - 1) * step);
+      if (step == 1) break;
     }
-    r = min(max(__builtin_amdgcn_readfirstlane(r), 0), n - 1);
+    if (base == 0 && count == 0) return {0, -1, 0};
+    r = base;
     lo = offset(r);
     hi = offset(r + 1);
     id = p.adapter[r];

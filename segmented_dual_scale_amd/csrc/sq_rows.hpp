@@ -126,9 +126,8 @@ __device__ __forceinline__ int div24(int x, int d) {
 // Request of a row in a packed batch: off[0..n] are row offsets, request i
 // holds rows off[i] .. off[i+1]-1.  req is the number of off[1..n] that are
 // <= row: -1 for a row before off[0], n behind off[n]; end is the first row
-// after the request.  One wave asks about one row: 64 offsets a step, after
-// one step over every (n/64)th where there are more.  Whatever off holds, only
-// off[0..n] is read.
+// after the request.  One wave asks about one row, 64 offsets a step, each step
+// leaving a 64th.  Whatever off holds, only off[0..n] is read.
 struct RowRequest {
   int32_t req;
   int64_t end;
@@ -137,18 +136,15 @@ struct RowRequest {
 __device__ __forceinline__ RowRequest find_request(const int32_t *off, int32_t n, int64_t row) {
   const int lane = threadIdx.x & 63;
   int base = 0, limit = n;  // off[1..base] <= row; off beyond limit > row
-  if (n > 64) {
-    const int step = (n + 63) / 64;
-    const int32_t v = off[min((lane + 1) * step, n)];
-    base = min(__popcll(__ballot(v <= row)) * step, n);
-    limit = min(base + step, n);
+  while (limit - base > 64) {
+    const int step = (limit - base + 63) / 64, at = base + (lane + 1) * step;
+    const int32_t v = off[min(at, limit)];
+    base += __popcll(__ballot(at <= limit && v <= row)) * step;
+    limit = min(base + step, limit);
   }
-  int req = base;
-  for (int i = base; i < limit; i += 64) {
-    const int at = i + 1 + lane;
-    const int32_t v = off[min(at, n)];
-    req += __popcll(__ballot(at <= limit && v <= row));
-  }
+  const int at = base + 1 + lane;
+  const int32_t v = off[min(at, limit)];
+  int req = base + __popcll(__ballot(at <= limit && v <= row));
   req = __builtin_amdgcn_readfirstlane(req);
   RowRequest r;
   r.end = off[min(req + 1, n)];

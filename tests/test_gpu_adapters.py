@@ -131,6 +131,25 @@ def test_adapter_add(lens, K, N, nseg, rank, ids, ranks):
     c.check(c.run(base=None), torch.zeros_like(again), base=False)
 
 
+@pytest.mark.parametrize("n_req,length", [(64 * 64 * 64 + 1, 1), (70001, 2), (5000, 40)])
+def test_very_many_requests(n_req, length):
+    """Three and four steps of the search for a tile's request; the formula for
+    all rows with each of the two adapters at a time."""
+    K, N, rank = 64, 32, 16
+    lens = [i % (length + 1) for i in range(n_req)]
+    c = Case([sum(lens)], K, N, [N], rank, [1], None)
+    c.off = offsets(lens)
+    c.adapter = torch.arange(n_req, device=DEV, dtype=torch.int32) % 5 % 2
+    y = c.run()
+    row_id = torch.repeat_interleave(c.adapter, torch.tensor(lens, device=DEV))
+    for i in (0, 1):
+        rows = row_id == i
+        one = Case.__new__(Case)
+        one.__dict__.update(c.__dict__, x=c.x[rows], base=c.base[rows], lens=[int(rows.sum())],
+                            ids=[i])
+        one.check(y[rows])
+
+
 def test_defaults_and_strided_rows():
     c = Case([40, 9], 128, 96, [96], 32, [1, 0])
     M = 49

@@ -234,6 +234,7 @@ ADA = [
     ([3, 0, 0, 5, 1], 9, 64, True, True),
     ([1] * 300, 300, 200, True, False),          # single rows, more requests than a wave
     ([2] * 3000, 6000, 72, False, True),         # many requests, several rows per wave
+    ([i % 3 for i in range(270000)], 270000, 24, False, False),  # three steps of the search
     ([20000, 1, 0, 9999], 30000, 520, True, False),
     ([260], 260, 4096, True, True),              # the most a wave holds
     ([50, 250], 300, 4099, True, True),          # past it, a short last piece
