@@ -645,21 +645,24 @@ int run_tiles_for(const AdapterProblem &p, int64_t rows, int64_t at_once) {
 // Whether the form in one launch is taken.  It saves a launch and t's way
 // through memory, and pays with one workgroup walking the whole of K and with
 // reading x and a once per run of columns.  One launch | two (us, MI355X, rank
-// 16, 32, 64):
+// 16, 32, 64; 1024 and 4096 rows in four requests, 8192 in eight; x from the
+// last-level cache):
 //   N 1536               K 1536                  K 3584                  K 6144
-//   64 requests of a row  6.1  7.5 10.2           8.2 10.7 15.4          10.5 14.2 21.1
-//                       | 7.8  8.6  9.1         | 8.4  9.2 10.2         | 8.7  9.7 11.3
-//   1024 rows             6.7  8.2 11.4           8.6 12.4 18.9          14.0 19.1 27.5
-//                      | 10.3 11.4 16.3        | 10.9 12.3 19.0        | 12.0 14.3 21.7
-//   4096 rows            12.8 14.4 17.6          15.9 17.5 21.1          19.1 21.1 25.6
-//                      | 14.4 17.5 22.6        | 18.5 20.7 27.1        | 21.8 23.8 32.9
+//   64 requests of a row  6.3  7.6  8.7           8.0  8.1 10.9           8.3  9.9 14.7
+//                       | 7.7  8.2  8.8         | 8.1  8.8  9.8         | 8.3  9.3 10.9
+//   1024 rows             6.5  7.8  9.1           7.8  9.8 13.8          12.3 13.8 19.4
+//                       | 9.3 10.2 14.9        | 10.1 11.5 17.7        | 11.3 12.8 20.1
+//   4096 rows            13.6 15.5 17.3          19.6 20.5 26.3          21.0 26.2 35.5
+//                      | 13.3 16.0 20.4        | 18.0 19.6 25.6        | 21.9 22.7 31.1
 //   N 4608, 3 segments
-//   8192 rows            38.8 42.2 59.6          54.0 59.5 80.1          78.6 84.5 112.9
-//                      | 41.1 45.0 59.2        | 47.2 52.9 73.4        | 60.9 70.3  99.5
+//   4096 rows            21.5 23.1 35.9          31.1 31.7 44.5          42.8 44.0 58.6
+//                      | 24.5 31.4 42.1        | 29.1 37.9 50.6        | 33.9 48.9 65.7
+//   8192 rows            38.4 41.3 57.7          55.3 58.8 78.6          76.5 84.8 110.1
+//                      | 39.4 47.3 57.1        | 46.0 58.0 71.0        | 67.2 78.7  96.9
 // So: K up to 4096, less for few rows of high rank, and x no more than the
 // caches hold: above, x comes from memory, which many short copies per
-// workgroup use less well (8192 rows, K 6144, rank 64, x from memory: 58
-// against 48 us, though 41 against 45 with x in the last-level cache).
+// workgroup use less well (8192 rows, K 6144, N 1536, rank 64, x from memory:
+// 58 against 47 us, though 41 against 49 with x in the last-level cache).
 bool in_one_launch(const AdapterProblem &p, bool few) {
   if (p.rank > 64) return false;
   if (few) return p.K <= (p.rank > 16 ? 2048 : 4096);
@@ -672,7 +675,8 @@ bool in_one_launch(const AdapterProblem &p, bool few) {
 // more than the time of one, or what all read of x and a from the caches at 13
 // TB/s, whichever is more.  64 requests, K 1536, six segments of 24 blocks,
 // rank 32: 15.6 us with runs of 12 (3 workgroups a CU), 17.9 with runs of 24;
-// 4096 rows, K 3584, N 1536, rank 64: 25.3 with runs of 12, 21.0 with one of 24.
+// 4096 rows of a request, K 3584, N 1536, rank 64: 24.2 with runs of 12, 19.7
+// with one of 24.
 int one_run_tiles(const AdapterProblem &p, bool few) {
   const int64_t tiles = few ? p.M : tile_bound(p, 16) - p.n_req / 2;  // about, not empty
   const double start = 3.0 + (p.K / 256.0) * (0.1 + 0.004 * p.rank);

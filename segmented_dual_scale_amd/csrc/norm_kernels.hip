@@ -834,7 +834,7 @@ namespace {
 // Bf16 outputs above this many bytes are stored past the caches: the 256 MB
 // last-level cache could not hold them for their reader, and their lines
 // would be written back during the next pass instead.  Group norm
-// 1024x1024x128 (268 MB out): 50 + 90 us for the two launches, against 73 +
+// 1024x1024x128 (268 MB out): 51 + 84 us for the two launches, against 73 +
 // 87 us with cached stores, whose write-back the next call's statistics pass
 // then waits for.
 constexpr int64_t kStreamBytes = 128 << 20;
