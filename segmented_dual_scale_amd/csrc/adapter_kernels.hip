@@ -249,17 +249,20 @@ __global__ __launch_bounds__(64 * WV) void adapter_shrink_kernel(AdapterProblem 
 }
 
 // ------------------------------------------------------------- expand ----
-// Four fp32 values as bf16: the upper halves of the fp32 words (hi), and what
-// they leave (lo).  x = hi + lo to 2^-15, so t enters the second product with
-// 16 bits of mantissa at the cost of a second matrix-core operand.
+// Four fp32 values as bf16: hi, the next value below in magnitude with a bf16's
+// bits, and lo, what that leaves.  x = hi + lo to 2^-15, so t enters the second
+// product with 16 bits of mantissa at the cost of a second matrix-core operand.
+// "Below" also where x itself is a bf16: neither part of a nonzero x is 0 then
+// and both have its sign, so an infinite factor gives x's infinity and not inf
+// + 0 inf = NaN (from |x| = 2^-110 up, where lo stays in bf16's range).  An
+// infinite x becomes the largest bf16 and infinity.
 __device__ __forceinline__ void split4(v4f f, v2u &hi, v2u &lo) {
   float h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t b = __float_as_uint(f[i]) & 0xffff0000u;
-    h[i] = __uint_as_float(b);
-    // an infinite t is all in hi: inf - inf would turn it into NaN
-    l[i] = (b & 0x7f800000u) == 0x7f800000u ? 0.0f : f[i] - h[i];
+    const uint32_t b = __float_as_uint(f[i]);
+    h[i] = __uint_as_float((b << 1 ? b - 1 : b) & 0xffff0000u);
+    l[i] = f[i] - h[i];
   }
   hi = v2u{cvt_bf16x2(h[0], h[1]), cvt_bf16x2(h[2], h[3])};
   lo = v2u{cvt_bf16x2(l[0], l[1]), cvt_bf16x2(l[2], l[3])};
