@@ -281,8 +281,8 @@ int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
  * N-segment j:
  *   t[q]    = alpha[i] * sum_k x[m][k] * a[i][j * rank + q][k]
  *   y[m][n] = bf16_rne( base[m][n] + sum_{q < rank_of[i]} t[q] * b[i][n][q] )
- * The products of bf16 values are summed in fp32; t is held to 16 bits or
- * more of mantissa.  An output-segmented layer [P1 SegLinear, pattern one]
+ * The products of bf16 values are summed in fp32 and t is an fp32 value (where
+ * it is below 2^-110 in magnitude it loses bits, as in bf16).  An output-segmented layer [P1 SegLinear, pattern one]
  * has one pair of factors per N-segment; a single segment is the usual
  * low-rank adapter.
  *   x_bf16      device bf16 [M][ld_x]: the layer's input before quantisation

@@ -249,22 +249,27 @@ __global__ __launch_bounds__(64 * WV) void adapter_shrink_kernel(AdapterProblem 
 }
 
 // ------------------------------------------------------------- expand ----
-// Four fp32 values as bf16: hi, the next value below in magnitude with a bf16's
-// bits, and lo, what that leaves.  x = hi + lo to 2^-15, so t enters the second
-// product with 16 bits of mantissa at the cost of a second matrix-core operand.
-// "Below" also where x itself is a bf16: neither part of a nonzero x is 0 then
-// and both have its sign, so an infinite factor gives x's infinity and not inf
-// + 0 inf = NaN (from |x| = 2^-110 up, where lo stays in bf16's range).  An
-// infinite x becomes the largest bf16 and infinity.
-__device__ __forceinline__ void split4(v4f f, v2u &hi, v2u &lo) {
-  float h[4], l[4];
+// Four fp32 values as bf16 parts whose sum they are: hi, the next value below in
+// magnitude with a bf16's bits, mid, the next below what hi leaves, and lo, the
+// eight bits that remain, so t enters the second product as it is, at the cost
+// of matrix-core operands.  "Below" also where x itself is a bf16: no part of a
+// nonzero x is 0 then and all have its sign, so an infinite factor gives x's
+// infinity and not inf + 0 inf = NaN (from |x| = 2^-110 up, where lo stays in
+// bf16's range).  An infinite x becomes two largest bf16 and infinity.
+__device__ __forceinline__ void split4(v4f f, v2u &hi, v2u &mid, v2u &lo) {
+  auto below = [](float x) {
+    const uint32_t b = __float_as_uint(x);
+    return __uint_as_float((b << 1 ? b - 1 : b) & 0xffff0000u);
+  };
+  float h[4], m[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t b = __float_as_uint(f[i]);
-    h[i] = __uint_as_float((b << 1 ? b - 1 : b) & 0xffff0000u);
-    l[i] = f[i] - h[i];
+    h[i] = below(f[i]);
+    m[i] = below(f[i] - h[i]);
+    l[i] = f[i] - h[i] - m[i];
   }
   hi = v2u{cvt_bf16x2(h[0], h[1]), cvt_bf16x2(h[2], h[3])};
+  mid = v2u{cvt_bf16x2(m[0], m[1]), cvt_bf16x2(m[2], m[3])};
   lo = v2u{cvt_bf16x2(l[0], l[1]), cvt_bf16x2(l[2], l[3])};
 }
 
@@ -290,22 +295,44 @@ __device__ __forceinline__ ColRun find_run(const NSegEnds &ns, int run, int per_
   return c;
 }
 
-// Four ranks of a row of t (lane l of a wave: row l/4, ranks 4 (l%4) .. +3 of a
-// 16 x 16 block) as the matrix-core operand of the block: lane 16 c + row holds
-// the hi halves of ranks 8c .. +7, and the lo halves 32 lanes on.
-__device__ __forceinline__ void store_operand(v4u *op, v4f v) {
-  const int lane = threadIdx.x & 63;
-  v2u hi, lo;
-  split4(v, hi, lo);
-  v2u *to = reinterpret_cast<v2u *>(op) + 2 * (16 * ((lane & 3) >> 1) + (lane >> 2)) + (lane & 1);
-  to[0] = hi;
-  to[64] = lo;
-}
+// A row block's t in LDS as matrix-core operands, RC blocks of 16 ranks: two
+// blocks make an operand each of hi, mid and lo parts, a block left alone one of
+// hi and mid and one of lo parts and zeros.
+template <int RC>
+struct TOperands {
+  static constexpr int kPairs = RC / 2, kB = (RC + 1) / 2;  // operands of B
+  static constexpr bool kAlone = RC % 2;
+  static constexpr int kAll = 3 * kPairs + 2 * kAlone;
+
+  // Four ranks of a row (lane l of a wave: row l/4, ranks 4 (l%4) .. +3) of
+  // block e: lane 16 c + row of an operand holds the contracted values 8c .. +7.
+  static __device__ __forceinline__ void store(v4u *op, int e, v4f v) {
+    const int lane = threadIdx.x & 63;
+    v2u hi, mid, lo;
+    split4(v, hi, mid, lo);
+    v2u *to = reinterpret_cast<v2u *>(op + 64 * 3 * (e / 2)) +
+              2 * (16 * ((lane & 3) >> 1) + (lane >> 2)) + (lane & 1);
+    if (kAlone && e == RC - 1) {
+      to[0] = hi;
+      to[64] = mid;
+      to[128] = lo;
+      to[192] = v2u{0u, 0u};
+    } else {
+      to += 64 * (e & 1);
+      to[0] = hi;
+      to[128] = mid;
+      to[256] = lo;
+    }
+  }
+};
 
 // The second product for a workgroup's rows and a run of columns.  t stands in
 // LDS as matrix-core operands; the four waves take the run's blocks of 64
-// columns in turn.  16 ranks fill one instruction: its 32 contracted values
-// are t's hi then lo halves against the 16 values of B twice.  A block's B (RC
+// columns in turn.  32 ranks take three instructions, one for each part of t
+// against the same operand of B, and 16 ranks alone two: hi and mid parts
+// against the 16 values of B twice, lo parts against them and zeros.  (Both
+// launches, 8192 x 1536, rank 64, K 6144: 48.4 us; t in two parts, which holds 16
+// bits of it, 47.6; an operand of B for every 16 ranks 56.4.)  A block's B (RC
 // blocks of 16 ranks) is 2 RC KiB of contiguous memory, copied to LDS with
 // chunk c of column n at place c ^ f(n), and held in registers for all rows,
 // so the next block's copy runs under this one's products; its base is loaded
@@ -318,6 +345,7 @@ __device__ __forceinline__ int b_place(int chunk, int col) {
 
 template <int MT, int RC>
 struct Expand {
+  using Ops = TOperands<RC>;
   static constexpr int kB = 2048 * RC;        // bytes of a block's B, per wave
   static constexpr int kOut = 16 * 68 * 4;    // 16 rows of 64 columns, padded, per wave
   static constexpr int kBytes = 4 * (kB + kOut);
@@ -383,9 +411,12 @@ struct Expand {
   __device__ __forceinline__ void columns_of(const v4u *tv, int rank) {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int orow = lane >> 3, ocol = 8 * (lane & 7);  // this lane's place in a row of y
+    const uint32_t lower = g < 2 ? ~0u : 0u;  // not against the zeros
     for (bool first = true; n0 < run.end; n0 += 256, first = false) {
       const bool more = n0 + 256 < run.end;
-      v4u b[RC][4];
+      v4u b[Ops::kB][4];
+      // this lane's first rank of operand q of B
+      auto rank_at = [&](int q) { return 32 * q + 8 * (q < Ops::kPairs ? g : g & 1); };
       if (t.adapter >= 0) {
         // vector-memory operations end in the order of their issue, and a whole
         // tile issues its 2 MT stores of y behind the copy of the next B: the
@@ -396,25 +427,26 @@ struct Expand {
         else
           wait_copies<0>();
 #pragma unroll
-        for (int e = 0; e < RC; ++e)
+        for (int q = 0; q < Ops::kB; ++q)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int n = 16 * j + r;
-            b[e][j] = *reinterpret_cast<const v4u *>(b_lds + 32 * RC * n +
-                                                     16 * b_place<RC>(2 * e + (g & 1), n));
+            b[q][j] = *reinterpret_cast<const v4u *>(b_lds + 32 * RC * n +
+                                                     16 * b_place<RC>(rank_at(q) / 8, n));
           }
         __builtin_amdgcn_s_waitcnt(0xc07f);  // the reads are done: the buffer is free
         __builtin_amdgcn_sched_barrier(0);
         copy_b(n0 + 256);
 #pragma unroll
-        for (int e = 0; e < RC; ++e) {
-          if (16 * e + 16 > rank) {  // what is stored past an adapter's rank is not used
+        for (int q = 0; q < Ops::kB; ++q) {
+          if (32 * q + (q < Ops::kPairs ? 32 : 16) > rank) {
+            // what is stored past an adapter's rank is not used
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int at = 16 * e + 8 * (g & 1) + 2 * q;
-                b[e][j][q] = at + 1 < rank ? b[e][j][q] : at < rank ? b[e][j][q] & 0xffffu : 0u;
+              for (int w = 0; w < 4; ++w) {
+                const int at = rank_at(q) + 2 * w;
+                b[q][j][w] = at + 1 < rank ? b[q][j][w] : at < rank ? b[q][j][w] & 0xffffu : 0u;
               }
           }
         }
@@ -428,10 +460,16 @@ struct Expand {
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int e = 0; e < RC; ++e) {
-            const v4u tf = tv[(i * RC + e) * 64 + lane];
+          for (int q = 0; q < Ops::kB; ++q) {
+            const v4u *tq = tv + (i * Ops::kAll + 3 * q) * 64 + lane;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[j] = mfma(b[e][j], tf, acc[j]);
+            for (int part = q < Ops::kPairs ? 2 : 1; part >= 0; --part) {
+              const v4u tf = tq[64 * part];
+              const bool half = q == Ops::kPairs && part == 1;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                acc[j] = mfma(half ? b[q][j] & lower : b[q][j], tf, acc[j]);
+            }
           }
           __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -463,12 +501,14 @@ struct Expand {
 template <int MT, int RC>
 __global__ __launch_bounds__(256) void adapter_expand_kernel(AdapterProblem p) {
   using Ex = Expand<MT, RC>;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[MT * RC * 1024 + Ex::kBytes];
+  using Ops = TOperands<RC>;
+  constexpr int kOps = MT * Ops::kAll * 1024;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kOps + Ex::kBytes];
   const ColRun run = find_run(p.ns, blockIdx.y, p.run_tiles);
   const RowTile t = find_tile<16 * MT>(p, blockIdx.x);
   if (t.rows == 0 || run.seg == p.ns.n || (t.adapter < 0 && p.base == p.y)) return;
   v4u *tv = reinterpret_cast<v4u *>(smem);
-  Ex ex(p, t, run, smem + MT * RC * 1024);
+  Ex ex(p, t, run, smem + kOps);
   int rank = 0;
   if (t.adapter >= 0) {
     // t first and all of it at once, then what is needed after it: loads come
@@ -495,9 +535,12 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(AdapterProblem p) {
     ex.first_base();
     rank = rank_of(p, t.adapter);
 #pragma unroll
-    for (int i = 0; i < F; ++i)
-      if (wave + 4 * i < MT * RC)
-        store_operand(tv + 64 * (wave + 4 * i), (u[i][0] + u[i][1]) + (u[i][2] + u[i][3]));
+    for (int i = 0; i < F; ++i) {
+      const int f = wave + 4 * i;
+      if (f < MT * RC)
+        Ops::store(tv + 64 * Ops::kAll * (f / RC), f % RC,
+                   (u[i][0] + u[i][1]) + (u[i][2] + u[i][3]));
+    }
   } else {
     ex.first_base();
   }
@@ -514,8 +557,9 @@ template <int MT, int RC>
 __global__ __launch_bounds__(256) void adapter_one_kernel(AdapterProblem p) {
   using Sh = Shrink<MT, RC, 4>;
   using Ex = Expand<MT, RC>;
+  using Ops = TOperands<RC>;
   // the copies' buffers become the sums, B and the output rows, the operands
-  constexpr int kOperands = Sh::kSums + Ex::kBytes, kAfter = kOperands + MT * RC * 1024;
+  constexpr int kOperands = Sh::kSums + Ex::kBytes, kAfter = kOperands + MT * Ops::kAll * 1024;
   __shared__ __attribute__((aligned(1024))) uint8_t
       smem[Sh::kBytes > kAfter ? Sh::kBytes : kAfter];
   const ColRun run = find_run(p.ns, blockIdx.y, p.run_tiles);
@@ -533,7 +577,8 @@ __global__ __launch_bounds__(256) void adapter_one_kernel(AdapterProblem p) {
     Sh::gather(acc, smem);
     ex.copy_b(ex.n0);  // behind the sums, under the making of the operands
     for (int f = threadIdx.x >> 6; f < MT * RC; f += 4)
-      store_operand(tv + 64 * f, Sh::block(smem, f, 16 * (f % RC), rank, alpha));
+      Ops::store(tv + 64 * Ops::kAll * (f / RC), f % RC,
+                 Sh::block(smem, f, 16 * (f % RC), rank, alpha));
     __syncthreads();
   }
   ex.columns(tv, rank);
@@ -569,7 +614,7 @@ __global__ __launch_bounds__(256) void adapter_expand_wide_kernel(AdapterProblem
     for (int i = 0; i < MT; ++i)
       tp[i] = (t.row0 + min(16 * i + r, t.rows - 1)) * 16 + k;
     for (int c = 0; c < rank; c += 16) {
-      v4u b[4], tv[MT];
+      v4u b[4], tv[MT], tl[MT];
 #pragma unroll
       for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const v4u *>(bp[j] + c);
 #pragma unroll
@@ -580,10 +625,11 @@ __global__ __launch_bounds__(256) void adapter_expand_wide_kernel(AdapterProblem
           u += *reinterpret_cast<const v4f *>(q);
           v += *reinterpret_cast<const v4f *>(q + 4);
         }
-        v2u h0, h1, l0, l1;
-        split4(u, h0, l0);
-        split4(v, h1, l1);
-        tv[i] = g >= 2 ? v4u{l0[0], l0[1], l1[0], l1[1]} : v4u{h0[0], h0[1], h1[0], h1[1]};
+        v2u h0, h1, m0, m1, l0, l1;
+        split4(u, h0, m0, l0);
+        split4(v, h1, m1, l1);
+        tv[i] = g >= 2 ? v4u{m0[0], m0[1], m1[0], m1[1]} : v4u{h0[0], h0[1], h1[0], h1[1]};
+        tl[i] = g >= 2 ? v4u{0u, 0u, 0u, 0u} : v4u{l0[0], l0[1], l1[0], l1[1]};
       }
       if (c + 16 > rank) {  // what is stored past an adapter's rank is not used
 #pragma unroll
@@ -597,7 +643,11 @@ __global__ __launch_bounds__(256) void adapter_expand_wide_kernel(AdapterProblem
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mfma(b[j], tv[i], acc[i][j]);
+        for (int j = 0; j < 4; ++j) {
+          // the lo parts fill half an instruction: zeros against the other half
+          acc[i][j] = mfma(b[j] & (g < 2 ? ~0u : 0u), tl[i], acc[i][j]);
+          acc[i][j] = mfma(b[j], tv[i], acc[i][j]);
+        }
     }
   }
 #pragma unroll

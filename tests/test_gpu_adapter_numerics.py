@@ -73,3 +73,31 @@ def test_infinite_factors_give_the_formula_s_infinities(lens, K, rank):
     assert torch.equal(y.isnan(), ref.isnan())
     assert torch.equal(y.isinf(), ref.isinf())
     assert torch.equal(y[ref.isinf()], ref[ref.isinf()])
+
+
+@pytest.mark.parametrize("lens,K,rank", FORMS)
+def test_t_keeps_its_24_bits(lens, K, rank):
+    """Every y is one product t b and a base that cancels its upper bits, so
+    what t loses shows.  t = x0 a0 + x1 a1 in fp32 is off by 2^-24 of |x0 a0| + |x1
+    a1| (a sum, its parts exact), and so is its product with b; the sum of t's
+    parts against b, and the base, by at most 8 2^-24 of |t b| + |base| (at most
+    four terms that are not 0, alignment inside an instruction); y rounds at
+    2^-8."""
+    M, N = sum(lens), 3 * 80
+    g = gen(rank * K + 1)
+    x = torch.zeros(M, K, device=DEV, dtype=BF)
+    x[:, [1, 40]] = torch.randn(M, 2, generator=g, device=DEV).to(BF)
+    a = torch.zeros(1, rank, K, device=DEV, dtype=BF)
+    a[:, :, [1, 40]] = torch.randn(1, rank, 2, generator=g, device=DEV).to(BF)
+    b = torch.zeros(1, N, rank, device=DEV, dtype=BF)
+    n = torch.arange(N, device=DEV)
+    b[0, n, n % rank] = torch.randn(N, generator=g, device=DEV).to(BF)
+    parts = x[:, None, [1, 40]].double() * a[:, :, [1, 40]].double()  # [M][rank][2]
+    pick = b[0, n, n % rank].double()
+    tb = parts.sum(-1)[:, n % rank] * pick
+    U = parts.abs().sum(-1)[:, n % rank] * pick.abs()
+    base = (-tb).to(BF)
+    ref = base.double() + tb
+    err = (call(x, a, b, lens, base=base).double() - ref).abs()
+    tol = 2.0 ** -8 * ref.abs() + 2.0 ** -24 * (U + 8 * (tb.abs() + base.double().abs()))
+    assert (err <= tol).all(), float((err / tol).max())
