@@ -532,9 +532,9 @@ __device__ __forceinline__ v4u gn_apply8(v4u z, const GnAffine &f) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     v[j] = __builtin_fmaf(v[j] - f.mu[j], f.a[j], f.b[j]);
-    if (ACT == 1) v[j] = silu_hw(v[j]);
     if (ACT == 2) v[j] = gelu_hw(v[j]);
   }
+  if (ACT == 1) silu8_hw(v);
   return pack8(v);
 }
 
