@@ -196,7 +196,10 @@ int segquant_activate_quantize(const uint16_t *z_bf16, int64_t M, int64_t K, int
  *   scale, shift  device bf16 [B][ld_mod], each optional (NULL: 0): two chunks
  *               of a conditioning layer's output as they are, ld_mod its
  *               leading dimension (ignored when both are NULL)
- *   act_kind    SEGQ_ACT_NONE, SEGQ_ACT_SILU or SEGQ_ACT_GELU
+ *   act_kind    SEGQ_ACT_NONE, SEGQ_ACT_SILU or SEGQ_ACT_GELU.  act(t) is
+ *               within 2^-17 of its true value, relative, down to 2^-125
+ *               (segquant_activate_quantize: 2^-19), so the two calls may
+ *               round to neighbouring bf16 values
  *   act_scales, q_out, ld_q, q_layout, x_out, ld_xo
  *               the outputs of segquant_activate_quantize, K-segments over
  *               the C channels.  x_out may be z_bf16 when ld_xo = ld_z

@@ -22,7 +22,11 @@ def silu(v):
     return v / (1 + torch.exp(-v))
 
 
-ACTS = {"silu": (S.SEGQ_ACT_SILU, silu, 128.0)}
+def gelu(v):
+    return v / 2 * torch.erfc(-v / math.sqrt(2.0))
+
+
+ACTS = {"silu": (S.SEGQ_ACT_SILU, silu, 128.0), "gelu": (S.SEGQ_ACT_GELU, gelu, 14.0)}
 
 
 def through_the_norm(t, kind):

@@ -11,7 +11,7 @@ import pytest
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 SRC = os.path.join(HERE, "numerics", "norm_activation_sweep.c")
-FUNCTIONS = 1
+FUNCTIONS = 2
 
 
 @pytest.mark.skipif(shutil.which("gcc") is None, reason="needs a C compiler")
