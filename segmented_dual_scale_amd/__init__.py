@@ -539,8 +539,8 @@ def _codes_out(out, M: int, K: int, layout: int, device, new):
                          f"{out.device}")
     ld = _row_ld(out[0] if planes else out, "out")
     if M <= 1:
-        ld = out.stride(0) if planes else (out.shape[-1] + 15) // 16 * 16
-    if planes and out.stride(0) != M * ld:
+        ld = out.stride(0) if planes and M else (out.shape[-1] + 15) // 16 * 16
+    if planes and M and out.stride(0) != M * ld:
         raise ValueError("out: the second plane must follow the first")
     return out, out.data_ptr(), ld
 
