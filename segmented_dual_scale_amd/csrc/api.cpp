@@ -377,24 +377,73 @@ static int check_rows(const uint16_t *p, int64_t ld, int64_t len, const char *wh
   return SEGQ_OK;
 }
 
-// Whether an output's rows share elements with another matrix's, M rows each.
-// Two matrices may stand side by side in one buffer, or be the same one where
-// `in_place` allows it: every element is then read before it is written.
-static bool rows_meet(const uint16_t *p, int64_t ld_p, int64_t w_p, const uint16_t *q, int64_t ld_q,
-                      int64_t w_q, int64_t M, bool in_place) {
-  if (!p || !q || (in_place && p == q && ld_p == ld_q)) return false;
-  typedef __int128 I;  // leading dimensions have no upper limit
-  const I d = (reinterpret_cast<intptr_t>(q) - reinterpret_cast<intptr_t>(p)) / 2;
-  if (d >= (I)(M - 1) * ld_p + w_p || d + (I)(M - 1) * ld_q + w_q <= 0) return false;
-  if (ld_p == ld_q) {
-    const I r = (d % ld_p + ld_p) % ld_p;
-    if (r >= w_p && r + w_q <= ld_p) return false;
+typedef __int128 I128;  // leading dimensions have no upper limit
+
+static I128 floor_div(I128 a, I128 b) {  // b > 0
+  return a / b - (a % b < 0 ? 1 : 0);
+}
+
+// Sum of floor((a i + b) / m) over 0 <= i < n, for a, b >= 0 and m > 0: whole
+// multiples of m taken out, then the same count seen along the other axis, as
+// in Euclid's algorithm.  Modulo 2^128.
+static unsigned __int128 floor_sum(unsigned __int128 n, unsigned __int128 m, unsigned __int128 a,
+                                   unsigned __int128 b) {
+  unsigned __int128 sum = 0;
+  while (n > 0) {
+    sum += (n % 2 ? (n - 1) / 2 * n : n / 2 * (n - 1)) * (a / m) + n * (b / m);
+    const unsigned __int128 top = a % m * n + b % m;
+    n = top / m;
+    b = top % m;
+    const unsigned __int128 t = m;
+    m = a % m;
+    a = t;
+    if (!m) break;
   }
-  for (int64_t i = 0; i < M; ++i) {  // the first row of q that ends behind row i's start
-    const I past = (I)i * ld_p - d - w_q, j = past < 0 ? 0 : past / ld_q + 1;
-    if (j < M && d + j * ld_q < (I)i * ld_p + w_p) return true;
-  }
-  return false;
+  return sum;
+}
+
+// Rows of `width` bytes, `ld` bytes apart.
+struct Rows {
+  const void *at;
+  I128 ld, width;
+  int64_t n;
+};
+
+static Rows bf16_rows(const uint16_t *p, int64_t ld, int64_t width, int64_t n) {
+  return {p, 2 * (I128)ld, 2 * (I128)width, n};
+}
+
+// Whether two matrices share bytes; they may stand side by side in one buffer.
+// Rows i and j share some where 0 < i ld_p - d + w_p - j ld_q < w_p + w_q.  The
+// number of steps grows as the logarithm of the leading dimensions.
+static bool rows_meet(const Rows &p, const Rows &q) {
+  if (!p.at || !q.at || p.n < 1 || q.n < 1) return false;
+  const I128 d = (I128)reinterpret_cast<uintptr_t>(q.at) - (I128)reinterpret_cast<uintptr_t>(p.at);
+  const I128 q_end = d + (q.n - 1) * q.ld;  // q's last row
+  if (d >= (p.n - 1) * p.ld + p.width || q_end + q.width <= 0) return false;
+  // the rows of p that meet a row of q at `at`
+  auto met = [&](I128 at) {
+    I128 first = floor_div(at - p.width, p.ld) + 1, last = floor_div(at + q.width - 1, p.ld);
+    if (first < 0) first = 0;
+    if (last > p.n - 1) last = p.n - 1;
+    return first <= last;
+  };
+  if (met(d) || met(q_end)) return true;
+  // any other meeting is with rows of p between these two, where the rows j of
+  // q that row i meets are counted without a look at q's ends
+  I128 first = floor_div(d + q.width - 1, p.ld) + 1, last = floor_div(q_end - p.width, p.ld);
+  if (first < 0) first = 0;
+  if (last > p.n - 1) last = p.n - 1;
+  if (first > last) return false;
+  const I128 start = first * p.ld - d, a = p.ld % q.ld;
+  return floor_sum(last - first + 1, q.ld, a, start + p.width - 1) !=
+         floor_sum(last - first + 1, q.ld, a, start - q.width);
+}
+
+// The same for an output that may be the input itself: every element is then
+// read before it is written.
+static bool rows_meet_apart(const Rows &out, const Rows &in) {
+  return !(out.at == in.at && out.ld == in.ld) && rows_meet(out, in);
 }
 
 static int check_norm_params(const float *gamma, const float *beta, float eps) {
@@ -463,7 +512,7 @@ int segquant_groupnorm_quantize(const uint16_t *z_bf16, int64_t B, int64_t P, in
                 "(segquant_groupnorm_workspace_bytes)", need);
   if (workspace && !aligned16(workspace))
     return fail(SEGQ_ERR_ALIGN, "workspace is not 16-byte aligned");
-  if (rows_meet(x_out, ld_xo, C, z_bf16, ld_z, C, M, true))
+  if (rows_meet_apart(bf16_rows(x_out, ld_xo, C, M), bf16_rows(z_bf16, ld_z, C, M)))
     return fail(SEGQ_ERR_SHAPE, "x_out overlaps z_bf16");
   p.z = z_bf16;
   p.ld_z = ld_z;
@@ -510,12 +559,11 @@ int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
                            x_out, ld_xo, p.out)))
     return st;
   if (M == 0) return ok();
-  if (rows_meet(h_out, ld_ho, K, h_bf16, ld_h, K, M, true) ||
-      rows_meet(h_out, ld_ho, K, branch, ld_b, K, M, true))
+  const Rows h = bf16_rows(h_bf16, ld_h, K, M), br = bf16_rows(branch, ld_b, K, M);
+  const Rows ho = bf16_rows(h_out, ld_ho, K, M), xo = bf16_rows(x_out, ld_xo, K, M);
+  if (rows_meet_apart(ho, h) || rows_meet_apart(ho, br))
     return fail(SEGQ_ERR_SHAPE, "h_out overlaps h_bf16 or branch");
-  if (rows_meet(x_out, ld_xo, K, h_bf16, ld_h, K, M, false) ||
-      rows_meet(x_out, ld_xo, K, branch, ld_b, K, M, false) ||
-      rows_meet(x_out, ld_xo, K, h_out, ld_ho, K, M, false))
+  if (rows_meet(xo, h) || rows_meet(xo, br) || rows_meet(xo, ho))
     return fail(SEGQ_ERR_SHAPE, "x_out overlaps h_bf16, branch or h_out");
   p.h = h_bf16;
   p.M = M;
@@ -620,9 +668,10 @@ int segquant_adapter_add(int64_t M, int64_t N, int64_t K, const uint16_t *x_bf16
                 "adapters of this shape need a workspace of at least %zu bytes "
                 "(segquant_adapter_workspace_bytes)", need);
   if (!aligned16(workspace)) return fail(SEGQ_ERR_ALIGN, "workspace is not 16-byte aligned");
-  if (rows_meet(y_bf16, ld_y, N, x_bf16, ld_x, K, M, false))
+  const Rows y = bf16_rows(y_bf16, ld_y, N, M);
+  if (rows_meet(y, bf16_rows(x_bf16, ld_x, K, M)))
     return fail(SEGQ_ERR_SHAPE, "y_bf16 overlaps x_bf16");
-  if (rows_meet(y_bf16, ld_y, N, base_bf16, ld_base, N, M, true))
+  if (rows_meet_apart(y, bf16_rows(base_bf16, ld_base, N, M)))
     return fail(SEGQ_ERR_SHAPE, "y_bf16 overlaps base_bf16");
   p.x = x_bf16;
   p.ld_x = ld_x;
