@@ -203,7 +203,8 @@ int segquant_activate_quantize(const uint16_t *z_bf16, int64_t M, int64_t K, int
  *   act_scales, q_out, ld_q, q_layout, x_out, ld_xo
  *               the outputs of segquant_activate_quantize, K-segments over
  *               the C channels.  x_out may be z_bf16 when ld_xo = ld_z
- *               (SEGQ_ERR_SHAPE where their rows overlap otherwise).
+ *               (outputs and workspace must not overlap each other or an
+ *               input otherwise: SEGQ_ERR_SHAPE).
  *   workspace   device scratch, 16-byte aligned, of at least
  *               segquant_groupnorm_workspace_bytes() bytes (SEGQ_ERR_UNSUPPORTED
  *               with fewer), contents undefined afterwards; calls that share
@@ -261,8 +262,7 @@ size_t segquant_groupnorm_workspace_bytes(int64_t B, int64_t P, int64_t C, int32
  * One launch, no workspace.  Tensor pointers 16-byte aligned (row_offset 4),
  * ld_h, ld_b, ld_ho, ld_xo and ld_mod multiples of 8, ld_q of 16; K needs no
  * alignment; K-segment boundaries up to 4194240.  M may be 0.  Outputs must
- * not overlap each other or, but for h_out as above, inputs: SEGQ_ERR_SHAPE
- * where x_out or h_out does.
+ * not overlap each other or, but for h_out as above, inputs: SEGQ_ERR_SHAPE.
  */
 int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int64_t ld_h,
                               const uint16_t *branch, int64_t ld_b, const uint16_t *gate,
@@ -304,10 +304,10 @@ int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
  *   n_nseg, nseg_offset, nseg_width
  *               N-segments (host), boundaries multiples of 16
  *   base_bf16   optional device bf16 [M][ld_base]: the layer's output (NULL:
- *               0); may be y_bf16 when ld_base = ld_y, else apart from it
- *               (SEGQ_ERR_SHAPE)
- *   y_bf16      device bf16 [M][ld_y]; must not overlap x (SEGQ_ERR_SHAPE), a
- *               or b
+ *               0); may be y_bf16 when ld_base = ld_y
+ *   y_bf16      device bf16 [M][ld_y]; y_bf16 and the workspace must not
+ *               overlap each other or, but for base_bf16 as above, an input:
+ *               SEGQ_ERR_SHAPE
  *   workspace   device scratch, 16-byte aligned, of at least
  *               segquant_adapter_workspace_bytes() bytes (SEGQ_ERR_UNSUPPORTED
  *               with fewer), contents undefined afterwards; calls that share

@@ -112,6 +112,111 @@ int hip_status(hipError_t e, const char *what) {
   return ok();
 }
 
+// ------------------------------------------- operands that share memory --
+typedef __int128 I128;  // leading dimensions have no upper limit
+
+I128 floor_div(I128 a, I128 b) {  // b > 0
+  return a / b - (a % b < 0 ? 1 : 0);
+}
+
+// Sum of floor((a i + b) / m) over 0 <= i < n, for a, b >= 0 and m > 0: whole
+// multiples of m taken out, then the same count seen along the other axis, as
+// in Euclid's algorithm.  Modulo 2^128.
+unsigned __int128 floor_sum(unsigned __int128 n, unsigned __int128 m, unsigned __int128 a,
+                                   unsigned __int128 b) {
+  unsigned __int128 sum = 0;
+  while (n > 0) {
+    sum += (n % 2 ? (n - 1) / 2 * n : n / 2 * (n - 1)) * (a / m) + n * (b / m);
+    const unsigned __int128 top = a % m * n + b % m;
+    n = top / m;
+    b = top % m;
+    const unsigned __int128 t = m;
+    m = a % m;
+    a = t;
+    if (!m) break;
+  }
+  return sum;
+}
+
+// Rows of `width` bytes, `ld` bytes apart.
+struct Rows {
+  const void *at;
+  I128 ld, width;
+  int64_t n;
+};
+
+Rows bf16_rows(const uint16_t *p, int64_t ld, int64_t width, int64_t n) {
+  return {p, 2 * (I128)ld, 2 * (I128)width, n};
+}
+
+Rows one_run(const void *p, I128 bytes) { return {p, bytes, bytes, 1}; }
+
+// Whether two matrices share bytes; they may stand side by side in one buffer.
+// Rows i and j share some where 0 < i ld_p - d + w_p - j ld_q < w_p + w_q.  The
+// number of steps grows as the logarithm of the leading dimensions.
+bool rows_meet(const Rows &p, const Rows &q) {
+  if (!p.at || !q.at || p.n < 1 || q.n < 1) return false;
+  const I128 d = (I128)reinterpret_cast<uintptr_t>(q.at) - (I128)reinterpret_cast<uintptr_t>(p.at);
+  const I128 q_end = d + (q.n - 1) * q.ld;  // q's last row
+  if (d >= (p.n - 1) * p.ld + p.width || q_end + q.width <= 0) return false;
+  // the rows of p that meet a row of q at `at`
+  auto met = [&](I128 at) {
+    I128 first = floor_div(at - p.width, p.ld) + 1, last = floor_div(at + q.width - 1, p.ld);
+    if (first < 0) first = 0;
+    if (last > p.n - 1) last = p.n - 1;
+    return first <= last;
+  };
+  if (met(d) || met(q_end)) return true;
+  // any other meeting is with rows of p between these two, where the rows j of
+  // q that row i meets are counted without a look at q's ends
+  I128 first = floor_div(d + q.width - 1, p.ld) + 1, last = floor_div(q_end - p.width, p.ld);
+  if (first < 0) first = 0;
+  if (last > p.n - 1) last = p.n - 1;
+  if (first > last) return false;
+  const I128 start = first * p.ld - d, a = p.ld % q.ld;
+  return floor_sum(last - first + 1, q.ld, a, start + p.width - 1) !=
+         floor_sum(last - first + 1, q.ld, a, start - q.width);
+}
+
+// An operand of a call.  For an input, the outputs (bit i: the i'th) that may be
+// the input itself, where every element is read before it is written.
+struct Operand {
+  const char *name;
+  Rows rows;
+  unsigned in_place;
+};
+
+// Refuse a call whose outputs share bytes with each other or with an input.
+template <size_t NOut, size_t NIn>
+int check_apart(const Operand (&outs)[NOut], const Operand (&ins)[NIn]) {
+  const Operand *all[NOut + NIn];
+  I128 at[NOut + NIn], end[NOut + NIn];
+  for (size_t i = 0; i < NOut + NIn; ++i) {
+    all[i] = i < NOut ? &outs[i] : &ins[i - NOut];
+    const Rows &r = all[i]->rows;
+    at[i] = (I128)reinterpret_cast<uintptr_t>(r.at);
+    end[i] = r.at && r.n > 0 ? at[i] + (r.n - 1) * r.ld + r.width : at[i];
+  }
+  for (size_t i = 0; i < NOut; ++i)
+    for (size_t j = i + 1; j < NOut + NIn; ++j) {
+      if (end[i] <= at[j] || end[j] <= at[i]) continue;
+      const Rows &out = all[i]->rows, &in = all[j]->rows;
+      if (j >= NOut && (all[j]->in_place >> i & 1) && out.at == in.at && out.ld == in.ld) continue;
+      if (rows_meet(out, in))
+        return fail(SEGQ_ERR_SHAPE, "%s overlaps %s", all[i]->name, all[j]->name);
+    }
+  return SEGQ_OK;
+}
+
+// The codes a call writes, and the scales it reads for them.
+Rows code_rows(const sq::NormOut &o, int64_t M, int64_t K) {
+  return {o.q, o.ld_q, K, o.plane_stride ? 2 * M : M};
+}
+
+Rows scale_rows(const sq::NormOut &o) {
+  return one_run(o.q ? o.act : nullptr, 4 * (I128)sizeof(float) * o.ks.n);
+}
+
 }  // namespace
 
 namespace sq {
@@ -377,75 +482,6 @@ static int check_rows(const uint16_t *p, int64_t ld, int64_t len, const char *wh
   return SEGQ_OK;
 }
 
-typedef __int128 I128;  // leading dimensions have no upper limit
-
-static I128 floor_div(I128 a, I128 b) {  // b > 0
-  return a / b - (a % b < 0 ? 1 : 0);
-}
-
-// Sum of floor((a i + b) / m) over 0 <= i < n, for a, b >= 0 and m > 0: whole
-// multiples of m taken out, then the same count seen along the other axis, as
-// in Euclid's algorithm.  Modulo 2^128.
-static unsigned __int128 floor_sum(unsigned __int128 n, unsigned __int128 m, unsigned __int128 a,
-                                   unsigned __int128 b) {
-  unsigned __int128 sum = 0;
-  while (n > 0) {
-    sum += (n % 2 ? (n - 1) / 2 * n : n / 2 * (n - 1)) * (a / m) + n * (b / m);
-    const unsigned __int128 top = a % m * n + b % m;
-    n = top / m;
-    b = top % m;
-    const unsigned __int128 t = m;
-    m = a % m;
-    a = t;
-    if (!m) break;
-  }
-  return sum;
-}
-
-// Rows of `width` bytes, `ld` bytes apart.
-struct Rows {
-  const void *at;
-  I128 ld, width;
-  int64_t n;
-};
-
-static Rows bf16_rows(const uint16_t *p, int64_t ld, int64_t width, int64_t n) {
-  return {p, 2 * (I128)ld, 2 * (I128)width, n};
-}
-
-// Whether two matrices share bytes; they may stand side by side in one buffer.
-// Rows i and j share some where 0 < i ld_p - d + w_p - j ld_q < w_p + w_q.  The
-// number of steps grows as the logarithm of the leading dimensions.
-static bool rows_meet(const Rows &p, const Rows &q) {
-  if (!p.at || !q.at || p.n < 1 || q.n < 1) return false;
-  const I128 d = (I128)reinterpret_cast<uintptr_t>(q.at) - (I128)reinterpret_cast<uintptr_t>(p.at);
-  const I128 q_end = d + (q.n - 1) * q.ld;  // q's last row
-  if (d >= (p.n - 1) * p.ld + p.width || q_end + q.width <= 0) return false;
-  // the rows of p that meet a row of q at `at`
-  auto met = [&](I128 at) {
-    I128 first = floor_div(at - p.width, p.ld) + 1, last = floor_div(at + q.width - 1, p.ld);
-    if (first < 0) first = 0;
-    if (last > p.n - 1) last = p.n - 1;
-    return first <= last;
-  };
-  if (met(d) || met(q_end)) return true;
-  // any other meeting is with rows of p between these two, where the rows j of
-  // q that row i meets are counted without a look at q's ends
-  I128 first = floor_div(d + q.width - 1, p.ld) + 1, last = floor_div(q_end - p.width, p.ld);
-  if (first < 0) first = 0;
-  if (last > p.n - 1) last = p.n - 1;
-  if (first > last) return false;
-  const I128 start = first * p.ld - d, a = p.ld % q.ld;
-  return floor_sum(last - first + 1, q.ld, a, start + p.width - 1) !=
-         floor_sum(last - first + 1, q.ld, a, start - q.width);
-}
-
-// The same for an output that may be the input itself: every element is then
-// read before it is written.
-static bool rows_meet_apart(const Rows &out, const Rows &in) {
-  return !(out.at == in.at && out.ld == in.ld) && rows_meet(out, in);
-}
-
 static int check_norm_params(const float *gamma, const float *beta, float eps) {
   if (!(eps >= 1.17549435e-38f) || eps > 3.0e38f)
     return fail(SEGQ_ERR_SHAPE, "eps must be positive, finite and at least 2^-126");
@@ -512,8 +548,16 @@ int segquant_groupnorm_quantize(const uint16_t *z_bf16, int64_t B, int64_t P, in
                 "(segquant_groupnorm_workspace_bytes)", need);
   if (workspace && !aligned16(workspace))
     return fail(SEGQ_ERR_ALIGN, "workspace is not 16-byte aligned");
-  if (rows_meet_apart(bf16_rows(x_out, ld_xo, C, M), bf16_rows(z_bf16, ld_z, C, M)))
-    return fail(SEGQ_ERR_SHAPE, "x_out overlaps z_bf16");
+  const Operand outs[] = {{"x_out", bf16_rows(x_out, ld_xo, C, M)},
+                          {"q_out", code_rows(p.out, M, C)},
+                          {"workspace", one_run(workspace, need)}};
+  const Operand ins[] = {{"z_bf16", bf16_rows(z_bf16, ld_z, C, M), 1},
+                         {"gamma", one_run(gamma, sizeof(float) * (I128)C)},
+                         {"beta", one_run(beta, sizeof(float) * (I128)C)},
+                         {"scale", bf16_rows(scale, ld_mod, C, B)},
+                         {"shift", bf16_rows(shift, ld_mod, C, B)},
+                         {"act_scales", scale_rows(p.out)}};
+  if ((st = check_apart(outs, ins))) return st;
   p.z = z_bf16;
   p.ld_z = ld_z;
   p.eps = eps;
@@ -559,12 +603,19 @@ int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
                            x_out, ld_xo, p.out)))
     return st;
   if (M == 0) return ok();
-  const Rows h = bf16_rows(h_bf16, ld_h, K, M), br = bf16_rows(branch, ld_b, K, M);
-  const Rows ho = bf16_rows(h_out, ld_ho, K, M), xo = bf16_rows(x_out, ld_xo, K, M);
-  if (rows_meet_apart(ho, h) || rows_meet_apart(ho, br))
-    return fail(SEGQ_ERR_SHAPE, "h_out overlaps h_bf16 or branch");
-  if (rows_meet(xo, h) || rows_meet(xo, br) || rows_meet(xo, ho))
-    return fail(SEGQ_ERR_SHAPE, "x_out overlaps h_bf16, branch or h_out");
+  const Operand outs[] = {{"h_out", bf16_rows(h_out, ld_ho, K, M)},
+                          {"x_out", bf16_rows(x_out, ld_xo, K, M)},
+                          {"q_out", code_rows(p.out, M, K)}};
+  const Operand ins[] = {{"h_bf16", bf16_rows(h_bf16, ld_h, K, M), 1},
+                         {"branch", bf16_rows(branch, ld_b, K, M), 1},
+                         {"gate", bf16_rows(gate, ld_mod, K, n_req)},
+                         {"scale", bf16_rows(scale, ld_mod, K, n_req)},
+                         {"shift", bf16_rows(shift, ld_mod, K, n_req)},
+                         {"gamma", one_run(gamma, sizeof(float) * (I128)K)},
+                         {"beta", one_run(beta, sizeof(float) * (I128)K)},
+                         {"row_offset", one_run(row_offset, sizeof(int32_t) * ((I128)n_req + 1))},
+                         {"act_scales", scale_rows(p.out)}};
+  if ((st = check_apart(outs, ins))) return st;
   p.h = h_bf16;
   p.M = M;
   p.K = K;
@@ -668,11 +719,18 @@ int segquant_adapter_add(int64_t M, int64_t N, int64_t K, const uint16_t *x_bf16
                 "adapters of this shape need a workspace of at least %zu bytes "
                 "(segquant_adapter_workspace_bytes)", need);
   if (!aligned16(workspace)) return fail(SEGQ_ERR_ALIGN, "workspace is not 16-byte aligned");
-  const Rows y = bf16_rows(y_bf16, ld_y, N, M);
-  if (rows_meet(y, bf16_rows(x_bf16, ld_x, K, M)))
-    return fail(SEGQ_ERR_SHAPE, "y_bf16 overlaps x_bf16");
-  if (rows_meet_apart(y, bf16_rows(base_bf16, ld_base, N, M)))
-    return fail(SEGQ_ERR_SHAPE, "y_bf16 overlaps base_bf16");
+  const I128 factors = 2 * (I128)n_adapters * rank;  // bytes of a per column of it, of b per row
+  const Operand outs[] = {{"y_bf16", bf16_rows(y_bf16, ld_y, N, M)},
+                          {"workspace", one_run(workspace, need)}};
+  const Operand ins[] = {{"base_bf16", bf16_rows(base_bf16, ld_base, N, M), 1},
+                         {"x_bf16", bf16_rows(x_bf16, ld_x, K, M)},
+                         {"a", one_run(a, factors * n_nseg * K)},
+                         {"b", one_run(b, factors * N)},
+                         {"row_offset", one_run(row_offset, sizeof(int32_t) * ((I128)n_req + 1))},
+                         {"adapter", one_run(adapter, sizeof(int32_t) * (I128)n_req)},
+                         {"rank_of", one_run(rank_of, sizeof(int32_t) * (I128)n_adapters)},
+                         {"alpha", one_run(alpha, sizeof(float) * (I128)n_adapters)}};
+  if ((st = check_apart(outs, ins))) return st;
   p.x = x_bf16;
   p.ld_x = ld_x;
   p.row_offset = row_offset;

@@ -64,3 +64,69 @@ def test_many_interleaved_rows_take_no_time():
     assert not refused(groupnorm(**kw, x=FAKE2 + 2 * 64))
     assert refused(groupnorm(**kw, x=FAKE2 + 2 * 144))
     assert time.perf_counter() - start < 1.0
+
+
+# every operand in 4 MiB of its own
+A = {name: 0x1000000 + (i << 22) for i, name in enumerate(
+    ["z", "gamma", "beta", "scale", "shift", "act", "q", "x", "work", "h", "branch", "gate", "h_out",
+     "row_offset", "base", "ids", "rank_of", "a", "b", "alpha", "y"])}
+GN = dict({k: A[k] for k in ("z", "gamma", "beta", "scale", "shift", "act", "q", "x")}, B=2, Px=4)
+GN2 = dict(GN, Px=10000, work=A["work"], work_bytes=1 << 22)  # two launches
+ADA = {k: A[k] for k in ("h", "branch", "gate", "scale", "shift", "gamma", "beta", "act", "q", "x",
+                         "h_out", "row_offset")}
+ADP = {k: A[k] for k in ("x", "row_offset", "ids", "rank_of", "a", "b", "alpha", "base", "y")}
+ADP2 = dict(ADP, M=64, rank=80, work=A["work"], work_bytes=1 << 22)
+
+
+def test_operands_apart_go_on_to_the_launch():
+    assert 0 < S.segquant_groupnorm_workspace_bytes(2, 10000, 64, 8) < 1 << 22
+    assert 0 < S.segquant_adapter_workspace_bytes(64, 64, 64, 2, 80) < 1 << 22
+    for call, kw in ((groupnorm, GN), (groupnorm, GN2), (adanorm, ADA), (adapter, ADP),
+                     (adapter, ADP2)):
+        assert not refused(call(**kw))
+        assert not refused(call(**kw, layout=1)) if call is not adapter else True
+
+
+@pytest.mark.parametrize("call,kw,out,operand,last", [
+    # the operand's last byte or more before its end: the output starts there
+    *[(groupnorm, GN, out, name, size - 16) for out in ("q", "x") for name, size in (
+        ("gamma", 256), ("beta", 256), ("scale", 256), ("shift", 256))],
+    (groupnorm, GN, "q", "act", 0), (groupnorm, GN, "x", "act", 0),
+    (groupnorm, GN, "q", "z", 0), (groupnorm, GN, "q", "z", 8 * 128 - 16),
+    (groupnorm, GN, "q", "x", 0), (groupnorm, GN, "x", "q", 8 * 64 - 16),
+    *[(groupnorm, GN2, "work", name, 0) for name in ("z", "gamma", "beta", "scale", "shift", "act",
+                                                     "q", "x")],
+    *[(adanorm, ADA, out, name, size - 16) for out in ("q", "x", "h_out") for name, size in (
+        ("gamma", 256), ("beta", 256), ("scale", 256), ("shift", 256), ("gate", 256))],
+    *[(adanorm, ADA, out, "row_offset", 0) for out in ("q", "x", "h_out")],
+    *[(adanorm, ADA, out, "act", 0) for out in ("q", "x", "h_out")],
+    *[(adanorm, ADA, "q", name, 8 * 128 - 16) for name in ("h", "branch", "x", "h_out")],
+    (adanorm, ADA, "x", "h_out", 0),
+    *[(adapter, ADP, "y", name, size - 16) for name, size in (
+        ("a", 2 * 16 * 64 * 2), ("b", 2 * 64 * 16 * 2))],
+    *[(adapter, ADP, "y", name, 0) for name in ("row_offset", "ids", "rank_of", "alpha")],
+    *[(adapter, ADP2, "work", name, 0) for name in ("x", "row_offset", "ids", "rank_of", "alpha",
+                                                    "a", "b", "base", "y")],
+])
+def test_an_output_on_another_operand(call, kw, out, operand, last):
+    kw = {**kw, out: kw[operand] + last}
+    assert refused(call(**kw))
+    if out != "work" and last > 0:  # one 16-byte step on, it stands behind it
+        assert not refused(call(**{**kw, out: kw[out] + 16}))
+
+
+def test_the_second_plane_of_codes_counts():
+    kw = dict(GN, q=A["z"] - 8 * 64)  # the first plane ends where z starts
+    assert not refused(groupnorm(**kw, layout=0))
+    assert refused(groupnorm(**kw, layout=1))
+
+
+def test_outputs_side_by_side_with_inputs():
+    # codes in the padding of z's rows, x_out beside scale and shift
+    assert not refused(groupnorm(**dict(GN, ld_z=128, q=A["z"] + 128, ld_q=256)))
+    assert not refused(groupnorm(**dict(GN, scale=A["x"] + 128, ld_xo=128, ld_mod=128)))
+    # in place
+    assert not refused(groupnorm(**dict(GN, x=A["z"])))
+    assert not refused(adanorm(**dict(ADA, h_out=A["h"])))
+    assert not refused(adanorm(**dict(ADA, h_out=A["branch"])))
+    assert not refused(adapter(**dict(ADP, y=A["base"])))
