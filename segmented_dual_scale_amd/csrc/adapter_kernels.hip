@@ -730,8 +730,11 @@ bool in_one_launch(const AdapterProblem &p, bool few) {
 // rank 32: 15.6 us with runs of 12 (3 workgroups a CU), 17.9 with runs of 24;
 // 4096 rows of a request, K 3584, N 1536, rank 64: 24.2 with runs of 12, 19.7
 // with one of 24.
-int one_run_tiles(const AdapterProblem &p, bool few) {
-  const int64_t tiles = few ? p.M : tile_bound(p, 16) - p.n_req / 2;  // about, not empty
+int one_run_tiles(const AdapterProblem &p) {
+  // about as many as are not empty (by_row: about a row each).  64 requests of 8
+  // rows, K and N 1536, rank 16: 6.7 us; taken for 512 tiles, which leaves 64
+  // workgroups, 9.4
+  const int64_t tiles = p.by_row ? p.M : tile_bound(p, 16) - p.n_req / 2;
   const double start = 3.0 + (p.K / 256.0) * (0.1 + 0.004 * p.rank);
   double best = 0.0;
   int take = 4;
@@ -771,7 +774,7 @@ size_t adapter_plan(AdapterProblem &p) {
   p.k_per_split = 256 * ((steps + p.splits - 1) / p.splits);
   p.expand_mt = few ? 1 : 4;
   p.one = in_one_launch(p, few);
-  p.run_tiles = p.one ? one_run_tiles(p, few)
+  p.run_tiles = p.one ? one_run_tiles(p)
                       : run_tiles_for(p, tile_bound(p, 16 * p.expand_mt), few ? 1024 : 768);
   return p.one ? 0 : sizeof(float) * (size_t)p.splits * (size_t)p.M * (size_t)rt;
 }
