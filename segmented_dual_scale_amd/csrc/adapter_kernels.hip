@@ -701,25 +701,40 @@ int run_tiles_for(const AdapterProblem &p, int64_t rows, int64_t at_once) {
 // 16, 32, 64; 1024 and 4096 rows in four requests, 8192 in eight; x from the
 // last-level cache):
 //   N 1536               K 1536                  K 3584                  K 6144
-//   64 requests of a row  6.3  7.6  8.7           8.0  8.1 10.9           8.3  9.9 14.7
-//                       | 7.7  8.2  8.8         | 8.1  8.8  9.8         | 8.3  9.3 10.9
-//   1024 rows             6.5  7.8  9.1           7.8  9.8 13.8          12.3 13.8 19.4
-//                       | 9.3 10.2 14.9        | 10.1 11.5 17.7        | 11.3 12.8 20.1
-//   4096 rows            13.6 15.5 17.3          19.6 20.5 26.3          21.0 26.2 35.5
-//                      | 13.3 16.0 20.4        | 18.0 19.6 25.6        | 21.9 22.7 31.1
+//   64 requests of a row  6.5  7.6  8.6           8.1  8.1 10.7           8.7  9.9 14.5
+//                       | 7.8  8.2  8.7         | 8.1  8.9  9.7         | 8.4  9.4 10.9
+//   1024 rows             6.8  7.9  9.4           8.2 10.5 13.9          12.5 13.8 19.5
+//                       | 9.7 10.4 15.2        | 10.7 11.9 17.7        | 11.8 13.0 20.4
+//   4096 rows            14.0 15.5 17.0          19.9 20.1 26.8          21.3 26.4 35.6
+//                      | 14.2 16.4 20.8        | 18.6 19.9 26.1        | 22.5 22.8 31.6
 //   N 4608, 3 segments
-//   4096 rows            21.5 23.1 35.9          31.1 31.7 44.5          42.8 44.0 58.6
-//                      | 24.5 31.4 42.1        | 29.1 37.9 50.6        | 33.9 48.9 65.7
-//   8192 rows            38.4 41.3 57.7          55.3 58.8 78.6          76.5 84.8 110.1
-//                      | 39.4 47.3 57.1        | 46.0 58.0 71.0        | 67.2 78.7  96.9
+//   4096 rows            21.6 22.5 36.1          31.8 31.5 44.5          42.9 43.7 58.5
+//                      | 28.3 28.7 43.6        | 33.5 35.2 51.9        | 38.2 47.0 66.9
+//   8192 rows            38.9 41.2 57.9          55.7 58.8 78.9          72.4 83.6 108.9
+//                      | 40.2 47.5 57.7        | 47.1 58.4 71.7        | 61.4 79.2  97.6
 // So: K up to 4096, less for few rows of high rank, and x no more than the
 // caches hold: above, x comes from memory, which many short copies per
 // workgroup use less well (8192 rows, K 6144, N 1536, rank 64, x from memory:
 // 58 against 47 us, though 41 against 49 with x in the last-level cache).
+// A few rows per request fill a sixteenth of a tile or little more in either
+// form, and the table goes on, rank 16 (MB of x):
+//   rows, requests        4096, 512     16384, 1024    65536, 4096   65536, 65536
+//   N 1536, K 1536     13.9 | 16.5 (12)  38 |  43 (48) 189 | 200 (192)  866 |  901
+//           K 4096     18.5 | 21.5 (32)  68 |  70 (128) 277 | 295 (512) 1176 | 1195
+//   N 4608, 3 segments
+//           K 1536     30.5 | 33.5      135 | 139      561 | 521      2642 | 2518
+//           K 4096     42.7 | 41.9      198 | 176      807 | 665      3562 | 3221
+// There what counts is x read again by every segment after the first, as far as
+// it passes the 256 MB of the last-level cache.  Cells with the slower form: N
+// 1536, 4096 rows, K 3584 (1 to 7 %), 64 rows, K 3584, rank 32 (10 %), 1024 rows,
+// K 6144, rank 64 (5 %); N 4608, 4096 rows, K 6144, ranks 32 and 64 (8 and 14 %);
+// K 4096 with 3 segments up to 16384 rows of few to a request (2 to 13 %).
 bool in_one_launch(const AdapterProblem &p, bool few) {
   if (p.rank > 64) return false;
-  if (few) return p.K <= (p.rank > 16 ? 2048 : 4096);
-  return p.K <= 4096 && 2 * p.M * p.K <= (48 << 20);
+  const int64_t x_bytes = 2 * p.M * p.K;
+  if (few)
+    return p.K <= (p.rank > 16 ? 2048 : 4096) && x_bytes * (p.ns.n - 1) <= (256 << 20);
+  return p.K <= 4096 && x_bytes <= (48 << 20);
 }
 
 // Column blocks of a run in one launch: a longer run walks K fewer times, a

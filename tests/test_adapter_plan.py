@@ -56,3 +56,11 @@ def test_single_rows_keep_their_runs(program):
                        (2, 64)):
         assert plan["one"] and plan["by_row"]
         assert plan["run_blocks"] == (4 if n == 2 else 12)
+
+
+def test_few_rows_per_request_with_an_x_beyond_the_caches(program):
+    """Every segment after the first reads x again in one launch: two launches
+    where that is more than the last-level cache holds."""
+    case = (65536, 4608, 4096, 4096, 16)
+    one, large, small = plans(program, (*case, 1), (*case, 3), (4096, 4608, 4096, 512, 16, 3))
+    assert one["one"] and small["one"] and not large["one"]
