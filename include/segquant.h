@@ -290,7 +290,9 @@ int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
  * low-rank adapter.
  *   x_bf16      device bf16 [M][ld_x]: the layer's input before quantisation
  *   n_req, row_offset  as segquant_adanorm_quantize, row_offset required; rows
- *               of no request are left as they are in y
+ *               of no request are left as they are in y.  Where offsets
+ *               decrease, rows that are not in one request alone may hold
+ *               anything
  *   adapter     device int32 [n_req]; an index outside [0, n_adapters) (-1,
  *               say) means no adapter: y = base for that request's rows
  *   rank        stored rank, a multiple of SEGQ_ADAPTER_RANK_STEP up to
