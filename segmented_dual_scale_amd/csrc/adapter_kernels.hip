@@ -412,20 +412,13 @@ struct Expand {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int orow = lane >> 3, ocol = 8 * (lane & 7);  // this lane's place in a row of y
     const uint32_t lower = g < 2 ? ~0u : 0u;  // not against the zeros
-    for (bool first = true; n0 < run.end; n0 += 256, first = false) {
+    for (; n0 < run.end; n0 += 256) {
       const bool more = n0 + 256 < run.end;
       v4u b[Ops::kB][4];
       // this lane's first rank of operand q of B
       auto rank_at = [&](int q) { return 32 * q + 8 * (q < Ops::kPairs ? g : g & 1); };
       if (t.adapter >= 0) {
-        // vector-memory operations end in the order of their issue, and a whole
-        // tile issues its 2 MT stores of y behind the copy of the next B: the
-        // copy is done while they are still under way (8192 x 1536, rank 64:
-        // 18.7 against 19.3 us; a store that a mask leaves out does not count)
-        if (FULL && !first)
-          wait_copies<2 * MT>();
-        else
-          wait_copies<0>();
+        wait_copies<0>();
 #pragma unroll
         for (int q = 0; q < Ops::kB; ++q)
 #pragma unroll
@@ -742,8 +735,8 @@ bool in_one_launch(const AdapterProblem &p, bool few) {
 // and blocks of a wave, two or three of them side by side on a CU at hardly
 // more than the time of one, or what all read of x and a from the caches at 13
 // TB/s, whichever is more.  64 requests, K 1536, six segments of 24 blocks,
-// rank 32: 15.6 us with runs of 12 (3 workgroups a CU), 17.9 with runs of 24;
-// 4096 rows of a request, K 3584, N 1536, rank 64: 24.2 with runs of 12, 19.7
+// rank 32: 13.6 us with runs of 12 (3 workgroups a CU), 13.9 with runs of 24;
+// 4096 rows of a request, K 3584, N 1536, rank 64: 24.9 with runs of 12, 20.2
 // with one of 24.
 int one_run_tiles(const AdapterProblem &p) {
   // about as many as are not empty (by_row: about a row each).  64 requests of 8
