@@ -143,6 +143,7 @@ struct Rows {
   const void *at;
   I128 ld, width;
   int64_t n;
+  bool empty() const { return !at || width < 1 || n < 1; }
 };
 
 Rows bf16_rows(const uint16_t *p, int64_t ld, int64_t width, int64_t n) {
@@ -155,7 +156,7 @@ Rows one_run(const void *p, I128 bytes) { return {p, bytes, bytes, 1}; }
 // Rows i and j share some where 0 < i ld_p - d + w_p - j ld_q < w_p + w_q.  The
 // number of steps grows as the logarithm of the leading dimensions.
 bool rows_meet(const Rows &p, const Rows &q) {
-  if (!p.at || !q.at || p.n < 1 || q.n < 1) return false;
+  if (p.empty() || q.empty()) return false;
   const I128 d = (I128)reinterpret_cast<uintptr_t>(q.at) - (I128)reinterpret_cast<uintptr_t>(p.at);
   const I128 q_end = d + (q.n - 1) * q.ld;  // q's last row
   if (d >= (p.n - 1) * p.ld + p.width || q_end + q.width <= 0) return false;
@@ -195,7 +196,7 @@ int check_apart(const Operand (&outs)[NOut], const Operand (&ins)[NIn]) {
     all[i] = i < NOut ? &outs[i] : &ins[i - NOut];
     const Rows &r = all[i]->rows;
     at[i] = (I128)reinterpret_cast<uintptr_t>(r.at);
-    end[i] = r.at && r.n > 0 ? at[i] + (r.n - 1) * r.ld + r.width : at[i];
+    end[i] = r.empty() ? at[i] : at[i] + (r.n - 1) * r.ld + r.width;
   }
   for (size_t i = 0; i < NOut; ++i)
     for (size_t j = i + 1; j < NOut + NIn; ++j) {

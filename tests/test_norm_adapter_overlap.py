@@ -130,3 +130,12 @@ def test_outputs_side_by_side_with_inputs():
     assert not refused(adanorm(**dict(ADA, h_out=A["h"])))
     assert not refused(adanorm(**dict(ADA, h_out=A["branch"])))
     assert not refused(adapter(**dict(ADP, y=A["base"])))
+
+
+def test_a_workspace_that_the_call_does_not_use_may_stand_anywhere():
+    assert S.segquant_groupnorm_workspace_bytes(2, 4, 64, 8) == 0
+    for name in ("z", "x", "q", "scale"):
+        assert not refused(groupnorm(**GN, work=A[name] + 64, work_bytes=1 << 20))
+    assert S.segquant_adapter_workspace_bytes(8, 64, 64, 2, 16) == 0
+    for name in ("x", "y", "a", "base"):
+        assert not refused(adapter(**ADP, work=A[name] + 64, work_bytes=1 << 20))
