@@ -33,7 +33,8 @@
  *     call returns.  The only scratch memory is the optional, caller-owned
  *     workspace of segquant_gemm_w8a8_seg (its size from
  *     segquant_gemm_workspace_bytes) and the caller-owned workspaces of
- *     segquant_groupnorm_quantize and segquant_adapter_add.
+ *     segquant_groupnorm_quantize, segquant_adapter_add and
+ *     segquant_gemm_mxfp4.
  *   - Segment lists are HOST arrays (offset[n], width[n]), read only during
  *     the call: offsets start at 0, are contiguous, widths are positive and
  *     sum to the segmented dimension.  Every K-segment boundary except the
@@ -49,7 +50,7 @@
  *     changes no buffer.  segquant_last_error() gives the thread's detail
  *     text for its last failing call.  Nothing is thrown, printed or aborted.
  *   - The library is thread-safe; its only state is that thread-local text.
- *   - Inputs must not hold NaN.  +-Inf saturates to the end of its half's
+ *   - Inputs must not hold NaN (MXFP4 carries it: see there).  +-Inf saturates to the end of its half's
  *     code range when that half's inverse scale is nonzero; an infinite
  *     value in a half whose scale is zero is outside the contract.
  */
@@ -273,6 +274,170 @@ int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
                               const int32_t *kseg_width, const float *act_scales, int8_t *q_out,
                               int64_t ld_q, int32_t q_layout, uint16_t *x_out, int64_t ld_xo,
                               void *stream);
+
+/*
+ * Microscaled 4-bit floating point (MXFP4, of the OCP Microscaling Formats
+ * specification, version 1.0).  Along K, blocks of 32 neighbours share a power
+ * of two 2^(s - 127), s one byte; an element is a 4-bit float c times it, c =
+ * 0, 0.5, 1, 1.5, 2, 3, 4 or 6 (codes 0 .. 7; bit 3 the sign).  Quantising:
+ *   s = max(0, 127 + floor(log2 max |x|) - 2)        (0 for a block of zeros)
+ *   c = x / 2^(s - 127) rounded to nearest, ties to the even code, magnitudes
+ *       above 6 to 6
+ * A block that holds an infinity or a NaN gets s = 255, which is NaN: so are
+ * its values and every product with it.
+ *
+ * An MXFP4 matrix of R rows and K columns (K % 64 == 0) is two byte arrays in
+ * the operand order of the matrix cores, rows padded to a multiple of 16:
+ *   codes   KT = ceil(K / 128).  The codes of row r, columns k and k + 1 (k
+ *           even) in the low and high half of byte
+ *           ((r/16 * KT + k/128) * 64 + k%128/32 * 16 + r%16) * 16 + k%32/2
+ *   scales  KS = ceil(K / 512).  s of row r, block k/32 in byte
+ *           ((r/16 * KS + k/512) * 64 + k%128/32 * 16 + r%16) * 4 + k%512/128
+ * Columns K .. 128 KT - 1 hold codes and scales 0, the rest of the padding
+ * anything.  Rows of an activation are tokens, of a weight output columns.
+ */
+
+/* Bytes of the two arrays (0 for sizes that have no such matrix; R may be 0). */
+size_t segquant_mxfp4_code_bytes(int64_t R, int64_t K);
+size_t segquant_mxfp4_scale_bytes(int64_t R, int64_t K);
+
+/*
+ * segquant_quantize_mxfp4 -- x = bf16_rne(act(z)), or z itself
+ * (SEGQ_ACT_NONE), as MXFP4; act as in segquant_groupnorm_quantize.
+ *   z_bf16      device bf16 [M][ld_z]
+ *   codes, scales  device, the arrays of M rows and K columns, 16- and 4-byte
+ *               aligned; they must not overlap each other or z_bf16
+ * One launch per 2^20 rows.  Requires K % 64 == 0, z_bf16 16-byte aligned, ld_z a
+ * multiple of 8, M <= 2^27, K <= 2^22.  M may be 0.
+ */
+int segquant_quantize_mxfp4(const uint16_t *z_bf16, int64_t M, int64_t K, int64_t ld_z,
+                            int32_t act_kind, uint8_t *codes, uint8_t *scales, void *stream);
+
+/*
+ * segquant_quantize_weight_mxfp4 -- a weight W [K][N] (Y = X W) as an MXFP4
+ * matrix of N rows and K columns.
+ *   w           device fp32 [K][ld_w]
+ * Requires K % 64 == 0, N % 16 == 0, K <= 2^22, N <= 2^27.  Offline; one launch.
+ */
+int segquant_quantize_weight_mxfp4(const float *w, int64_t K, int64_t N, int64_t ld_w,
+                                   uint8_t *codes, uint8_t *scales, void *stream);
+
+/* segquant_unpack_mxfp4 -- the fp32 values [R][ld_x] of an MXFP4 matrix.  For
+ * inspection and tests.  One launch. */
+int segquant_unpack_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t R, int64_t K,
+                          float *x, int64_t ld_x, void *stream);
+
+/*
+ * segquant_gemm_mxfp4 -- the linear layer on MXFP4 weights and activations:
+ *   y[m][n] = bf16_rne( sum_k x[m][k] w[n][k] )
+ * in fp32, by the matrix cores' scaled products of 128 columns.  The
+ * activation is either
+ *   z_bf16 != NULL: bf16 [M][ld_z], quantised by the call as by
+ *                   segquant_quantize_mxfp4 with act_kind, or
+ *   x_codes, x_scales != NULL: an MXFP4 matrix of M rows (act_kind
+ *                   SEGQ_ACT_NONE).
+ *   w_codes, w_scales  an MXFP4 matrix of N rows
+ *   y_bf16      device bf16 [M][ld_y]
+ *   workspace   device scratch, 16-byte aligned, of at least
+ *               segquant_gemm_mxfp4_workspace_bytes() bytes where z_bf16 is
+ *               given (SEGQ_ERR_UNSUPPORTED with fewer), contents undefined
+ *               afterwards; calls that share one must be ordered.  NULL where
+ *               that size is 0.
+ * One launch, or quantisation and product where a workspace is asked for.  The
+ * order of every sum is fixed.  y_bf16 and the workspace must not overlap each
+ * other or an input: SEGQ_ERR_SHAPE.  Requires K % 64 == 0, N % 16 == 0, 16-byte
+ * aligned pointers (scales 4), ld_z and ld_y multiples of 8, M and N <= 2^27,
+ * K <= 2^22, M * N <= 2^37.  M may be 0.
+ */
+int segquant_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint16_t *z_bf16, int64_t ld_z,
+                        int32_t act_kind, const uint8_t *x_codes, const uint8_t *x_scales,
+                        const uint8_t *w_codes, const uint8_t *w_scales, uint16_t *y_bf16,
+                        int64_t ld_y, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace of segquant_gemm_mxfp4 on bf16 input of these sizes (0: none).  On
+ * invalid sizes returns 0 and sets segquant_last_error(). */
+size_t segquant_gemm_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
+ * segquant_rmsnorm_quantize -- the residual update and root-mean-square norm in
+ * front of a quantised layer, fused with its quantisation.  Over the K values
+ * of each row:
+ *   h' = bf16_rne(h + branch)                    (where branch is given)
+ *   x  = bf16_rne(h' / sqrt(mean h'^2 + eps) * gamma[k])             (fp32)
+ *   codes of x exactly as segquant_quantize_dualscale; its MXFP4 form exactly as
+ *   segquant_quantize_mxfp4
+ *   h_bf16, branch, h_out  as segquant_adanorm_quantize
+ *   eps         at least 2^-126
+ *   gamma       device fp32 [K], optional (NULL: 1)
+ *   n_kseg .. ld_xo  the outputs of segquant_activate_quantize
+ *   mx_codes, mx_scales  device, both or neither: x as an MXFP4 matrix of M rows
+ *               (then K % 64 == 0 and K <= 2^22)
+ * At least one of h_out, q_out, x_out and mx_codes.  One launch, no workspace;
+ * the order of every sum is fixed.  Alignment as segquant_adanorm_quantize
+ * (mx_codes 16, mx_scales 4).  M may be 0.  Outputs must not overlap each other
+ * or, but for h_out as there, inputs: SEGQ_ERR_SHAPE.  Values above about 2^60
+ * in magnitude overflow the fp32 squares.
+ */
+int segquant_rmsnorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int64_t ld_h,
+                              const uint16_t *branch, int64_t ld_b, uint16_t *h_out, int64_t ld_ho,
+                              float eps, const float *gamma, int32_t n_kseg,
+                              const int32_t *kseg_offset, const int32_t *kseg_width,
+                              const float *act_scales, int8_t *q_out, int64_t ld_q,
+                              int32_t q_layout, uint16_t *x_out, int64_t ld_xo, uint8_t *mx_codes,
+                              uint8_t *mx_scales, void *stream);
+
+/* Which elements of a head turn together, of its first R: 2i and 2i + 1, or
+ * i and i + R/2. */
+#define SEGQ_ROTARY_PAIRS 0
+#define SEGQ_ROTARY_HALVES 1
+#define SEGQ_ROTARY_MAX_AXES 8
+#define SEGQ_ROTARY_MAX_HEAD 512
+
+/*
+ * segquant_qk_rotary -- what stands between the QKV layer and attention: the
+ * root-mean-square norm of each head of q and k, then rotary positions of one
+ * or several axes (text; height and width; time, height and width).  For every
+ * sample b, token l and head, over its D elements:
+ *   t   = x / sqrt(mean x^2 + eps) * gamma[d]      (where norm; else t = x)
+ *   a'  = a cos u - b sin u,  b' = b cos u + a sin u   for pair i = (a, b) of
+ *         the first R elements of t, u = positions[l][axis of i] * freq[i]
+ *   out = bf16_rne(t'); elements from R on are not turned
+ * R is the sum of the axis widths: the first axis has the first
+ * axis_width[0] / 2 pairs, and so on.  Angles are formed in fp64 and reduced
+ * before they are rounded: any int32 position is as good as a small one.
+ *   q, k        device bf16 [B][L][heads][D], any strides, which are HOST
+ *               arrays of three: elements between samples, tokens and heads,
+ *               multiples of 8, not negative.  k may be NULL: q alone.
+ *   q_out, k_out  the same; each may be its input with the same strides
+ *   norm        0: no norm (gammas NULL)
+ *   eps         at least 2^-126 (unused without norm)
+ *   q_gamma, k_gamma  device fp32 [D], each optional (NULL: 1)
+ *   positions   device int32 [L][n_axes], or one such table per sample,
+ *               pos_batch_stride elements apart (0: one for all)
+ *   axis_width  HOST array, n_axes of them: even, not negative, R a multiple of
+ *               16 up to D
+ *   freq        device fp64 [R / 2], radians per position
+ *               (segquant_rotary_frequencies gives the usual ones)
+ * One launch; nothing is summed out of order.  Requires D a multiple of 8 up to
+ * SEGQ_ROTARY_MAX_HEAD, 16-byte aligned q, k, outputs and gammas, 8-byte aligned
+ * freq, B * L * heads <= 2^30 for q and k together.  B or L may be 0.  An output
+ * must not overlap itself, the other or, but for its own as above, an input:
+ * SEGQ_ERR_SHAPE.  Beside another tensor of the same sample and token strides
+ * (q and k inside one QKV matrix) the overlap is exact, else an output's whole
+ * extent counts where its rows are not evenly spaced.
+ */
+int segquant_qk_rotary(int64_t B, int64_t L, int32_t D, const uint16_t *q, int32_t q_heads,
+                       const int64_t *q_stride, uint16_t *q_out, const int64_t *q_out_stride,
+                       const uint16_t *k, int32_t k_heads, const int64_t *k_stride,
+                       uint16_t *k_out, const int64_t *k_out_stride, int32_t norm, float eps,
+                       const float *q_gamma, const float *k_gamma, const int32_t *positions,
+                       int64_t pos_batch_stride, int32_t n_axes, const int32_t *axis_width,
+                       const double *freq, int32_t style, void *stream);
+
+/* The usual frequencies, theta^(-2j / width) for pair j of an axis, into the HOST
+ * array freq [R / 2].  Host-only: no GPU work. */
+int segquant_rotary_frequencies(int32_t n_axes, const int32_t *axis_width, double theta,
+                                double *freq);
 
 /* Storage granularity and limit of adapter ranks. */
 #define SEGQ_ADAPTER_RANK_STEP 16

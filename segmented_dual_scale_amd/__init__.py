@@ -36,7 +36,11 @@ __all__ = [
     "segquant_gemm_halves", "segquant_gemm_w8a8_seg_noalloc", "SEGQ_NOALLOC_SCRATCH_BYTES",
     "SEGQ_ACT_NONE", "segquant_groupnorm_workspace_bytes", "segquant_groupnorm_quantize",
     "segquant_adanorm_quantize", "segquant_adapter_workspace_bytes", "segquant_adapter_add",
-    "SEGQ_ADAPTER_RANK_STEP", "SEGQ_ADAPTER_RANK_MAX",
+    "SEGQ_ADAPTER_RANK_STEP", "SEGQ_ADAPTER_RANK_MAX", "segquant_rmsnorm_quantize",
+    "segquant_mxfp4_bytes", "segquant_quantize_mxfp4", "segquant_quantize_weight_mxfp4",
+    "segquant_unpack_mxfp4", "segquant_gemm_mxfp4", "segquant_gemm_mxfp4_workspace_bytes",
+    "SEGQ_ROTARY_PAIRS", "SEGQ_ROTARY_HALVES", "SEGQ_ROTARY_MAX_AXES", "SEGQ_ROTARY_MAX_HEAD",
+    "segquant_rotary_frequencies", "segquant_qk_rotary",
 ]
 
 SEGQ_OK = 0
@@ -64,6 +68,10 @@ SEGQ_KERNEL_SMALLM = 2
 SEGQ_NOALLOC_SCRATCH_BYTES = 64 << 20
 SEGQ_ADAPTER_RANK_STEP = 16
 SEGQ_ADAPTER_RANK_MAX = 256
+SEGQ_ROTARY_PAIRS = 0
+SEGQ_ROTARY_HALVES = 1
+SEGQ_ROTARY_MAX_AXES = 8
+SEGQ_ROTARY_MAX_HEAD = 512
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # SEGQUANT_LIBRARY names another build of the same library (the tests use it
@@ -119,6 +127,19 @@ def load_library():
         "segquant_adapter_add": [I64, I64, I64, P, I64, I32, P, P, I32, I32, P, P, P, P, I32, P, P,
                                  P, I64, P, I64, P, ctypes.c_size_t, P],
         "segquant_adapter_workspace_bytes": [I64, I64, I64, I32, I32, I32, P, P],
+        "segquant_mxfp4_code_bytes": [I64, I64],
+        "segquant_mxfp4_scale_bytes": [I64, I64],
+        "segquant_quantize_mxfp4": [P, I64, I64, I64, I32, P, P, P],
+        "segquant_quantize_weight_mxfp4": [P, I64, I64, I64, P, P, P],
+        "segquant_unpack_mxfp4": [P, P, I64, I64, P, I64, P],
+        "segquant_gemm_mxfp4": [I64, I64, I64, P, I64, I32, P, P, P, P, P, I64, P,
+                                ctypes.c_size_t, P],
+        "segquant_gemm_mxfp4_workspace_bytes": [I64, I64, I64],
+        "segquant_rmsnorm_quantize": [P, I64, I64, I64, P, I64, P, I64, F32, P, I32, P, P, P, P,
+                                      I64, I32, P, I64, P, P, P],
+        "segquant_rotary_frequencies": [I32, P, ctypes.c_double, P],
+        "segquant_qk_rotary": [I64, I64, I32, P, I32, P, P, P, P, I32, P, P, P, I32, F32, P, P, P,
+                               I64, I32, P, P, I32, P],
         "segquant_gemm_halves": [P, I32],
         "segquant_version": [],
         "segquant_status_string": [ctypes.c_int],
@@ -136,6 +157,9 @@ def load_library():
     lib.segquant_gemm_workspace_bytes.restype = ctypes.c_size_t
     lib.segquant_groupnorm_workspace_bytes.restype = ctypes.c_size_t
     lib.segquant_adapter_workspace_bytes.restype = ctypes.c_size_t
+    lib.segquant_mxfp4_code_bytes.restype = ctypes.c_size_t
+    lib.segquant_mxfp4_scale_bytes.restype = ctypes.c_size_t
+    lib.segquant_gemm_mxfp4_workspace_bytes.restype = ctypes.c_size_t
     _lib = lib
     return lib
 
@@ -700,3 +724,241 @@ def segquant_adapter_add(x, a, b, adapter, row_offset, base=None, alpha=None, ra
                _want(out, "out", bf, y_shape, at), _row_ld(out, "out"), ws, ws_bytes),
            "segquant_adapter_add")
     return out
+
+
+# ------------------------- the 4-bit layer, the norm before it, q and k behind --
+@functools.lru_cache(maxsize=256)
+def segquant_mxfp4_bytes(R: int, K: int) -> Tuple[int, int]:
+    """Bytes of the codes and of the scales of an MXFP4 matrix of R rows."""
+    lib = load_library()
+    codes = int(lib.segquant_mxfp4_code_bytes(R, K))
+    if R and not codes:
+        raise ValueError(segquant_last_error())
+    return codes, int(lib.segquant_mxfp4_scale_bytes(R, K))
+
+
+def _mx_new(R: int, K: int, device):
+    import torch
+    codes, scales = segquant_mxfp4_bytes(R, K)
+    return (torch.empty(codes, dtype=torch.uint8, device=device),
+            torch.empty(scales, dtype=torch.uint8, device=device))
+
+
+def _mx_ptrs(mx, name: str, R: int, K: int, at: int):
+    """The two arrays of an MXFP4 matrix (None: not given) -> their addresses."""
+    import torch
+    if mx is None:
+        return None, None
+    codes, scales = mx
+    n, m = segquant_mxfp4_bytes(R, K)
+    return (_want_array(codes, name + " codes", torch.uint8, (n,), at),
+            _want_array(scales, name + " scales", torch.uint8, (m,), at))
+
+
+def segquant_quantize_mxfp4(z, act_kind: int = SEGQ_ACT_NONE, out=None):
+    """bf16 z [M][K] -> the MXFP4 matrix (codes, scales) of its activation: two
+    uint8 arrays of segquant_mxfp4_bytes(M, K)."""
+    import torch
+    fn = load_library().segquant_quantize_mxfp4
+    if z.dim() != 2 or z.dtype is not torch.bfloat16:
+        raise ValueError(f"z must be bfloat16 [M][K], got {z.dtype} {tuple(z.shape)}")
+    M, K = z.shape
+    at = z.get_device()
+    if out is None:
+        out = _mx_new(M, K, z.device)
+    _check(_on(at, fn, z.data_ptr(), M, K, _row_ld(z, "z"), act_kind,
+               *_mx_ptrs(out, "out", M, K, at)), "segquant_quantize_mxfp4")
+    return out
+
+
+def segquant_quantize_weight_mxfp4(w, out=None):
+    """fp32 W [K][N] (Y = X W) -> the MXFP4 matrix (codes, scales) of N rows and
+    K columns.  Offline."""
+    import torch
+    fn = load_library().segquant_quantize_weight_mxfp4
+    if w.dim() != 2 or w.dtype is not torch.float32:
+        raise ValueError(f"w must be float32 [K][N], got {w.dtype} {tuple(w.shape)}")
+    K, N = w.shape
+    at = w.get_device()
+    if out is None:
+        out = _mx_new(N, K, w.device)
+    _check(_on(at, fn, w.data_ptr(), K, N, _ld(w, "w"), *_mx_ptrs(out, "out", N, K, at)),
+           "segquant_quantize_weight_mxfp4")
+    return out
+
+
+def segquant_unpack_mxfp4(mx, R: int, K: int, out=None):
+    """An MXFP4 matrix (codes, scales) -> its values, fp32 [R][K]."""
+    import torch
+    fn = load_library().segquant_unpack_mxfp4
+    at = mx[0].get_device()
+    if out is None:
+        out = torch.empty((R, K), dtype=torch.float32, device=mx[0].device)
+    _check(_on(at, fn, *_mx_ptrs(mx, "mx", R, K, at), R, K,
+               _want(out, "out", torch.float32, (R, K), at), _ld(out, "out")),
+           "segquant_unpack_mxfp4")
+    return out
+
+
+def segquant_gemm_mxfp4_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load_library().segquant_gemm_mxfp4_workspace_bytes(M, N, K))
+
+
+_gemm_mx_bytes = functools.lru_cache(maxsize=256)(segquant_gemm_mxfp4_workspace_bytes)
+
+
+def segquant_gemm_mxfp4(z, w, N: int, K: Optional[int] = None, xq=None, M: Optional[int] = None,
+                        act_kind: int = SEGQ_ACT_NONE, out=None, workspace="auto"):
+    """The linear layer on MXFP4 weights and activations: bf16 y [M][N].
+
+    z: bf16 [M][K], quantised by the call behind its activation; or None with
+    xq = an MXFP4 matrix (codes, scales) of M rows and K columns (M may be left
+    to out).  w: the (codes, scales) of segquant_quantize_weight_mxfp4, N its
+    columns.  workspace: a device tensor, None, or "auto" (from torch's
+    allocator when the library asks for one)."""
+    import torch
+    fn = load_library().segquant_gemm_mxfp4
+    bf = torch.bfloat16
+    ld_z = ws_bytes = 0
+    ptr = ws = None
+    if (z is None) == (xq is None):
+        raise ValueError("exactly one of z and xq must be given")
+    if z is not None:
+        if z.dim() != 2 or z.dtype is not bf:
+            raise ValueError(f"z must be bfloat16 [M][K], got {z.dtype} {tuple(z.shape)}")
+        if M not in (None, z.shape[0]) or K not in (None, z.shape[1]):
+            raise ValueError(f"z of shape {tuple(z.shape)} with M {M} and K {K}")
+        M, K = z.shape
+        dev, at, ptr, ld_z = z.device, z.get_device(), z.data_ptr(), _row_ld(z, "z")
+        workspace, ws, ws_bytes = _workspace(workspace, _gemm_mx_bytes, (M, N, K), dev)
+    else:
+        if M is None and out is not None:
+            M = out.shape[0]
+        if M is None or K is None:
+            raise ValueError("M (or out) and K are required with a pre-quantised input")
+        dev, at = xq[0].device, xq[0].get_device()
+    if out is None:
+        out = torch.empty((M, N), dtype=bf, device=dev)
+    _check(_on(at, fn, M, N, K, ptr, ld_z, act_kind, *_mx_ptrs(xq, "xq", M, K, at),
+               *_mx_ptrs(w, "w", N, K, at), _want(out, "out", bf, (M, N), at),
+               _row_ld(out, "out"), ws, ws_bytes), "segquant_gemm_mxfp4")
+    return out
+
+
+def segquant_rmsnorm_quantize(h, eps: float = 1e-6, gamma=None, branch=None, act_scales=None,
+                              kseg: Optional[Sequence[int]] = None, layout: int = SEGQ_Q_SIGNED,
+                              out=None, x_out=None, h_out=None, mx_out=None,
+                              want_codes: bool = True):
+    """The residual update and root-mean-square norm before a layer, on bf16
+    rows h [M][K]: h' = h + branch (when branch is given), x = h' / rms(h') with
+    optional fp32 gamma [K].  Returns (codes or None, x or None, h' or None,
+    (MXFP4 codes, scales) or None): codes as segquant_quantize_dualscale (when
+    act_scales is given and want_codes), the others if tensors are passed (or
+    True to allocate them)."""
+    import torch
+    fn = load_library().segquant_rmsnorm_quantize
+    bf, f32 = torch.bfloat16, torch.float32
+    if h.dim() != 2 or h.dtype is not bf:
+        raise ValueError(f"h must be bfloat16 [M][K], got {h.dtype} {tuple(h.shape)}")
+    shape, dev, at = h.shape, h.device, h.get_device()
+    M, K = shape
+    if x_out is True:
+        x_out = torch.empty((M, -(-K // 8) * 8), dtype=bf, device=dev)[:, :K]
+    if h_out is True:
+        h_out = torch.empty((M, -(-K // 8) * 8), dtype=bf, device=dev)[:, :K]
+    if mx_out is True:
+        mx_out = _mx_new(M, K, dev)
+    n, off, wid, *_ = _segments(kseg, K)
+    act = q = None
+    ld_q = 0
+    if act_scales is not None and want_codes:
+        act = _want_array(act_scales, "act_scales", f32, (4, n), at)
+        out, q, ld_q = _codes_out(out, M, K, layout, dev, torch.empty)
+    else:
+        out = None
+    _check(_on(at, fn, h.data_ptr(), M, K, _row_ld(h, "h"), _want(branch, "branch", bf, shape, at),
+               _row_ld(branch, "branch"), _want(h_out, "h_out", bf, shape, at),
+               _row_ld(h_out, "h_out"), eps, _want_array(gamma, "gamma", f32, (K,), at), n, off,
+               wid, act, q, ld_q, layout, _want(x_out, "x_out", bf, shape, at),
+               _row_ld(x_out, "x_out"), *_mx_ptrs(mx_out, "mx_out", M, K, at)),
+           "segquant_rmsnorm_quantize")
+    return out, x_out, h_out, mx_out
+
+
+@functools.lru_cache(maxsize=256)
+def _axes(widths: Tuple[int, ...]):
+    import numpy as np
+    w = np.asarray(widths, dtype=np.int32)
+    w.flags.writeable = False
+    return len(w), w.ctypes.data, sum(widths), w  # the address belongs to the array
+
+
+def segquant_rotary_frequencies(widths: Sequence[int], theta: float = 10000.0):
+    """theta^(-2j / width) for the pairs of each axis: fp64 [sum(widths) / 2] on
+    the CPU."""
+    import torch
+    n, ptr, R, _ = _axes(tuple(map(int, widths)))
+    freq = torch.empty(max(R, 0) // 2, dtype=torch.float64)
+    _check(load_library().segquant_rotary_frequencies(n, ptr, theta, freq.data_ptr() or None),
+           "segquant_rotary_frequencies")
+    return freq
+
+
+def _head_strides(t, name: str, shape, at: int):
+    """A [B][L][heads][D] tensor (None: not given) -> its address and strides."""
+    import torch
+    if t is None:
+        return None, None
+    if t.dim() != 4 or t.stride(3) != 1 and t.shape[3] > 1 and t.numel():
+        raise ValueError(f"{name} must be 4-D with unit stride in its last dimension")
+    return (_want(t, name, torch.bfloat16, shape, at), (ctypes.c_int64 * 3)(*t.stride()[:3]))
+
+
+def segquant_qk_rotary(q, k, positions, freq, widths: Sequence[int],
+                       style: int = SEGQ_ROTARY_PAIRS, q_gamma=None, k_gamma=None,
+                       eps: float = 1e-6, norm: bool = True, q_out=None, k_out=None):
+    """Root-mean-square norm of each head (when norm), then rotary positions of
+    the axes whose widths are given, on bf16 q [B][L][Hq][D] and k
+    [B][L][Hk][D] (or None) of any strides with unit stride in D: views of a
+    packed QKV matrix, heads before tokens.  positions: int32 [L][axes] or
+    [B][L][axes]; freq: fp64 [sum(widths) / 2], radians per position
+    (segquant_rotary_frequencies, moved to the GPU); q_gamma, k_gamma: fp32 [D].
+    Returns (q', k'): q_out and k_out, which may be q and k, or contiguous
+    tensors allocated here."""
+    import torch
+    fn = load_library().segquant_qk_rotary
+    if q.dim() != 4 or q.dtype is not torch.bfloat16:
+        raise ValueError(f"q must be bfloat16 [B][L][heads][D], got {q.dtype} {tuple(q.shape)}")
+    B, L, Hq, D = q.shape
+    at = q.get_device()
+    n, axes, R, _ = _axes(tuple(map(int, widths)))
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_shape, Hk = None, 0
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError(f"k must be bfloat16 [B][L][heads][D], got {tuple(k.shape)}")
+        Hk = k.shape[2]
+        k_shape = (B, L, Hk, D)
+        if k_out is None:
+            k_out = torch.empty(k_shape, dtype=q.dtype, device=q.device)
+    elif k_out is not None or k_gamma is not None:
+        raise ValueError("k_out or k_gamma without k")
+    if positions.dim() == 3:
+        pos, per = _want_array(positions, "positions", torch.int32, (B, L, n), at), L * n
+    else:
+        pos, per = _want_array(positions, "positions", torch.int32, (L, n), at), 0
+    f32 = torch.float32
+    _check(_on(at, fn, B, L, D, *_with_heads(q, "q", q.shape, Hq, at),
+               *_head_strides(q_out, "q_out", q.shape, at), *_with_heads(k, "k", k_shape, Hk, at),
+               *_head_strides(k_out, "k_out", k_shape, at), int(bool(norm)), eps,
+               _want_array(q_gamma, "q_gamma", f32, (D,), at),
+               _want_array(k_gamma, "k_gamma", f32, (D,), at), pos, per, n, axes,
+               _want_array(freq, "freq", torch.float64, (R // 2,), at), style),
+           "segquant_qk_rotary")
+    return q_out, k_out
+
+
+def _with_heads(t, name: str, shape, heads: int, at: int):
+    ptr, strides = _head_strides(t, name, shape, at)
+    return ptr, heads, strides

@@ -20,7 +20,8 @@ OUT = os.path.join(HERE, "libsegquant.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["api.cpp", "act_kernels.hip", "weight_kernels.hip", "gemm_tile.hip", "gemm_lds.hip",
-           "gemm_smallm.hip", "noalloc.hip", "norm_kernels.hip", "adapter_kernels.hip"]
+           "gemm_smallm.hip", "noalloc.hip", "norm_kernels.hip", "adapter_kernels.hip",
+           "rmsnorm_kernels.hip", "rotary_kernels.hip", "mx_kernels.hip", "gemm_mx.hip"]
 # ceiling probes for the benchmark (matrix-core-only loop, streaming read):
 # a library of their own, not part of the layer's
 PROBE_SOURCES = ["probes.hip"]

@@ -7,6 +7,7 @@
 // nothing is thrown across the ABI.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -15,6 +16,7 @@
 #include "../../include/segquant.h"
 #include "sq_api.hpp"
 #include "sq_launch.hpp"
+#include "sq_mx.hpp"
 #include "sq_rows.hpp"
 
 namespace {
@@ -636,6 +638,434 @@ int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
   p.n_req = n_req;
   p.rows_per_req = M / n_req;
   return hip_status(sq::launch_adanorm(p, (hipStream_t)stream), "adanorm launch");
+}
+
+// ------------------------------------------- MXFP4, norm before, rotary behind --
+static int mx_sizes(int64_t R, int64_t K, int64_t max_rows = 1 << 27) {
+  if (R < 0 || K < 1) return fail(SEGQ_ERR_SHAPE, "bad shape %lld x %lld", (long long)R, (long long)K);
+  if (K % 64) return fail(SEGQ_ERR_ALIGN, "MXFP4 needs K %% 64 == 0 (K=%lld)", (long long)K);
+  if (R > max_rows || K > (1 << 22))
+    return fail(SEGQ_ERR_UNSUPPORTED, "%lld rows > %lld or K %lld > 2^22", (long long)R,
+                (long long)max_rows, (long long)K);
+  return SEGQ_OK;
+}
+
+size_t segquant_mxfp4_code_bytes(int64_t R, int64_t K) {
+  if (mx_sizes(R, K, kI32Max)) return 0;
+  ok();
+  return (size_t)sq::mx_code_bytes(R, K);
+}
+
+size_t segquant_mxfp4_scale_bytes(int64_t R, int64_t K) {
+  if (mx_sizes(R, K, kI32Max)) return 0;
+  ok();
+  return (size_t)sq::mx_scale_bytes(R, K);
+}
+
+static int check_mx(const uint8_t *codes, const uint8_t *scales, const char *what) {
+  if (!codes || !scales) return fail(SEGQ_ERR_NULL, "%s codes or scales is NULL", what);
+  if (!aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u))
+    return fail(SEGQ_ERR_ALIGN, "%s codes must be 16-byte and scales 4-byte aligned", what);
+  return SEGQ_OK;
+}
+
+static int check_act(int32_t act_kind) {
+  if (act_kind != SEGQ_ACT_NONE && act_kind != SEGQ_ACT_SILU && act_kind != SEGQ_ACT_GELU)
+    return fail(SEGQ_ERR_SHAPE, "unknown act_kind %d", act_kind);
+  return SEGQ_OK;
+}
+
+int segquant_quantize_mxfp4(const uint16_t *z_bf16, int64_t M, int64_t K, int64_t ld_z,
+                            int32_t act_kind, uint8_t *codes, uint8_t *scales, void *stream) {
+  int st = check_x(z_bf16, M, K, ld_z);
+  if (st || (st = mx_sizes(M, K)) || (st = check_act(act_kind))) return st;
+  if (M == 0) return ok();
+  if ((st = check_mx(codes, scales, "output"))) return st;
+  const Operand outs[] = {{"codes", one_run(codes, sq::mx_code_bytes(M, K))},
+                          {"scales", one_run(scales, sq::mx_scale_bytes(M, K))}};
+  const Operand ins[] = {{"z_bf16", bf16_rows(z_bf16, ld_z, K, M)}};
+  if ((st = check_apart(outs, ins))) return st;
+  return hip_status(sq::launch_quantize_mx(z_bf16, M, K, ld_z, act_kind, codes, scales,
+                                           (hipStream_t)stream),
+                    "quantize_mxfp4 launch");
+}
+
+int segquant_quantize_weight_mxfp4(const float *w, int64_t K, int64_t N, int64_t ld_w,
+                                   uint8_t *codes, uint8_t *scales, void *stream) {
+  int st = mx_sizes(N, K);
+  if (st) return st;
+  if (N < 1 || ld_w < N)
+    return fail(SEGQ_ERR_SHAPE, "N %lld < 1 or ld_w %lld < N", (long long)N, (long long)ld_w);
+  if (N % 16) return fail(SEGQ_ERR_ALIGN, "weight needs N %% 16 == 0 (N=%lld)", (long long)N);
+  if (!w) return fail(SEGQ_ERR_NULL, "w is NULL");
+  if (reinterpret_cast<uintptr_t>(w) & 3u) return fail(SEGQ_ERR_ALIGN, "w is not 4-byte aligned");
+  if ((st = check_mx(codes, scales, "output"))) return st;
+  const Operand outs[] = {{"codes", one_run(codes, sq::mx_code_bytes(N, K))},
+                          {"scales", one_run(scales, sq::mx_scale_bytes(N, K))}};
+  const Operand ins[] = {{"w", {w, 4 * (I128)ld_w, 4 * (I128)N, K}}};
+  if ((st = check_apart(outs, ins))) return st;
+  return hip_status(
+      sq::launch_quantize_weight_mx(w, K, N, ld_w, codes, scales, (hipStream_t)stream),
+      "quantize_weight_mxfp4 launch");
+}
+
+int segquant_unpack_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t R, int64_t K,
+                          float *x, int64_t ld_x, void *stream) {
+  int st = mx_sizes(R, K);
+  if (st) return st;
+  if (ld_x < K) return fail(SEGQ_ERR_SHAPE, "ld_x %lld < K %lld", (long long)ld_x, (long long)K);
+  if (R == 0) return ok();
+  if ((st = check_mx(codes, scales, "input"))) return st;
+  if (!x) return fail(SEGQ_ERR_NULL, "x is NULL");
+  if (reinterpret_cast<uintptr_t>(x) & 3u) return fail(SEGQ_ERR_ALIGN, "x is not 4-byte aligned");
+  const Operand outs[] = {{"x", {x, 4 * (I128)ld_x, 4 * (I128)K, R}}};
+  const Operand ins[] = {{"codes", one_run(codes, sq::mx_code_bytes(R, K))},
+                         {"scales", one_run(scales, sq::mx_scale_bytes(R, K))}};
+  if ((st = check_apart(outs, ins))) return st;
+  return hip_status(sq::launch_unpack_mx(codes, scales, R, K, x, ld_x, (hipStream_t)stream),
+                    "unpack_mxfp4 launch");
+}
+
+static int mx_gemm_sizes(int64_t M, int64_t N, int64_t K) {
+  int st;
+  if ((st = mx_sizes(M, K)) || (st = mx_sizes(N, K))) return st;
+  if (N < 1) return fail(SEGQ_ERR_SHAPE, "N %lld < 1", (long long)N);
+  if (N % 16) return fail(SEGQ_ERR_ALIGN, "GEMM needs N %% 16 == 0 (N=%lld)", (long long)N);
+  if ((I128)M * N > (I128)1 << 37)
+    return fail(SEGQ_ERR_UNSUPPORTED, "M %lld x N %lld > 2^37", (long long)M, (long long)N);
+  return SEGQ_OK;
+}
+
+size_t segquant_gemm_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (mx_gemm_sizes(M, N, K)) return 0;
+  ok();
+  return M ? (size_t)(sq::mx_code_bytes(M, K) + sq::mx_scale_bytes(M, K)) : 0;
+}
+
+int segquant_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint16_t *z_bf16, int64_t ld_z,
+                        int32_t act_kind, const uint8_t *x_codes, const uint8_t *x_scales,
+                        const uint8_t *w_codes, const uint8_t *w_scales, uint16_t *y_bf16,
+                        int64_t ld_y, void *workspace, size_t workspace_bytes, void *stream) {
+  int st = mx_gemm_sizes(M, N, K);
+  if (st || (st = check_act(act_kind))) return st;
+  if (M == 0) return ok();
+  if ((z_bf16 != nullptr) == (x_codes != nullptr))
+    return fail(SEGQ_ERR_NULL, "exactly one of z_bf16 and x_codes must be given");
+  size_t need = 0;
+  if (z_bf16) {
+    if ((st = check_x(z_bf16, M, K, ld_z))) return st;
+    need = segquant_gemm_mxfp4_workspace_bytes(M, N, K);
+  } else {
+    if ((st = check_mx(x_codes, x_scales, "x"))) return st;
+    if (act_kind != SEGQ_ACT_NONE)
+      return fail(SEGQ_ERR_UNSUPPORTED, "an activation of input that is quantised already");
+  }
+  if ((st = check_mx(w_codes, w_scales, "w"))) return st;
+  if (!y_bf16) return fail(SEGQ_ERR_NULL, "y_bf16 is NULL");
+  if ((st = check_rows(y_bf16, ld_y, N, "y_bf16"))) return st;
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(SEGQ_ERR_UNSUPPORTED,
+                "bf16 input of this shape needs a workspace of at least %zu bytes "
+                "(segquant_gemm_mxfp4_workspace_bytes)", need);
+  if (!aligned16(workspace)) return fail(SEGQ_ERR_ALIGN, "workspace is not 16-byte aligned");
+  const I128 codes = sq::mx_code_bytes(M, K), scales = sq::mx_scale_bytes(M, K);
+  const Operand outs[] = {{"y_bf16", bf16_rows(y_bf16, ld_y, N, M)},
+                          {"workspace", one_run(workspace, need)}};
+  const Operand ins[] = {{"z_bf16", bf16_rows(z_bf16, ld_z, K, M)},
+                         {"x_codes", one_run(x_codes, codes)},
+                         {"x_scales", one_run(z_bf16 ? nullptr : x_scales, scales)},
+                         {"w_codes", one_run(w_codes, sq::mx_code_bytes(N, K))},
+                         {"w_scales", one_run(w_scales, sq::mx_scale_bytes(N, K))}};
+  if ((st = check_apart(outs, ins))) return st;
+  sq::MxGemmProblem p{M, N, K, x_codes, x_scales, w_codes, w_scales, y_bf16, ld_y};
+  if (z_bf16) {
+    uint8_t *c = static_cast<uint8_t *>(workspace), *s = c + sq::mx_code_bytes(M, K);
+    const hipError_t e =
+        sq::launch_quantize_mx(z_bf16, M, K, ld_z, act_kind, c, s, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_status(e, "quantize_mxfp4 launch");
+    p.x = c;
+    p.x_scale = s;
+  }
+  return hip_status(sq::launch_gemm_mx(p, (hipStream_t)stream), "gemm_mxfp4 launch");
+}
+
+int segquant_rmsnorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int64_t ld_h,
+                              const uint16_t *branch, int64_t ld_b, uint16_t *h_out, int64_t ld_ho,
+                              float eps, const float *gamma, int32_t n_kseg,
+                              const int32_t *kseg_offset, const int32_t *kseg_width,
+                              const float *act_scales, int8_t *q_out, int64_t ld_q,
+                              int32_t q_layout, uint16_t *x_out, int64_t ld_xo, uint8_t *mx_codes,
+                              uint8_t *mx_scales, void *stream) {
+  sq::RmsNormProblem p{};
+  int st = check_x(h_bf16, M, K, ld_h);
+  if (st) return st;
+  if (!branch && h_out) return fail(SEGQ_ERR_NULL, "h_out without branch");
+  if ((st = check_norm_params(gamma, nullptr, eps))) return st;
+  if ((st = check_rows(branch, ld_b, K, "branch"))) return st;
+  if ((st = check_rows(h_out, ld_ho, K, "h_out"))) return st;
+  if (h_out && h_out == h_bf16 && ld_ho != ld_h)
+    return fail(SEGQ_ERR_SHAPE, "h_out on h_bf16 needs ld_ho = ld_h");
+  if (mx_codes || mx_scales) {
+    if ((st = mx_sizes(M, K, kI32Max))) return st;
+    if ((st = check_mx(mx_codes, mx_scales, "output"))) return st;
+    p.mx = {mx_codes, mx_scales, sq::mx_tiles_k(K), sq::mx_scale_tiles_k(K)};
+  }
+  if (M > 0 && !q_out && !x_out && !h_out && !mx_codes)
+    return fail(SEGQ_ERR_NULL, "none of h_out, q_out, x_out and mx_codes is given");
+  if ((st = check_norm_out(M, K, n_kseg, kseg_offset, kseg_width, act_scales, q_out, ld_q, q_layout,
+                           x_out, ld_xo, p.out)))
+    return st;
+  if (M == 0) return ok();
+  const Operand outs[] = {{"h_out", bf16_rows(h_out, ld_ho, K, M)},
+                          {"x_out", bf16_rows(x_out, ld_xo, K, M)},
+                          {"q_out", code_rows(p.out, M, K)},
+                          {"mx_codes", one_run(mx_codes, mx_codes ? sq::mx_code_bytes(M, K) : 0)},
+                          {"mx_scales",
+                           one_run(mx_scales, mx_codes ? sq::mx_scale_bytes(M, K) : 0)}};
+  const Operand ins[] = {{"h_bf16", bf16_rows(h_bf16, ld_h, K, M), 1},
+                         {"branch", bf16_rows(branch, ld_b, K, M), 1},
+                         {"gamma", one_run(gamma, sizeof(float) * (I128)K)},
+                         {"act_scales", scale_rows(p.out)}};
+  if ((st = check_apart(outs, ins))) return st;
+  p.h = h_bf16;
+  p.M = M;
+  p.K = K;
+  p.ld_h = ld_h;
+  p.branch = branch;
+  p.ld_b = ld_b;
+  p.h_out = h_out;
+  p.ld_ho = ld_ho;
+  p.eps = eps;
+  p.gamma = gamma;
+  return hip_status(sq::launch_rmsnorm(p, (hipStream_t)stream), "rmsnorm launch");
+}
+
+static int rotary_axes(int32_t n_axes, const int32_t *axis_width, int32_t *ends, int64_t &R) {
+  if (n_axes < 1 || n_axes > SEGQ_ROTARY_MAX_AXES)
+    return fail(SEGQ_ERR_SHAPE, "%d axes outside [1, %d]", n_axes, SEGQ_ROTARY_MAX_AXES);
+  if (!axis_width) return fail(SEGQ_ERR_NULL, "axis_width is NULL");
+  R = 0;
+  for (int32_t i = 0; i < n_axes; ++i) {
+    if (axis_width[i] < 0 || axis_width[i] % 2 || axis_width[i] > SEGQ_ROTARY_MAX_HEAD)
+      return fail(SEGQ_ERR_SHAPE, "axis %d has width %d", i, axis_width[i]);
+    R += axis_width[i];
+    ends[i] = (int32_t)(R / 2);
+  }
+  if (R % 16 || R > SEGQ_ROTARY_MAX_HEAD)
+    return fail(SEGQ_ERR_SHAPE, "axis widths add up to %lld: not a multiple of 16 up to %d",
+                (long long)R, SEGQ_ROTARY_MAX_HEAD);
+  return SEGQ_OK;
+}
+
+int segquant_rotary_frequencies(int32_t n_axes, const int32_t *axis_width, double theta,
+                                double *freq) {
+  int32_t ends[SEGQ_ROTARY_MAX_AXES];
+  int64_t R;
+  const int st = rotary_axes(n_axes, axis_width, ends, R);
+  if (st) return st;
+  if (!(theta > 0.0) || !std::isfinite(theta))
+    return fail(SEGQ_ERR_SHAPE, "theta must be positive and finite");
+  if (R && !freq) return fail(SEGQ_ERR_NULL, "freq is NULL");
+  for (int32_t i = 0; i < n_axes; ++i)
+    for (int32_t j = 0; j < axis_width[i] / 2; ++j)
+      *freq++ = std::pow(theta, -2.0 * j / axis_width[i]);
+  return ok();
+}
+
+// The bytes of a [B][L][heads][D] tensor: rows where all its runs are evenly
+// spaced (exact), else its whole extent.
+static Rows head_rows(const uint16_t *p, const int64_t *stride, int64_t B, int64_t L, int64_t heads,
+                      int64_t D, bool &exact) {
+  struct Dim {
+    I128 stride;
+    int64_t n;
+  } d[3] = {{stride[0], B}, {stride[1], L}, {stride[2], heads}};
+  exact = true;
+  if (!p || !B || !L || !heads) return {nullptr, 0, 0, 0};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (d[j].stride > d[j + 1].stride) {
+        const Dim t = d[j];
+        d[j] = d[j + 1];
+        d[j + 1] = t;
+      }
+  I128 run = D, extent = D, ld = 0;
+  int64_t n = 1;
+  for (const Dim &e : d) {
+    if (e.n == 1) continue;
+    extent += e.stride * (e.n - 1);
+    if (n == 1 && e.stride == run) run *= e.n;
+    else if (n == 1 && e.stride > run) ld = e.stride, n = e.n;
+    else if (n > 1 && e.stride == ld * n) n *= e.n;
+    else exact = false;
+  }
+  if (!exact || n == 1) return {p, 2 * extent, 2 * extent, 1};
+  return {p, 2 * ld, 2 * run, n};
+}
+
+// Whether the elements of an output lie apart from each other.
+static bool heads_apart(const int64_t *stride, int64_t B, int64_t L, int64_t heads, int64_t D) {
+  const int64_t n[3] = {B, L, heads};
+  bool used[3] = {false, false, false};
+  I128 extent = D;
+  for (int step = 0; step < 3; ++step) {
+    int best = -1;
+    for (int i = 0; i < 3; ++i)
+      if (!used[i] && n[i] > 1 && (best < 0 || stride[i] < stride[best])) best = i;
+    if (best < 0) break;
+    if (stride[best] < extent) return false;
+    used[best] = true;
+    extent += (I128)stride[best] * (n[best] - 1);
+  }
+  return true;
+}
+
+struct Heads {
+  const char *name;
+  const uint16_t *p;
+  const int64_t *stride;
+  int64_t heads;
+};
+
+static bool heads_meet(const Heads &x, const Heads &y, int64_t B, int64_t L, int64_t D) {
+  bool ex, ey;
+  const Rows rx = head_rows(x.p, x.stride, B, L, x.heads, D, ex);
+  const Rows ry = head_rows(y.p, y.stride, B, L, y.heads, D, ey);
+  const bool same = (B == 1 || x.stride[0] == y.stride[0]) && (L == 1 || x.stride[1] == y.stride[1]);
+  const bool whole = (x.heads == 1 || x.stride[2] == D) && (y.heads == 1 || y.stride[2] == D);
+  if ((ex && ey) || !same || !whole) return rows_meet(rx, ry);
+  if (!rows_meet(rx, ry)) return false;
+  // two columns of one matrix per sample: offsets of a token of y from one of x
+  const I128 d = ((I128)reinterpret_cast<uintptr_t>(y.p) - (I128)reinterpret_cast<uintptr_t>(x.p));
+  const I128 wx = 2 * (I128)x.heads * D, wy = 2 * (I128)y.heads * D;
+  const I128 sb = 2 * (I128)x.stride[0], sl = 2 * (I128)x.stride[1];
+  for (int64_t b = 1 - B; b < B; ++b) {
+    const I128 at = d + b * sb;  // at + l sl inside (-wy, wx) for some |l| < L?
+    if (L == 1 || sl == 0) {
+      if (at > -wy && at < wx) return true;
+      continue;
+    }
+    I128 first = floor_div(-wy - at, sl) + 1, last = floor_div(wx - 1 - at, sl);
+    if (first < 1 - L) first = 1 - L;
+    if (last > L - 1) last = L - 1;
+    if (first <= last) return true;
+  }
+  return false;
+}
+
+static int check_heads(const uint16_t *p, const int64_t *stride, int64_t B, int64_t L,
+                       int64_t heads, const char *what) {
+  if (!p || !stride) return fail(SEGQ_ERR_NULL, "%s or its strides is NULL", what);
+  if (!aligned16(p)) return fail(SEGQ_ERR_ALIGN, "%s is not 16-byte aligned", what);
+  const int64_t n[3] = {B, L, heads};
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] <= 1) continue;
+    if (stride[i] < 0)
+      return fail(SEGQ_ERR_SHAPE, "%s has a stride of %lld", what, (long long)stride[i]);
+    if (stride[i] % 8)
+      return fail(SEGQ_ERR_ALIGN, "%s: stride %lld is not a multiple of 8", what,
+                  (long long)stride[i]);
+  }
+  return SEGQ_OK;
+}
+
+int segquant_qk_rotary(int64_t B, int64_t L, int32_t D, const uint16_t *q, int32_t q_heads,
+                       const int64_t *q_stride, uint16_t *q_out, const int64_t *q_out_stride,
+                       const uint16_t *k, int32_t k_heads, const int64_t *k_stride,
+                       uint16_t *k_out, const int64_t *k_out_stride, int32_t norm, float eps,
+                       const float *q_gamma, const float *k_gamma, const int32_t *positions,
+                       int64_t pos_batch_stride, int32_t n_axes, const int32_t *axis_width,
+                       const double *freq, int32_t style, void *stream) {
+  sq::RotaryProblem p{};
+  if (B < 0 || L < 0 || D < 1 || q_heads < 1 || (k && k_heads < 1))
+    return fail(SEGQ_ERR_SHAPE, "bad shape B=%lld L=%lld D=%d, %d and %d heads", (long long)B,
+                (long long)L, D, q_heads, k_heads);
+  if (D % 8) return fail(SEGQ_ERR_ALIGN, "head width %d is not a multiple of 8", D);
+  if (D > SEGQ_ROTARY_MAX_HEAD)
+    return fail(SEGQ_ERR_UNSUPPORTED, "head width %d > %d", D, SEGQ_ROTARY_MAX_HEAD);
+  const int64_t heads = (int64_t)q_heads + (k ? k_heads : 0);
+  if (B > (1 << 30) || L > (1 << 30) || (I128)B * L * heads > 1 << 30)
+    return fail(SEGQ_ERR_UNSUPPORTED, "B %lld x L %lld x %lld heads > 2^30", (long long)B,
+                (long long)L, (long long)heads);
+  int64_t R;
+  int st = rotary_axes(n_axes, axis_width, p.axis_end, R);
+  if (st) return st;
+  if (R > D) return fail(SEGQ_ERR_SHAPE, "axis widths add up to %lld > %d", (long long)R, D);
+  if (style != SEGQ_ROTARY_PAIRS && style != SEGQ_ROTARY_HALVES)
+    return fail(SEGQ_ERR_SHAPE, "unknown style %d", style);
+  if (!norm && (q_gamma || k_gamma)) return fail(SEGQ_ERR_SHAPE, "a gamma without norm");
+  if (!k && (k_out || k_gamma)) return fail(SEGQ_ERR_NULL, "k_out or k_gamma without k");
+  if (norm && (st = check_norm_params(q_gamma, k_gamma, eps))) return st;
+  if (B == 0 || L == 0) return ok();
+  if ((st = check_heads(q, q_stride, B, L, q_heads, "q"))) return st;
+  if ((st = check_heads(q_out, q_out_stride, B, L, q_heads, "q_out"))) return st;
+  if (k) {
+    if ((st = check_heads(k, k_stride, B, L, k_heads, "k"))) return st;
+    if ((st = check_heads(k_out, k_out_stride, B, L, k_heads, "k_out"))) return st;
+  }
+  if (!positions || (R && !freq)) return fail(SEGQ_ERR_NULL, "positions or freq is NULL");
+  if ((reinterpret_cast<uintptr_t>(positions) & 3u) || (reinterpret_cast<uintptr_t>(freq) & 7u))
+    return fail(SEGQ_ERR_ALIGN, "positions must be 4-byte and freq 8-byte aligned");
+  if (B > 1 && pos_batch_stride != 0 && pos_batch_stride < L * n_axes)
+    return fail(SEGQ_ERR_SHAPE, "pos_batch_stride %lld < %lld", (long long)pos_batch_stride,
+                (long long)(L * n_axes));
+  const Heads outs[] = {{"q_out", q_out, q_out_stride, q_heads},
+                        {"k_out", k_out, k_out_stride, k_heads}};
+  const Heads ins[] = {{"q", q, q_stride, q_heads}, {"k", k, k_stride, k_heads}};
+  const int64_t tables = B > 1 && pos_batch_stride ? B : 1;
+  const I128 table = sizeof(int32_t) * (I128)L * n_axes;
+  const Operand side[] = {
+      {"positions", {positions, tables > 1 ? sizeof(int32_t) * (I128)pos_batch_stride : table, table,
+                     tables}},
+      {"freq", one_run(freq, sizeof(double) * (I128)R / 2)},
+      {"q_gamma", one_run(q_gamma, sizeof(float) * (I128)D)},
+      {"k_gamma", one_run(k_gamma, sizeof(float) * (I128)D)}};
+  for (int i = 0; i < (k ? 2 : 1); ++i) {
+    const Heads &o = outs[i];
+    if (!heads_apart(o.stride, B, L, o.heads, D))
+      return fail(SEGQ_ERR_SHAPE, "%s overlaps itself", o.name);
+    if (i == 1 && heads_meet(o, outs[0], B, L, D))
+      return fail(SEGQ_ERR_SHAPE, "k_out overlaps q_out");
+    for (int j = 0; j < (k ? 2 : 1); ++j) {
+      const Heads &in = ins[j];
+      const bool same = (B == 1 || o.stride[0] == in.stride[0]) &&
+                        (L == 1 || o.stride[1] == in.stride[1]) &&
+                        (o.heads == 1 || o.stride[2] == in.stride[2]);
+      if (i == j && o.p == in.p && same) continue;  // each element is read before it is written
+      if (heads_meet(o, in, B, L, D))
+        return fail(SEGQ_ERR_SHAPE, "%s overlaps %s", o.name, in.name);
+    }
+    bool exact;
+    const Operand out[] = {{o.name, head_rows(o.p, o.stride, B, L, o.heads, D, exact)}};
+    if ((st = check_apart(out, side))) return st;
+  }
+  p.B = B;
+  p.L = L;
+  p.D = D;
+  p.R = (int32_t)R;
+  const uint16_t *in[] = {q, k};
+  uint16_t *out[] = {q_out, k_out};
+  const float *gamma[] = {q_gamma, k_gamma};
+  sq::RotaryTensor *t[] = {&p.q, &p.k};
+  for (int i = 0; i < (k ? 2 : 1); ++i) {
+    t[i]->in = in[i];
+    t[i]->out = out[i];
+    t[i]->gamma = gamma[i];
+    t[i]->heads = (int32_t)outs[i].heads;
+    const int64_t n[] = {B, L, outs[i].heads};
+    for (int j = 0; j < 3; ++j) {
+      t[i]->in_stride[j] = n[j] > 1 ? ins[i].stride[j] : 0;
+      t[i]->out_stride[j] = n[j] > 1 ? outs[i].stride[j] : 0;
+    }
+  }
+  p.norm = norm != 0;
+  p.halves = style == SEGQ_ROTARY_HALVES;
+  p.eps = eps;
+  p.positions = positions;
+  p.pos_batch = B > 1 ? pos_batch_stride : 0;
+  p.freq = freq;
+  p.n_axes = n_axes;
+  return hip_status(sq::launch_rotary(p, (hipStream_t)stream), "rotary launch");
 }
 
 static int adapter_sizes(int64_t M, int64_t N, int64_t K, int32_t n_req, int32_t rank,

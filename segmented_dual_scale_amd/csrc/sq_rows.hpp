@@ -1,6 +1,6 @@
-// sq_rows.hpp -- what the kernels around the layer share: norm_kernels.hip
-// (the normalisations that feed it) and adapter_kernels.hip (the low-rank
-// adapters beside it).  First the host-side launch interface of the C-ABI front
+// sq_rows.hpp -- what the kernels around the layer share: norm_kernels.hip and
+// rmsnorm_kernels.hip (the normalisations that feed it), rotary_kernels.hip
+// (q and k behind it) and adapter_kernels.hip (the low-rank adapters beside it).  First the host-side launch interface of the C-ABI front
 // end (api.cpp), whose arguments are already validated; then device helpers.
 #pragma once
 
@@ -74,6 +74,55 @@ struct AdaNormProblem {
 };
 
 hipError_t launch_adanorm(const AdaNormProblem &p, hipStream_t s);
+
+// MXFP4 rows (sq_mx.hpp); codes null: none.
+struct MxOut {
+  uint8_t *codes, *scales;
+  int64_t kt, ks;  // tiles along K of the codes, of the scales
+};
+
+struct RmsNormProblem {
+  const uint16_t *h;
+  int64_t M, K, ld_h;
+  const uint16_t *branch;  // optional: h' = h + branch
+  int64_t ld_b;
+  uint16_t *h_out;
+  int64_t ld_ho;
+  float eps;
+  const float *gamma;  // [K], optional
+  NormOut out;
+  MxOut mx;
+  int64_t rows_per;  // rows a row group walks, filled in by the launch
+};
+
+hipError_t launch_rmsnorm(const RmsNormProblem &p, hipStream_t s);
+
+// q or k: elements between samples, tokens and heads
+struct RotaryTensor {
+  const uint16_t *in;
+  uint16_t *out;
+  int64_t in_stride[3], out_stride[3];
+  const float *gamma;  // [D], optional
+  int32_t heads;
+};
+
+constexpr int kMaxAxes = 8;
+
+struct RotaryProblem {
+  int64_t B, L;
+  int32_t D, R;  // head width, its first R elements turn
+  RotaryTensor q, k;
+  bool norm, halves;
+  float eps;
+  const int32_t *positions;  // [L][n_axes], or one such table per sample
+  int64_t pos_batch;         // elements between samples, 0: shared
+  const double *freq;        // [R / 2]
+  int32_t n_axes;
+  int32_t axis_end[kMaxAxes];  // in pairs
+  int32_t chunks;  // waves per token, filled in by the launch
+};
+
+hipError_t launch_rotary(const RotaryProblem &p, hipStream_t s);
 
 struct AdapterProblem {
   int64_t M, N, K;
