@@ -30,11 +30,25 @@ struct MxGemmArgs {
   int32_t tiles_m, tiles_n;  // workgroup tiles
 };
 
+// Workgroup -> tile.  Workgroups go to the 8 XCDs in turn, so each XCD gets a
+// contiguous range of tiles, in groups of 8 row tiles, that share x and w in
+// its L2.
+__device__ __forceinline__ void tile_of(const MxGemmArgs &a, int &tm, int &tn) {
+  const int total = a.tiles_m * a.tiles_n, each = total >> 3, rest = total & 7;
+  const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
+  const int id = xcd * each + min(xcd, rest) + at;
+  const int span = 8 * a.tiles_n, first = id / span * 8, rows = min(8, a.tiles_m - first);
+  const int in = id - first * a.tiles_n;
+  tn = in / rows;
+  tm = first + in - tn * rows;
+}
+
 // Each wave computes (16 RM) x (16 RN) of y, its operands straight from memory.
 template <int RM, int RN>
 __global__ __launch_bounds__(256) void mx_gemm_kernel(MxGemmArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int tm = blockIdx.x % a.tiles_m, tn = blockIdx.x / a.tiles_m;
+  int tm, tn;
+  tile_of(a, tm, tn);
   const int m0 = (tm * 2 + (wave & 1)) * RM, n0 = (tn * 2 + (wave >> 1)) * RN;
   const uint8_t *xp[RM], *wp[RN], *xs[RM], *ws[RN];
 #pragma unroll
@@ -93,16 +107,246 @@ __global__ __launch_bounds__(256) void mx_gemm_kernel(MxGemmArgs a) {
   }
 }
 
+// ------------------------------------------------ both operands through LDS --
+typedef __attribute__((address_space(3))) void lds_void;
+
+// s_waitcnt: at most N vector-memory operations left and, with LGK, no LDS ones
+// (gfx9 encoding: vmcnt in bits 3:0 and 15:14).
+template <int N, bool LGK>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | ((LGK ? 0 : 15) << 8));
+}
+
+// 16 bytes a lane, to lds (uniform) + 16 lane
+__device__ __forceinline__ void copy16(const uint8_t *p, uint8_t *lds) {
+  __builtin_amdgcn_global_load_lds(p, (lds_void *)lds, 16, 0, 0);
+}
+
+__device__ __forceinline__ void keep_uniform(const uint8_t *&p) { asm("" : "+s"(p)); }
+
+template <int V>
+using lc = std::integral_constant<int, V>;
+
+// A workgroup of WM x WN waves owns 16 (WM RM) rows x 16 (WN RN) columns of y, a
+// wave RM x RN tiles of it.  K goes in stages of 128 through four LDS buffers,
+// filled by 16-byte global->LDS copies; scales in blocks of four stages through
+// two.  While a wave multiplies stage u it reads the operands of stage u + 1, one
+// x tile into the registers its last products have just released and one w tile
+// into a second set, and copies its part of stage u + 4 into the buffer that
+// stage u leaves: the one barrier of a stage says that all waves have read
+// stage u and that stage u + 1 has arrived.
+//
+// Of four neighbouring w tiles, instruction q takes rows 4 q .. 4 q + 3 of each,
+// so that its results in a lane, with those of the other three, are 16
+// neighbouring columns of y: 32 bytes a lane, 128 a row.  The copies bring them
+// into that order: every operand is read from LDS at 16 bytes a lane.
+template <int RM, int RN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a) {
+  constexpr int kWaves = WM * WN, kXT = WM * RM, kWT = WN * RN;
+  constexpr int kStage = (kXT + kWT) * 1024, kCopies = (kXT + kWT) / kWaves;
+  constexpr int kScaleGroups = (kXT + kWT) / 4, kScales = (kXT + kWT) * 256;
+  static_assert(RN % 4 == 0 && kXT % 4 == 0 && kXT % kWaves == 0 && kWT % kWaves == 0, "tiles");
+  extern __shared__ uint8_t smem[];
+  uint8_t *const scale_lds = smem + 4 * kStage;
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % WM, wn = wave / WM;
+  int tm, tn;
+  tile_of(a, tm, tn);
+  const int kt = a.kt;
+
+  // this wave's copies: KiB wave, wave + kWaves, ... of a stage, x tiles first.
+  // Lane (g, r) of w's KiB 4 t + q brings block g of row 4 q + r % 4 of tile 4 t + r / 4.
+  const uint8_t *src[kCopies];
+  uint32_t piece[kCopies];
+#pragma unroll
+  for (int c = 0; c < kCopies; ++c) {
+    const int t = c * kWaves + wave, wt = tn * kWT + ((t - kXT) & ~3);
+    if (t < kXT) {
+      src[c] = a.p.x + ((int64_t)min(tm * kXT + t, a.mt - 1) * kt << 10);
+      piece[c] = lane * 16;
+    } else {
+      const int first = min(wt, a.nt - 1), mine = min(wt + (r >> 2), a.nt - 1);
+      src[c] = a.p.w + ((int64_t)first * kt << 10);
+      piece[c] = ((uint32_t)((mine - first) * kt) << 10) +
+                 (g * 16 + 4 * ((t - kXT) & 3) + (r & 3)) * 16;
+    }
+  }
+  // copy c of the next stage; a uniform pointer moves on, the lane's part stays
+  // apart (the empty statement keeps the compiler from adding the two ahead of the
+  // loop, into two registers of every lane for each of them)
+  auto copy = [&](int c, int buf) {
+    const int t = c * kWaves + wave;
+    copy16(src[c] + piece[c], smem + buf * kStage + t * 1024);
+    src[c] += 1024;
+    keep_uniform(src[c]);
+  };
+  // scales: 1 KiB of four tiles a copy, in the same orders
+  auto copy_scales = [&](int s) {
+#pragma unroll
+    for (int c = 0; c < (kScaleGroups + kWaves - 1) / kWaves; ++c) {
+      const int q = c * kWaves + wave;
+      if (q >= kScaleGroups) break;
+      const uint8_t *p;
+      if (q * 4 < kXT)
+        p = a.p.x_scale + (((int64_t)min(tm * kXT + q * 4 + g, a.mt - 1) * a.ks + s) << 8) + 16 * r;
+      else
+        p = a.p.w_scale +
+            (((int64_t)min(tn * kWT + q * 4 - kXT + (r & 3), a.nt - 1) * a.ks + s) << 8) +
+            (r >> 2) * 64 + g * 16;
+      copy16(p, scale_lds + (s & 1) * kScales + q * 1024);
+    }
+  };
+  auto x_tile = [&](int buf, int i) {
+    return *reinterpret_cast<const v4u *>(smem + buf * kStage + (wm * RM + i) * 1024 + lane * 16);
+  };
+  auto w_tile = [&](int buf, int j) {
+    return *reinterpret_cast<const v4u *>(smem + buf * kStage + (kXT + wn * RN + j) * 1024 +
+                                          lane * 16);
+  };
+  auto x_scale = [&](int s, int i) {
+    return *reinterpret_cast<const uint32_t *>(scale_lds + (s & 1) * kScales +
+                                               (wm * RM + i) * 256 + lane * 4);
+  };
+  auto w_scale = [&](int s, int j) {
+    return *reinterpret_cast<const uint32_t *>(scale_lds + (s & 1) * kScales +
+                                               (kXT + wn * RN + j) * 256 + lane * 4);
+  };
+
+  v4f acc[RM][RN];
+#pragma unroll
+  for (int i = 0; i < RM; ++i)
+#pragma unroll
+    for (int j = 0; j < RN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  v4u x[RM], w[2][RN];
+  uint32_t sx[RM], sw[RN];
+
+  copy_scales(0);
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (u < kt) {
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) copy(c, u);
+    }
+  if (kt >= 4) wait_vm<3 * kCopies, false>();
+  else wait_vm<0, false>();
+  __builtin_amdgcn_s_barrier();
+#pragma unroll
+  for (int i = 0; i < RM; ++i) {
+    x[i] = x_tile(0, i);
+    sx[i] = x_scale(0, i);
+  }
+#pragma unroll
+  for (int j = 0; j < RN; ++j) {
+    w[0][j] = w_tile(0, j);
+    sw[j] = w_scale(0, j);
+  }
+
+  // stage u = 4 s + T.  WHOLE: stages u + 1 .. u + 4 exist.  At the end of K the
+  // operands read for a stage that does not exist are what its buffer holds, and
+  // no product takes them.
+  auto step = [&](int s, auto t_, auto whole_) {
+    constexpr int T = decltype(t_)::value;
+    constexpr bool WHOLE = decltype(whole_)::value != 0;
+    constexpr int NEXT = (T + 1) & 3;
+    const int u = 4 * s + T;
+    // stage u + 1 has arrived when at most the copies of u + 2 and u + 3 are left
+    if (WHOLE || u + 3 < kt) wait_vm<2 * kCopies, true>();
+    else if (u + 2 < kt) wait_vm<kCopies, true>();
+    else wait_vm<0, true>();
+    __builtin_amdgcn_s_barrier();
+    if (!WHOLE && u + 4 < kt) {
+      if (T == 0) copy_scales(s + 1);
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) copy(c, T);
+    }
+    if (WHOLE && T == 0) copy_scales(s + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    uint32_t nw[RN];
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+#pragma unroll
+      for (int j = 0; j < RN; ++j)
+        acc[i][j] = mx_mfma<T>(w[T & 1][j], sw[j], x[i], sx[i], acc[i][j]);
+      x[i] = x_tile(NEXT, i);
+#pragma unroll
+      for (int j = i * RN / RM; j < (i + 1) * RN / RM; ++j) w[(T + 1) & 1][j] = w_tile(NEXT, j);
+      if (T == 3) {
+        sx[i] = x_scale(s + 1, i);
+#pragma unroll
+        for (int j = i * RN / RM; j < (i + 1) * RN / RM; ++j) nw[j] = w_scale(s + 1, j);
+      }
+      if (WHOLE) {
+#pragma unroll
+        for (int c = i * kCopies / RM; c < (i + 1) * kCopies / RM; ++c) copy(c, T);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (T == 3) {
+#pragma unroll
+      for (int j = 0; j < RN; ++j) sw[j] = nw[j];
+    }
+  };
+  int s = 0;
+  for (; 4 * s + 8 <= kt; ++s) {
+    step(s, lc<0>{}, lc<1>{});
+    step(s, lc<1>{}, lc<1>{});
+    step(s, lc<2>{}, lc<1>{});
+    step(s, lc<3>{}, lc<1>{});
+  }
+  for (; 4 * s < kt; ++s) {
+    step(s, lc<0>{}, lc<0>{});
+    if (4 * s + 1 < kt) step(s, lc<1>{}, lc<0>{});
+    if (4 * s + 2 < kt) step(s, lc<2>{}, lc<0>{});
+    if (4 * s + 3 < kt) step(s, lc<3>{}, lc<0>{});
+  }
+  // lane (g, j) of x tile i: row j, columns 16 g .. 16 g + 15 of every 64
+#pragma unroll
+  for (int i = 0; i < RM; ++i) {
+    const int64_t m = (int64_t)(tm * kXT + wm * RM + i) * 16 + r;
+    if (m >= a.p.M) continue;
+#pragma unroll
+    for (int j = 0; j < RN; j += 4) {
+      const int n = (tn * kWT + wn * RN + j + g) * 16;
+      if (n >= a.p.N) continue;
+      uint16_t *y = a.p.y + m * a.p.ld_y + n;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const v4f &lo = acc[i][j + 2 * h], &hi = acc[i][j + 2 * h + 1];
+        *reinterpret_cast<v4u *>(y + 8 * h) =
+            v4u{cvt_bf16x2(lo[0], lo[1]), cvt_bf16x2(lo[2], lo[3]), cvt_bf16x2(hi[0], hi[1]),
+                cvt_bf16x2(hi[2], hi[3])};
+      }
+    }
+  }
+}
+
 }  // namespace
+
+template <int RM, int RN, int WM, int WN>
+static hipError_t launch_mx_lds(MxGemmArgs a, hipStream_t s) {
+  constexpr int kXT = WM * RM, kWT = WN * RN, kLds = (kXT + kWT) * (4 * 1024 + 2 * 256);
+  a.tiles_m = (a.mt + kXT - 1) / kXT;
+  a.tiles_n = (a.nt + kWT - 1) / kWT;
+  hipLaunchKernelGGL((mx_gemm_lds_kernel<RM, RN, WM, WN>),
+                     dim3((unsigned)(a.tiles_m * (int64_t)a.tiles_n)), dim3(64 * WM * WN), kLds, s,
+                     a);
+  return hipGetLastError();
+}
 
 hipError_t launch_gemm_mx(const MxGemmProblem &p, hipStream_t s) {
   MxGemmArgs a{p, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K),
                (int32_t)mx_row_tiles(p.M), (int32_t)mx_row_tiles(p.N), 0, 0};
-  a.tiles_m = (a.mt + 7) / 8;
-  a.tiles_n = (a.nt + 7) / 8;
-  hipLaunchKernelGGL((mx_gemm_kernel<4, 4>), dim3((unsigned)(a.tiles_m * (int64_t)a.tiles_n)),
-                     dim3(256), 0, s, a);
-  return hipGetLastError();
+  const int64_t big = (int64_t)((a.mt + 15) / 16) * ((a.nt + 15) / 16);
+  if (p.M <= 64) {
+    a.tiles_m = (a.mt + 7) / 8;
+    a.tiles_n = (a.nt + 7) / 8;
+    hipLaunchKernelGGL((mx_gemm_kernel<4, 4>), dim3((unsigned)(a.tiles_m * (int64_t)a.tiles_n)),
+                       dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  return big >= 200 ? launch_mx_lds<8, 4, 2, 4>(a, s) : launch_mx_lds<4, 4, 2, 2>(a, s);
 }
 
 }  // namespace sq
