@@ -110,17 +110,24 @@ __global__ __launch_bounds__(256) void mx_gemm_kernel(MxGemmArgs a) {
 // ------------------------------------------------ both operands through LDS --
 typedef __attribute__((address_space(3))) void lds_void;
 
-// s_waitcnt: at most N vector-memory operations left and, with LGK, no LDS ones
-// (gfx9 encoding: vmcnt in bits 3:0 and 15:14).
-template <int N, bool LGK>
+// s_waitcnt: at most N vector-memory operations left (gfx9 encoding: vmcnt in
+// bits 3:0 and 15:14).
+template <int N>
 __device__ __forceinline__ void wait_vm() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | ((LGK ? 0 : 15) << 8));
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
 // 16 bytes a lane, to lds (uniform) + 16 lane
 __device__ __forceinline__ void copy16(const uint8_t *p, uint8_t *lds) {
   __builtin_amdgcn_global_load_lds(p, (lds_void *)lds, 16, 0, 0);
+}
+
+// No memory access moves across.
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 __device__ __forceinline__ void keep_uniform(const uint8_t *&p) { asm("" : "+s"(p)); }
@@ -133,9 +140,10 @@ using lc = std::integral_constant<int, V>;
 // filled by 16-byte global->LDS copies; scales in blocks of four stages through
 // two.  While a wave multiplies stage u it reads the operands of stage u + 1, one
 // x tile into the registers its last products have just released and one w tile
-// into a second set, and copies its part of stage u + 4 into the buffer that
-// stage u leaves: the one barrier of a stage says that all waves have read
-// stage u and that stage u + 1 has arrived.
+// into a second set, and copies its part of stage u + 3 into the buffer of stage
+// u - 1.  The one barrier of a stage says that stage u + 1 has arrived and that
+// all waves have multiplied stage u - 1, and so read it: reads in flight need
+// not end before it.
 //
 // Of four neighbouring w tiles, instruction q takes rows 4 q .. 4 q + 3 of each,
 // so that its results in a lane, with those of the other three, are 16
@@ -143,10 +151,10 @@ using lc = std::integral_constant<int, V>;
 // into that order: every operand is read from LDS at 16 bytes a lane.
 template <int RM, int RN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a) {
-  constexpr int kWaves = WM * WN, kXT = WM * RM, kWT = WN * RN;
-  constexpr int kStage = (kXT + kWT) * 1024, kCopies = (kXT + kWT) / kWaves;
-  constexpr int kScaleGroups = (kXT + kWT) / 4, kScales = (kXT + kWT) * 256;
-  static_assert(RN % 4 == 0 && kXT % 4 == 0 && kXT % kWaves == 0 && kWT % kWaves == 0, "tiles");
+  constexpr int kWaves = WM * WN, kXT = WM * RM, kWT = WN * RN, kTiles = kXT + kWT;
+  constexpr int kStage = kTiles * 1024, kCopies = (kTiles + kWaves - 1) / kWaves;
+  constexpr int kXS = (kXT + 3) / 4, kScaleGroups = kXS + kWT / 4, kScales = kScaleGroups * 1024;
+  static_assert(RN % 4 == 0 && kXT % 2 == 0, "tiles");
   extern __shared__ uint8_t smem[];
   uint8_t *const scale_lds = smem + 4 * kStage;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
@@ -156,13 +164,14 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
   tile_of(a, tm, tn);
   const int kt = a.kt;
 
-  // this wave's copies: KiB wave, wave + kWaves, ... of a stage, x tiles first.
+  // this wave's copies: KiB wave, wave + kWaves, ... of a stage, x tiles first; past
+  // the last of them that one again (waves that copy less would wait for less).
   // Lane (g, r) of w's KiB 4 t + q brings block g of row 4 q + r % 4 of tile 4 t + r / 4.
   const uint8_t *src[kCopies];
   uint32_t piece[kCopies];
 #pragma unroll
   for (int c = 0; c < kCopies; ++c) {
-    const int t = c * kWaves + wave, wt = tn * kWT + ((t - kXT) & ~3);
+    const int t = min(c * kWaves + wave, kTiles - 1), wt = tn * kWT + ((t - kXT) & ~3);
     if (t < kXT) {
       src[c] = a.p.x + ((int64_t)min(tm * kXT + t, a.mt - 1) * kt << 10);
       piece[c] = lane * 16;
@@ -177,7 +186,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
   // apart (the empty statement keeps the compiler from adding the two ahead of the
   // loop, into two registers of every lane for each of them)
   auto copy = [&](int c, int buf) {
-    const int t = c * kWaves + wave;
+    const int t = min(c * kWaves + wave, kTiles - 1);
     copy16(src[c] + piece[c], smem + buf * kStage + t * 1024);
     src[c] += 1024;
     keep_uniform(src[c]);
@@ -189,11 +198,11 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
       const int q = c * kWaves + wave;
       if (q >= kScaleGroups) break;
       const uint8_t *p;
-      if (q * 4 < kXT)
+      if (q < kXS)
         p = a.p.x_scale + (((int64_t)min(tm * kXT + q * 4 + g, a.mt - 1) * a.ks + s) << 8) + 16 * r;
       else
         p = a.p.w_scale +
-            (((int64_t)min(tn * kWT + q * 4 - kXT + (r & 3), a.nt - 1) * a.ks + s) << 8) +
+            (((int64_t)min(tn * kWT + (q - kXS) * 4 + (r & 3), a.nt - 1) * a.ks + s) << 8) +
             (r >> 2) * 64 + g * 16;
       copy16(p, scale_lds + (s & 1) * kScales + q * 1024);
     }
@@ -211,7 +220,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
   };
   auto w_scale = [&](int s, int j) {
     return *reinterpret_cast<const uint32_t *>(scale_lds + (s & 1) * kScales +
-                                               (kXT + wn * RN + j) * 256 + lane * 4);
+                                               (4 * kXS + wn * RN + j) * 256 + lane * 4);
   };
 
   v4f acc[RM][RN];
@@ -224,14 +233,14 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
 
   copy_scales(0);
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
+  for (int u = 0; u < 3; ++u)
     if (u < kt) {
 #pragma unroll
       for (int c = 0; c < kCopies; ++c) copy(c, u);
     }
-  if (kt >= 4) wait_vm<3 * kCopies, false>();
-  else wait_vm<0, false>();
-  __builtin_amdgcn_s_barrier();
+  if (kt >= 3) wait_vm<2 * kCopies>();
+  else wait_vm<0>();
+  stage_barrier();
 #pragma unroll
   for (int i = 0; i < RM; ++i) {
     x[i] = x_tile(0, i);
@@ -243,25 +252,23 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
     sw[j] = w_scale(0, j);
   }
 
-  // stage u = 4 s + T.  WHOLE: stages u + 1 .. u + 4 exist.  At the end of K the
-  // operands read for a stage that does not exist are what its buffer holds, and
-  // no product takes them.
+  // stage u = 4 s + T.  WHOLE: stages u + 1 .. u + 3 exist, and u + 4 for T = 0.  At
+  // the end of K the operands read for a stage that does not exist are what its
+  // buffer holds, and no product takes them.
   auto step = [&](int s, auto t_, auto whole_) {
     constexpr int T = decltype(t_)::value;
     constexpr bool WHOLE = decltype(whole_)::value != 0;
-    constexpr int NEXT = (T + 1) & 3;
+    constexpr int NEXT = (T + 1) & 3, FREE = (T + 3) & 3;
     const int u = 4 * s + T;
-    // stage u + 1 has arrived when at most the copies of u + 2 and u + 3 are left
-    if (WHOLE || u + 3 < kt) wait_vm<2 * kCopies, true>();
-    else if (u + 2 < kt) wait_vm<kCopies, true>();
-    else wait_vm<0, true>();
-    __builtin_amdgcn_s_barrier();
-    if (!WHOLE && u + 4 < kt) {
-      if (T == 0) copy_scales(s + 1);
+    // stage u + 1 has arrived when at most the copies of u + 2 are left
+    if (WHOLE || u + 2 < kt) wait_vm<kCopies>();
+    else wait_vm<0>();
+    stage_barrier();
+    if (T == 0 && (WHOLE || u + 4 < kt)) copy_scales(s + 1);
+    if (!WHOLE && u + 3 < kt) {
 #pragma unroll
-      for (int c = 0; c < kCopies; ++c) copy(c, T);
+      for (int c = 0; c < kCopies; ++c) copy(c, FREE);
     }
-    if (WHOLE && T == 0) copy_scales(s + 1);
     __builtin_amdgcn_sched_barrier(0);
     uint32_t nw[RN];
 #pragma unroll
@@ -279,7 +286,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
       }
       if (WHOLE) {
 #pragma unroll
-        for (int c = i * kCopies / RM; c < (i + 1) * kCopies / RM; ++c) copy(c, T);
+        for (int c = i * kCopies / RM; c < (i + 1) * kCopies / RM; ++c) copy(c, FREE);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -326,7 +333,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
 
 template <int RM, int RN, int WM, int WN>
 static hipError_t launch_mx_lds(MxGemmArgs a, hipStream_t s) {
-  constexpr int kXT = WM * RM, kWT = WN * RN, kLds = (kXT + kWT) * (4 * 1024 + 2 * 256);
+  constexpr int kXT = WM * RM, kWT = WN * RN, kLds = 4096 * (kXT + kWT) + 2048 * ((kXT + 3) / 4 + kWT / 4);
   a.tiles_m = (a.mt + kXT - 1) / kXT;
   a.tiles_n = (a.nt + kWT - 1) / kWT;
   hipLaunchKernelGGL((mx_gemm_lds_kernel<RM, RN, WM, WN>),
