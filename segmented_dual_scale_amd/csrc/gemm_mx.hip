@@ -145,10 +145,11 @@ using lc = std::integral_constant<int, V>;
 // all waves have multiplied stage u - 1, and so read it: reads in flight need
 // not end before it.
 //
-// Of four neighbouring w tiles, instruction q takes rows 4 q .. 4 q + 3 of each,
-// so that its results in a lane, with those of the other three, are 16
-// neighbouring columns of y: 32 bytes a lane, 128 a row.  The copies bring them
-// into that order: every operand is read from LDS at 16 bytes a lane.
+// Of two neighbouring w tiles, instruction q takes rows 4 q .. 4 q + 3 and 8 + 4 q
+// .. 11 + 4 q of each, so that its results in a lane, with those of the other, are
+// 8 neighbouring columns of y, and a store fills 64 bytes of each of 16 rows.
+// The copies bring them into that order: every operand is read from LDS at 16
+// bytes a lane.
 template <int RM, int RN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a) {
   constexpr int kWaves = WM * WN, kXT = WM * RM, kWT = WN * RN, kTiles = kXT + kWT;
@@ -166,20 +167,21 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
 
   // this wave's copies: KiB wave, wave + kWaves, ... of a stage, x tiles first; past
   // the last of them that one again (waves that copy less would wait for less).
-  // Lane (g, r) of w's KiB 4 t + q brings block g of row 4 q + r % 4 of tile 4 t + r / 4.
+  // Lane (g, r) of w's KiB 2 t + q brings block g of the row that is row r of
+  // instruction q: 8 (r / 4 % 2) + 4 q + r % 4 of tile 2 t + r / 8.
   const uint8_t *src[kCopies];
   uint32_t piece[kCopies];
 #pragma unroll
   for (int c = 0; c < kCopies; ++c) {
-    const int t = min(c * kWaves + wave, kTiles - 1), wt = tn * kWT + ((t - kXT) & ~3);
+    const int t = min(c * kWaves + wave, kTiles - 1), wt = tn * kWT + ((t - kXT) & ~1);
     if (t < kXT) {
       src[c] = a.p.x + ((int64_t)min(tm * kXT + t, a.mt - 1) * kt << 10);
       piece[c] = lane * 16;
     } else {
-      const int first = min(wt, a.nt - 1), mine = min(wt + (r >> 2), a.nt - 1);
+      const int first = min(wt, a.nt - 1), mine = min(wt + (r >> 3), a.nt - 1);
       src[c] = a.p.w + ((int64_t)first * kt << 10);
       piece[c] = ((uint32_t)((mine - first) * kt) << 10) +
-                 (g * 16 + 4 * ((t - kXT) & 3) + (r & 3)) * 16;
+                 (g * 16 + 2 * (r & 4) + 4 * ((t - kXT) & 1) + (r & 3)) * 16;
     }
   }
   // copy c of the next stage; a uniform pointer moves on, the lane's part stays
@@ -202,8 +204,9 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
         p = a.p.x_scale + (((int64_t)min(tm * kXT + q * 4 + g, a.mt - 1) * a.ks + s) << 8) + 16 * r;
       else
         p = a.p.w_scale +
-            (((int64_t)min(tn * kWT + (q - kXS) * 4 + (r & 3), a.nt - 1) * a.ks + s) << 8) +
-            (r >> 2) * 64 + g * 16;
+            (((int64_t)min(tn * kWT + (q - kXS) * 4 + (g & 2) + (r >> 1 & 1), a.nt - 1) * a.ks + s)
+             << 8) +
+            (r >> 2) * 64 + (r & 1) * 32 + (g & 1) * 16;
       copy16(p, scale_lds + (s & 1) * kScales + q * 1024);
     }
   };
@@ -308,23 +311,19 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
     if (4 * s + 2 < kt) step(s, lc<2>{}, lc<0>{});
     if (4 * s + 3 < kt) step(s, lc<3>{}, lc<0>{});
   }
-  // lane (g, j) of x tile i: row j, columns 16 g .. 16 g + 15 of every 64
+  // lane (g, j) of x tile i: row j, columns 8 g .. 8 g + 7 of every 32
 #pragma unroll
   for (int i = 0; i < RM; ++i) {
     const int64_t m = (int64_t)(tm * kXT + wm * RM + i) * 16 + r;
     if (m >= a.p.M) continue;
 #pragma unroll
-    for (int j = 0; j < RN; j += 4) {
-      const int n = (tn * kWT + wn * RN + j + g) * 16;
+    for (int j = 0; j < RN; j += 2) {
+      const int n = (tn * kWT + wn * RN + j) * 16 + 8 * g;
       if (n >= a.p.N) continue;
-      uint16_t *y = a.p.y + m * a.p.ld_y + n;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const v4f &lo = acc[i][j + 2 * h], &hi = acc[i][j + 2 * h + 1];
-        *reinterpret_cast<v4u *>(y + 8 * h) =
-            v4u{cvt_bf16x2(lo[0], lo[1]), cvt_bf16x2(lo[2], lo[3]), cvt_bf16x2(hi[0], hi[1]),
-                cvt_bf16x2(hi[2], hi[3])};
-      }
+      const v4f &lo = acc[i][j], &hi = acc[i][j + 1];
+      *reinterpret_cast<v4u *>(a.p.y + m * a.p.ld_y + n) =
+          v4u{cvt_bf16x2(lo[0], lo[1]), cvt_bf16x2(lo[2], lo[3]), cvt_bf16x2(hi[0], hi[1]),
+              cvt_bf16x2(hi[2], hi[3])};
     }
   }
 }
