@@ -739,7 +739,8 @@ static int mx_gemm_sizes(int64_t M, int64_t N, int64_t K) {
 size_t segquant_gemm_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (mx_gemm_sizes(M, N, K)) return 0;
   ok();
-  return M ? (size_t)(sq::mx_code_bytes(M, K) + sq::mx_scale_bytes(M, K)) : 0;
+  if (M == 0 || sq::mx_quantises_inside(M, K)) return 0;
+  return (size_t)(sq::mx_code_bytes(M, K) + sq::mx_scale_bytes(M, K));
 }
 
 int segquant_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint16_t *z_bf16, int64_t ld_z,
@@ -778,6 +779,9 @@ int segquant_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint16_t *z_bf16,
                          {"w_scales", one_run(w_scales, sq::mx_scale_bytes(N, K))}};
   if ((st = check_apart(outs, ins))) return st;
   sq::MxGemmProblem p{M, N, K, x_codes, x_scales, w_codes, w_scales, y_bf16, ld_y};
+  if (z_bf16 && !need)
+    return hip_status(sq::launch_gemm_mx_bf16(p, z_bf16, ld_z, act_kind, (hipStream_t)stream),
+                      "gemm_mxfp4 launch");
   if (z_bf16) {
     uint8_t *c = static_cast<uint8_t *>(workspace), *s = c + sq::mx_code_bytes(M, K);
     const hipError_t e =

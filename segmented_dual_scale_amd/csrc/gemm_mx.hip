@@ -2,10 +2,12 @@
 //   y[m][n] = bf16( sum_b 2^(ex[m][b] + ew[n][b]) sum_{k in b} cx[m][k] cw[n][k] )
 // with the scaled 16x16x128 matrix-core instruction, which multiplies four
 // blocks of 32 by their two powers of two and adds in fp32.
+#include <cmath>
 #include <type_traits>
 
+#include "sq_activation.hpp"
 #include "sq_mx.hpp"
-#include "sq_rows.hpp"
+#include "sq_pieces.hpp"
 
 namespace sq {
 
@@ -43,68 +45,116 @@ __device__ __forceinline__ void tile_of(const MxGemmArgs &a, int &tm, int &tn) {
   tm = first + in - tn * rows;
 }
 
-// Each wave computes (16 RM) x (16 RN) of y, its operands straight from memory.
-template <int RM, int RN>
-__global__ __launch_bounds__(256) void mx_gemm_kernel(MxGemmArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int tm, tn;
-  tile_of(a, tm, tn);
-  const int m0 = (tm * 2 + (wave & 1)) * RM, n0 = (tn * 2 + (wave >> 1)) * RN;
-  const uint8_t *xp[RM], *wp[RN], *xs[RM], *ws[RN];
+// ------------------------------------------------------------- up to 16 rows --
+struct MxRowsArgs {
+  MxGemmProblem p;
+  const uint16_t *z;  // bf16 input (FUSED)
+  int64_t ld_z;
+  int32_t kt, ks;
+};
+
+// One tile of x rows, NT tiles of w columns to a workgroup whose waves take the
+// steps of 128 k in turn and add up through LDS: bound by the weight's bytes and,
+// below some megabytes of them, by latency, so a wave has four steps of weights in
+// flight before it looks at x.  FUSED (ACT as in mx_kernels.hip): each workgroup
+// quantises the few rows of z itself, to LDS.
+template <int WAVES, int NT, bool FUSED, int ACT>
+__global__ __launch_bounds__(64 * WAVES) void mx_rows_kernel(MxRowsArgs a) {
+  constexpr int P = 4;
+  extern __shared__ uint8_t smem[];
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int M = (int)a.p.M, K = (int)a.p.K, nt = (int)(a.p.N >> 4), n0 = blockIdx.x * NT;
+  const uint8_t *w[NT], *sw[NT];
 #pragma unroll
-  for (int i = 0; i < RM; ++i) {
-    const int64_t t = min(m0 + i, a.mt - 1);
-    xp[i] = a.p.x + ((t * a.kt) << 10) + 16 * lane;
-    xs[i] = a.p.x_scale + ((t * a.ks) << 8) + 4 * lane;
+  for (int j = 0; j < NT; ++j) {
+    const int64_t t = min(n0 + j, nt - 1);
+    w[j] = a.p.w + ((t * a.kt) << 10) + 16 * lane;
+    sw[j] = a.p.w_scale + ((t * a.ks) << 8) + 4 * lane;
   }
+  v4u wt[P][NT], xt[P];
+  uint32_t ws[P][NT], xs[P];
+  // steps u0, u0 + WAVES, ...; past the last one that again
+  auto load = [&](int u0) {
 #pragma unroll
-  for (int i = 0; i < RN; ++i) {
-    const int64_t t = min(n0 + i, a.nt - 1);
-    wp[i] = a.p.w + ((t * a.kt) << 10) + 16 * lane;
-    ws[i] = a.p.w_scale + ((t * a.ks) << 8) + 4 * lane;
+    for (int p = 0; p < P; ++p) {
+      const int u = min(u0 + p * WAVES, a.kt - 1);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        wt[p][j] = *reinterpret_cast<const v4u *>(w[j] + ((int64_t)u << 10));
+        ws[p][j] = *reinterpret_cast<const uint32_t *>(sw[j] + ((u >> 2) << 8));
+      }
+      if (!FUSED) {
+        xt[p] = *reinterpret_cast<const v4u *>(a.p.x + ((int64_t)u << 10) + 16 * lane);
+        xs[p] = *reinterpret_cast<const uint32_t *>(a.p.x_scale + ((u >> 2) << 8) + 4 * lane);
+      }
+    }
+  };
+  load(wave);
+  // block kb of row m at 16 (kb M + m), its scale behind all of them
+  uint8_t *const codes = smem, *const scales = smem + (K >> 5) * M * 16;
+  if (FUSED) {
+    for (int m = 0; m < M; ++m)
+      for (int k = 8 * threadIdx.x; k < K; k += 8 * 64 * WAVES) {
+        v4u v = *reinterpret_cast<const v4u *>(a.z + m * a.ld_z + k);
+        if (ACT) {
+          float f[8];
+          unpack8(v, f);
+          if (ACT == 1) silu8_hw(f);
+          if (ACT == 2) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = gelu_hw(f[i]);
+          }
+          v = pack8(f);
+        }
+        uint32_t byte;
+        const uint32_t c = mx_piece(v, byte);
+        const int at = (k >> 5) * M + m, q = k >> 3 & 3;
+        *reinterpret_cast<uint32_t *>(codes + 16 * at + 4 * q) = c;
+        if (q == 0) scales[at] = (uint8_t)byte;
+      }
+    __syncthreads();
   }
-  v4f acc[RM][RN];
+  v4f acc[NT];
 #pragma unroll
-  for (int i = 0; i < RM; ++i)
+  for (int j = 0; j < NT; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int u0 = wave; u0 < a.kt; u0 += P * WAVES) {
+    if (u0 != wave) load(u0);
 #pragma unroll
-    for (int j = 0; j < RN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = 0; s < a.ks; ++s) {
-    uint32_t sx[RM], sw[RN];
+    for (int p = 0; p < P; ++p) {
+      const int u = u0 + p * WAVES;
+      if (u >= a.kt) break;
+      v4u x = xt[p];
+      uint32_t sx;
+      if (FUSED) {
+        const int kb = 4 * u + g, at = kb * M + r;
+        x = v4u{0u, 0u, 0u, 0u};
+        sx = 0;
+        if (r < M && 32 * kb < K) {
+          x = *reinterpret_cast<const v4u *>(codes + 16 * at);
+          sx = scales[at];
+        }
+      } else {
+        sx = xs[p] >> (8 * (u & 3));
+      }
 #pragma unroll
-    for (int i = 0; i < RM; ++i) sx[i] = *reinterpret_cast<const uint32_t *>(xs[i] + ((int64_t)s << 8));
-#pragma unroll
-    for (int i = 0; i < RN; ++i) sw[i] = *reinterpret_cast<const uint32_t *>(ws[i] + ((int64_t)s << 8));
-    const int steps = min(4, a.kt - 4 * s);
-    auto step = [&](auto c) {
-      constexpr int STEP = decltype(c)::value;
-      if (STEP >= steps) return;
-      const int64_t at = (int64_t)(4 * s + STEP) << 10;
-      v4u x[RM], w[RN];
-#pragma unroll
-      for (int i = 0; i < RM; ++i) x[i] = *reinterpret_cast<const v4u *>(xp[i] + at);
-#pragma unroll
-      for (int i = 0; i < RN; ++i) w[i] = *reinterpret_cast<const v4u *>(wp[i] + at);
-#pragma unroll
-      for (int i = 0; i < RM; ++i)
-#pragma unroll
-        for (int j = 0; j < RN; ++j) acc[i][j] = mx_mfma<STEP>(w[j], sw[j], x[i], sx[i], acc[i][j]);
-    };
-    step(std::integral_constant<int, 0>{});
-    step(std::integral_constant<int, 1>{});
-    step(std::integral_constant<int, 2>{});
-    step(std::integral_constant<int, 3>{});
-  }
-#pragma unroll
-  for (int i = 0; i < RM; ++i) {
-    const int64_t m = (int64_t)(m0 + i) * 16 + (lane & 15);
-#pragma unroll
-    for (int j = 0; j < RN; ++j) {
-      const int n = (n0 + j) * 16 + 4 * (lane >> 4);
-      if (m < a.p.M && n < a.p.N)
-        *reinterpret_cast<v2u *>(a.p.y + m * a.p.ld_y + n) =
-            v2u{cvt_bf16x2(acc[i][j][0], acc[i][j][1]), cvt_bf16x2(acc[i][j][2], acc[i][j][3])};
+      for (int j = 0; j < NT; ++j)
+        acc[j] = mx_mfma<0>(wt[p][j], ws[p][j] >> (8 * (u & 3)), x, sx, acc[j]);
     }
   }
+  __syncthreads();  // all have read x
+  v4f *sums = reinterpret_cast<v4f *>(smem);
+#pragma unroll
+  for (int j = 0; j < NT; ++j) sums[(wave * NT + j) * 64 + lane] = acc[j];
+  __syncthreads();
+  if (wave >= NT) return;
+  v4f y = sums[wave * 64 + lane];
+#pragma unroll
+  for (int i = 1; i < WAVES; ++i) y += sums[(i * NT + wave) * 64 + lane];
+  const int n = (n0 + wave) * 16 + 4 * g;
+  if (r < M && n < a.p.N)
+    *reinterpret_cast<v2u *>(a.p.y + r * a.p.ld_y + n) =
+        v2u{cvt_bf16x2(y[0], y[1]), cvt_bf16x2(y[2], y[3])};
 }
 
 // ------------------------------------------------ both operands through LDS --
@@ -341,18 +391,81 @@ static hipError_t launch_mx_lds(MxGemmArgs a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Time of a product in us by tiles of some shape: workgroups beyond what fits the
+// chip at once go in further rounds, each of kt steps and what its start and end
+// cost.  step and fixed are fits to measured times from K = 128 to 12288.  A tile
+// that is alone on its CU goes in whole rounds; two on a CU overlap each other's
+// ends, so their rounds count in parts.
+struct MxTile {
+  int rows, cols;  // in tiles of 16
+  int per_cu;
+  float step, fixed;
+};
+
+static float mx_cost(const MxTile &t, const MxGemmArgs &a) {
+  const float tiles = (float)((a.mt + t.rows - 1) / t.rows) * (float)((a.nt + t.cols - 1) / t.cols);
+  float rounds = tiles / (256.0f * (float)t.per_cu);
+  if (t.per_cu == 1) rounds = ceilf(rounds);
+  return (rounds < 1.0f ? 1.0f : rounds) * ((float)a.kt * t.step + t.fixed);
+}
+
+// Measured, each against the next best (us): 9216x4608x12288 224x256 226, 256x256
+// 235, 128x128 265; 8192^3 256x256 239, 224x256 250, 128x256 276, 128x128 282;
+// 4429x4608x1536 128x128 24.9, 192x256 26.8, 256x256 29.7; 4096x1536x6144 128x256
+// 24.1, 128x128 24.6, 256x256 36.3; 1024x1536x1536 64x128 5.3, 128x128 7.0.
+constexpr MxTile kMxTiles[] = {
+    {16, 16, 1, 0.80f, 6.5f}, {14, 16, 1, 0.71f, 6.0f}, {12, 16, 1, 0.62f, 5.5f},
+    {8, 16, 1, 0.45f, 4.5f},  {8, 8, 2, 0.49f, 3.5f},   {4, 8, 2, 0.33f, 2.2f},
+};
+
+template <int WAVES, int NT>
+static hipError_t launch_rows(const MxRowsArgs &a, int32_t act, hipStream_t s) {
+  const int64_t nt = a.p.N / 16;
+  const dim3 grid((unsigned)((nt + NT - 1) / NT)), block(64 * WAVES);
+  size_t lds = sizeof(float) * 4 * 64 * NT * WAVES;
+  const size_t codes = (size_t)(a.p.M * (a.p.K / 32) * 17);
+  if (a.z && lds < codes) lds = codes;
+  if (!a.z) hipLaunchKernelGGL((mx_rows_kernel<WAVES, NT, false, 0>), grid, block, lds, s, a);
+  else if (act == 1) hipLaunchKernelGGL((mx_rows_kernel<WAVES, NT, true, 1>), grid, block, lds, s, a);
+  else if (act == 2) hipLaunchKernelGGL((mx_rows_kernel<WAVES, NT, true, 2>), grid, block, lds, s, a);
+  else hipLaunchKernelGGL((mx_rows_kernel<WAVES, NT, true, 0>), grid, block, lds, s, a);
+  return hipGetLastError();
+}
+
+// Up to 16 rows.  Two column tiles a workgroup where that leaves a workgroup per
+// CU; as many waves as leave each two steps of K and the chip about 4096.
+static hipError_t launch_mx_rows(const MxGemmProblem &p, const uint16_t *z, int64_t ld_z,
+                                 int32_t act, hipStream_t s) {
+  const MxRowsArgs a{p, z, ld_z, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K)};
+  const int64_t nt = p.N / 16;
+  if (nt >= 512) return a.kt >= 16 ? launch_rows<8, 2>(a, act, s) : launch_rows<4, 2>(a, act, s);
+  if (a.kt >= 32 && nt <= 256) return launch_rows<16, 1>(a, act, s);
+  return a.kt >= 16 ? launch_rows<8, 1>(a, act, s) : launch_rows<4, 1>(a, act, s);
+}
+
+// Every workgroup would quantise all of z again.
+bool mx_quantises_inside(int64_t M, int64_t K) { return M <= 16 && M * K <= 8192; }
+
+hipError_t launch_gemm_mx_bf16(const MxGemmProblem &p, const uint16_t *z, int64_t ld_z, int32_t act,
+                               hipStream_t s) {
+  return launch_mx_rows(p, z, ld_z, act, s);
+}
+
 hipError_t launch_gemm_mx(const MxGemmProblem &p, hipStream_t s) {
-  MxGemmArgs a{p, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K),
-               (int32_t)mx_row_tiles(p.M), (int32_t)mx_row_tiles(p.N), 0, 0};
-  const int64_t big = (int64_t)((a.mt + 15) / 16) * ((a.nt + 15) / 16);
-  if (p.M <= 64) {
-    a.tiles_m = (a.mt + 7) / 8;
-    a.tiles_n = (a.nt + 7) / 8;
-    hipLaunchKernelGGL((mx_gemm_kernel<4, 4>), dim3((unsigned)(a.tiles_m * (int64_t)a.tiles_n)),
-                       dim3(256), 0, s, a);
-    return hipGetLastError();
+  if (p.M <= 16) return launch_mx_rows(p, nullptr, 0, 0, s);
+  const MxGemmArgs a{p, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K),
+                     (int32_t)mx_row_tiles(p.M), (int32_t)mx_row_tiles(p.N), 0, 0};
+  int best = 0;
+  for (int i = 1; i < (int)(sizeof kMxTiles / sizeof kMxTiles[0]); ++i)
+    if (mx_cost(kMxTiles[i], a) < mx_cost(kMxTiles[best], a)) best = i;
+  switch (best) {
+    case 0: return launch_mx_lds<8, 4, 2, 4>(a, s);
+    case 1: return launch_mx_lds<7, 4, 2, 4>(a, s);
+    case 2: return launch_mx_lds<6, 4, 2, 4>(a, s);
+    case 3: return launch_mx_lds<4, 4, 2, 4>(a, s);
+    case 4: return launch_mx_lds<4, 4, 2, 2>(a, s);
+    default: return launch_mx_lds<2, 4, 2, 2>(a, s);
   }
-  return big >= 200 ? launch_mx_lds<8, 4, 2, 4>(a, s) : launch_mx_lds<4, 4, 2, 2>(a, s);
 }
 
 }  // namespace sq

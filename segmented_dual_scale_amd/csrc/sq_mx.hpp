@@ -52,6 +52,11 @@ struct MxGemmProblem {
 };
 
 hipError_t launch_gemm_mx(const MxGemmProblem &p, hipStream_t s);
+// Whether the product of bf16 input of this size quantises it itself, and that
+// product (x and x_scale of the problem unused).
+bool mx_quantises_inside(int64_t M, int64_t K);
+hipError_t launch_gemm_mx_bf16(const MxGemmProblem &p, const uint16_t *z, int64_t ld_z, int32_t act,
+                               hipStream_t s);
 
 // ------------------------------------------------------- device helpers --
 // The biased power of two of a block whose largest magnitude has these bf16 or
