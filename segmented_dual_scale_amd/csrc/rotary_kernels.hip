@@ -5,9 +5,9 @@
 //   pair i turns by the angle position[axis(i)] * freq[i]:
 //   a' = a cos - b sin,  b' = b cos + a sin
 //
-// Bound by memory: q and k read once and written once.  A wave takes the heads
-// of one token, so the token's angles are worked out once, one pair to a lane,
-// and shared through LDS.  The angle is reduced in fp64 pairs (the product of
+// Bound by memory: q and k read once and written once.  A wave takes heads of one
+// token, so the token's angles are worked out once, one pair to a lane, and
+// shared through LDS.  The angle is reduced in fp64 pairs (the product of
 // a position and a frequency, in turns, less its nearest quarter), so positions
 // up to 2^31 lose nothing; sine and cosine of what is left, at most pi/4, are
 // their Taylor polynomials to x^9 and x^8, off by less than 2^-25.
@@ -43,82 +43,102 @@ __device__ __forceinline__ float2 turn(int position, double freq) {
 // LPH lanes share a head, a unit of two 8-element pieces (eight pairs) each:
 // neighbouring pieces where pairs are neighbours, else the pieces half a turned
 // part apart; behind the R turned elements, neighbouring pieces again.  A wave
-// takes U times 64 / LPH heads of its token.
+// takes up to U times 64 / LPH heads of q or of k of one token: what depends on the
+// token alone (addresses, angles) is uniform or shared, and the weights of the norm
+// are multiplied into sine and cosine, four factors a pair, ahead of the heads.
 template <int LPH, int U, bool HALVES>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryProblem a) {
   __shared__ float2 angles[4][8 * LPH];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int kHeads = 64 / LPH;
-  const int64_t item = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + wave;
-  const int64_t token = item / a.chunks;
-  if (token >= a.B * a.L) return;  // whole waves; no barrier follows
-  const int chunk = (int)(item - token * a.chunks);
-  const int64_t b = token / a.L, l = token - b * a.L;
-  const int u = lane % LPH, sub = lane / LPH;
-  const int turned = a.R / 16;  // units that turn
-  const int lo = u < turned && HALVES ? 8 * u : 16 * u;
-  const int hi = u < turned && HALVES ? lo + a.R / 2 : lo + 8;
+  // uniform, below 2^32
+  const uint32_t item = (blockIdx.y * gridDim.x + blockIdx.x) * 4 + wave;
+  const uint32_t token = item / (uint32_t)a.chunks;
+  if (token >= (uint32_t)(a.B * a.L)) return;  // whole waves; no barrier follows
+  const int chunk = (int)(item - token * (uint32_t)a.chunks);
+  const uint32_t b = token / (uint32_t)a.L, l = token - b * (uint32_t)a.L;
+  const RotaryTensor &t = chunk < a.q_chunks ? a.q : a.k;
+  const int h0 = (chunk < a.q_chunks ? chunk : chunk - a.q_chunks) * U * kHeads + lane / LPH;
+  const uint16_t *in = t.in + b * t.in_stride[0] + l * t.in_stride[1];
+  uint16_t *out = t.out + b * t.out_stride[0] + l * t.out_stride[1];
+  const int u = lane % LPH;
+  const bool turns = u < a.R / 16;
+  const int lo = turns && HALVES ? 8 * u : 16 * u, hi = turns && HALVES ? lo + a.R / 2 : lo + 8;
   const bool has_lo = lo < a.D, has_hi = hi < a.D;
   v4u x[U][2];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const int h = (chunk * U + i) * kHeads + sub;
-    const RotaryTensor &t = h < a.q.heads ? a.q : a.k;
-    const int hh = h < a.q.heads ? h : h - a.q.heads;
-    const uint16_t *p = t.in + b * t.in_stride[0] + l * t.in_stride[1] + hh * t.in_stride[2];
+    const int h = h0 + i * kHeads;
+    const uint16_t *p = in + h * t.in_stride[2];
     x[i][0] = x[i][1] = v4u{0u, 0u, 0u, 0u};
-    if (hh < t.heads && has_lo) x[i][0] = *reinterpret_cast<const v4u *>(p + lo);
-    if (hh < t.heads && has_hi) x[i][1] = *reinterpret_cast<const v4u *>(p + hi);
+    if (h < t.heads && has_lo) x[i][0] = *reinterpret_cast<const v4u *>(p + lo);
+    if (h < t.heads && has_hi) x[i][1] = *reinterpret_cast<const v4u *>(p + hi);
   }
+  float g[16];
+  load8f<false>(t.gamma ? t.gamma + lo : nullptr, has_lo ? 8 : 0, 1.0f, g);
+  load8f<false>(t.gamma ? t.gamma + hi : nullptr, has_hi ? 8 : 0, 1.0f, g + 8);
+  const int32_t *pos = a.positions + b * a.pos_batch + (int64_t)l * a.n_axes;
   for (int i = lane; i < a.R / 2; i += 64) {
     int axis = 0;
     while (axis + 1 < a.n_axes && i >= a.axis_end[axis]) ++axis;
-    angles[wave][i] = turn(a.positions[b * a.pos_batch + l * a.n_axes + axis], a.freq[i]);
+    angles[wave][i] = turn(pos[axis], a.freq[i]);
   }
   __builtin_amdgcn_wave_barrier();  // the wave's own LDS accesses keep their order
-  float2 cs[8];
+  // element e of the unit turns with its partner: HALVES j and 8 + j, else 2 j and 2 j + 1
+  constexpr int A = HALVES ? 1 : 2, B = HALVES ? 8 : 1;
+  float ca[8], sb[8], cb[8], sa[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    cs[j] = u < turned ? angles[wave][8 * u + j] : make_float2(1.0f, 0.0f);
+  for (int j = 0; j < 8; ++j) {
+    const float2 cs = turns ? angles[wave][8 * u + j] : make_float2(1.0f, 0.0f);
+    ca[j] = cs.x * g[A * j];
+    sa[j] = cs.y * g[A * j];
+    cb[j] = cs.x * g[A * j + B];
+    sb[j] = cs.y * g[A * j + B];
+  }
+  const float inv_d = 1.0f / (float)a.D;
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const int h = (chunk * U + i) * kHeads + sub;
-    const RotaryTensor &t = h < a.q.heads ? a.q : a.k;
-    const int hh = h < a.q.heads ? h : h - a.q.heads;
+    const int h = h0 + i * kHeads;
     float f[16];
     unpack8(x[i][0], f);
     unpack8(x[i][1], f + 8);
+    float rstd = 1.0f;
     if (a.norm) {
       float s = 0.0f;
 #pragma unroll
       for (int j = 0; j < 16; ++j) s = __builtin_fmaf(f[j], f[j], s);
-      const float rstd = __builtin_amdgcn_rsqf(part_sum(s, LPH) / (float)a.D + a.eps);
-      float g[16];
-      load8f<false>(t.gamma ? t.gamma + lo : nullptr, has_lo ? 8 : 0, 1.0f, g);
-      load8f<false>(t.gamma ? t.gamma + hi : nullptr, has_hi ? 8 : 0, 1.0f, g + 8);
+      rstd = __builtin_amdgcn_rsqf(part_sum(s, LPH) * inv_d + a.eps);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) f[j] = f[j] * rstd * g[j];
+      for (int j = 0; j < 16; ++j) f[j] *= rstd;
     }
+    float o[16];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float &p = HALVES && u < turned ? f[j] : f[2 * j];
-      float &r = HALVES && u < turned ? f[8 + j] : f[2 * j + 1];
-      const float pa = p, pb = r;
-      p = pa * cs[j].x - pb * cs[j].y;
-      r = pb * cs[j].x + pa * cs[j].y;
+      const float p = f[A * j], r = f[A * j + B];
+      o[A * j] = __builtin_fmaf(p, ca[j], -(r * sb[j]));
+      o[A * j + B] = __builtin_fmaf(r, cb[j], p * sa[j]);
     }
-    if (hh >= t.heads) continue;
-    uint16_t *o = t.out + b * t.out_stride[0] + l * t.out_stride[1] + hh * t.out_stride[2];
-    if (has_lo) *reinterpret_cast<v4u *>(o + lo) = pack8(f);
-    if (has_hi) *reinterpret_cast<v4u *>(o + hi) = pack8(f + 8);
+    if (a.R < a.D && !turns) {  // not through 0 times a partner that may be infinite
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        o[A * j] = f[A * j] * ca[j];
+        o[A * j + B] = f[A * j + B] * cb[j];
+      }
+    }
+    if (h >= t.heads) continue;
+    uint16_t *p = out + h * t.out_stride[2];
+    if (has_lo) *reinterpret_cast<v4u *>(p + lo) = pack8(o);
+    if (has_hi) *reinterpret_cast<v4u *>(p + hi) = pack8(o + 8);
   }
 }
 
 template <int LPH, int U>
 void launch_rotary_u(const RotaryProblem &p, hipStream_t s) {
   RotaryProblem a = p;
-  const int heads = a.q.heads + a.k.heads, per = U * (64 / LPH);
-  a.chunks = (heads + per - 1) / per;
+  constexpr int per = U * (64 / LPH);
+  a.q_chunks = (a.q.heads + per - 1) / per;
+  a.chunks = a.q_chunks + (a.k.heads + per - 1) / per;
   // a grid dimension holds 2^32 threads
   const int64_t blocks = (a.B * a.L * a.chunks + 3) / 4, rows = (blocks + (1 << 20) - 1) >> 20;
   const dim3 grid((unsigned)((blocks + rows - 1) / rows), (unsigned)rows);
@@ -128,13 +148,12 @@ void launch_rotary_u(const RotaryProblem &p, hipStream_t s) {
 
 template <int LPH>
 void launch_rotary_lph(const RotaryProblem &a, hipStream_t s) {
-  const int64_t steps = (a.q.heads + a.k.heads + 64 / LPH - 1) / (64 / LPH);
+  constexpr int per = 64 / LPH;
+  const int steps = ((a.q.heads > a.k.heads ? a.q.heads : a.k.heads) + per - 1) / per;
   // few tokens: more waves rather than more heads a wave
-  const int64_t waves = a.B * a.L * steps;
-  if (waves <= 4096 || steps == 1) launch_rotary_u<LPH, 1>(a, s);
+  if (steps == 1 || a.B * a.L * steps <= 2048) launch_rotary_u<LPH, 1>(a, s);
   else if (steps % 3 == 0) launch_rotary_u<LPH, 3>(a, s);
-  else if (steps == 2) launch_rotary_u<LPH, 2>(a, s);
-  else launch_rotary_u<LPH, 4>(a, s);
+  else launch_rotary_u<LPH, 2>(a, s);
 }
 
 }  // namespace

@@ -119,7 +119,7 @@ struct RotaryProblem {
   const double *freq;        // [R / 2]
   int32_t n_axes;
   int32_t axis_end[kMaxAxes];  // in pairs
-  int32_t chunks;  // waves per token, filled in by the launch
+  int32_t q_chunks, chunks;  // waves per token for q, for both; filled in by the launch
 };
 
 hipError_t launch_rotary(const RotaryProblem &p, hipStream_t s);

@@ -221,3 +221,16 @@ def test_the_chain_of_a_block():
     close(q, *want[0])
     close(k, *want[1])
     assert torch.equal(t[0, :, 2].reshape(M, -1), y[:, 2 * H * D:])
+
+
+@pytest.mark.parametrize("style", [PAIRS, HALVES])
+def test_elements_that_do_not_turn_keep_to_themselves(style):
+    """Without the norm, an infinity or a NaN behind the turned part is one element's."""
+    g = gen(12)
+    q = normal(g, 1, 3, 2, 64).to(BF)
+    q[0, 1, 1, 40], q[0, 1, 1, 51] = float("inf"), float("nan")
+    pos = torch.randint(0, 99, (3, 1), generator=g, device=DEV, dtype=torch.int32)
+    freq = S.segquant_rotary_frequencies([32]).to(DEV)
+    out = S.segquant_qk_rotary(q, None, pos, freq, [32], style, norm=False)[0]
+    assert torch.equal(out[..., 32:].view(torch.int16), q[..., 32:].view(torch.int16))
+    assert not out[..., :32].isnan().any()
