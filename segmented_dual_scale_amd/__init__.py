@@ -904,14 +904,21 @@ def segquant_rotary_frequencies(widths: Sequence[int], theta: float = 10000.0):
     return freq
 
 
+@functools.lru_cache(maxsize=1024)
+def _stride_array(stride):
+    a = (ctypes.c_int64 * 3)(*stride[:3])
+    return ctypes.addressof(a), a  # the address belongs to the array
+
+
 def _head_strides(t, name: str, shape, at: int):
     """A [B][L][heads][D] tensor (None: not given) -> its address and strides."""
     import torch
     if t is None:
         return None, None
-    if t.dim() != 4 or t.stride(3) != 1 and t.shape[3] > 1 and t.numel():
-        raise ValueError(f"{name} must be 4-D with unit stride in its last dimension")
-    return (_want(t, name, torch.bfloat16, shape, at), (ctypes.c_int64 * 3)(*t.stride()[:3]))
+    ptr, stride = _want(t, name, torch.bfloat16, shape, at), t.stride()
+    if stride[3] != 1 and shape[3] > 1 and t.numel():
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    return ptr, _stride_array(stride)[0]
 
 
 def segquant_qk_rotary(q, k, positions, freq, widths: Sequence[int],
@@ -949,16 +956,13 @@ def segquant_qk_rotary(q, k, positions, freq, widths: Sequence[int],
     else:
         pos, per = _want_array(positions, "positions", torch.int32, (L, n), at), 0
     f32 = torch.float32
-    _check(_on(at, fn, B, L, D, *_with_heads(q, "q", q.shape, Hq, at),
-               *_head_strides(q_out, "q_out", q.shape, at), *_with_heads(k, "k", k_shape, Hk, at),
-               *_head_strides(k_out, "k_out", k_shape, at), int(bool(norm)), eps,
+    q_ptr, q_stride = _head_strides(q, "q", q.shape, at)
+    k_ptr, k_stride = _head_strides(k, "k", k_shape, at)
+    _check(_on(at, fn, B, L, D, q_ptr, Hq, q_stride, *_head_strides(q_out, "q_out", q.shape, at),
+               k_ptr, Hk, k_stride, *_head_strides(k_out, "k_out", k_shape, at), int(bool(norm)), eps,
                _want_array(q_gamma, "q_gamma", f32, (D,), at),
                _want_array(k_gamma, "k_gamma", f32, (D,), at), pos, per, n, axes,
                _want_array(freq, "freq", torch.float64, (R // 2,), at), style),
            "segquant_qk_rotary")
     return q_out, k_out
 
-
-def _with_heads(t, name: str, shape, heads: int, at: int):
-    ptr, strides = _head_strides(t, name, shape, at)
-    return ptr, heads, strides

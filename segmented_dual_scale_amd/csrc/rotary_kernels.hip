@@ -46,7 +46,8 @@ __device__ __forceinline__ float2 turn(int position, double freq) {
 // takes up to U times 64 / LPH heads of q or of k of one token: what depends on the
 // token alone (addresses, angles) is uniform or shared, and the weights of the norm
 // are multiplied into sine and cosine, four factors a pair, ahead of the heads.
-template <int LPH, int U, bool HALVES>
+// WHOLE: the units are all there and all turn (R = D = 16 LPH).
+template <int LPH, int U, bool HALVES, bool WHOLE>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryProblem a) {
   __shared__ float2 angles[4][8 * LPH];
   const int lane = threadIdx.x & 63;
@@ -63,23 +64,24 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryProblem a) {
   const uint16_t *in = t.in + b * t.in_stride[0] + l * t.in_stride[1];
   uint16_t *out = t.out + b * t.out_stride[0] + l * t.out_stride[1];
   const int u = lane % LPH;
-  const bool turns = u < a.R / 16;
-  const int lo = turns && HALVES ? 8 * u : 16 * u, hi = turns && HALVES ? lo + a.R / 2 : lo + 8;
-  const bool has_lo = lo < a.D, has_hi = hi < a.D;
+  const int R = WHOLE ? 16 * LPH : a.R;
+  const bool turns = WHOLE || u < R / 16;
+  const int lo = turns && HALVES ? 8 * u : 16 * u, hi = turns && HALVES ? lo + R / 2 : lo + 8;
+  const bool has_lo = WHOLE || lo < a.D, has_hi = WHOLE || hi < a.D;
   v4u x[U][2];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const int h = h0 + i * kHeads;
+    const int h = min(h0 + i * kHeads, t.heads - 1);  // past the last head that one again
     const uint16_t *p = in + h * t.in_stride[2];
-    x[i][0] = x[i][1] = v4u{0u, 0u, 0u, 0u};
-    if (h < t.heads && has_lo) x[i][0] = *reinterpret_cast<const v4u *>(p + lo);
-    if (h < t.heads && has_hi) x[i][1] = *reinterpret_cast<const v4u *>(p + hi);
+    if (!WHOLE) x[i][0] = x[i][1] = v4u{0u, 0u, 0u, 0u};
+    if (has_lo) x[i][0] = *reinterpret_cast<const v4u *>(p + lo);
+    if (has_hi) x[i][1] = *reinterpret_cast<const v4u *>(p + hi);
   }
   float g[16];
   load8f<false>(t.gamma ? t.gamma + lo : nullptr, has_lo ? 8 : 0, 1.0f, g);
   load8f<false>(t.gamma ? t.gamma + hi : nullptr, has_hi ? 8 : 0, 1.0f, g + 8);
   const int32_t *pos = a.positions + b * a.pos_batch + (int64_t)l * a.n_axes;
-  for (int i = lane; i < a.R / 2; i += 64) {
+  for (int i = lane; i < R / 2; i += 64) {
     int axis = 0;
     while (axis + 1 < a.n_axes && i >= a.axis_end[axis]) ++axis;
     angles[wave][i] = turn(pos[axis], a.freq[i]);
@@ -103,15 +105,13 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryProblem a) {
     float f[16];
     unpack8(x[i][0], f);
     unpack8(x[i][1], f + 8);
-    float rstd = 1.0f;
-    if (a.norm) {
-      float s = 0.0f;
+    float s = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) s = __builtin_fmaf(f[j], f[j], s);
-      rstd = __builtin_amdgcn_rsqf(part_sum(s, LPH) * inv_d + a.eps);
+    for (int j = 0; j < 16; ++j) s = __builtin_fmaf(f[j], f[j], s);
+    s = __builtin_amdgcn_rsqf(part_sum(s, LPH) * inv_d + a.eps);
+    const float rstd = a.norm ? s : 1.0f;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) f[j] *= rstd;
-    }
+    for (int j = 0; j < 16; ++j) f[j] *= rstd;
     float o[16];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -119,7 +119,7 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryProblem a) {
       o[A * j] = __builtin_fmaf(p, ca[j], -(r * sb[j]));
       o[A * j + B] = __builtin_fmaf(r, cb[j], p * sa[j]);
     }
-    if (a.R < a.D && !turns) {  // not through 0 times a partner that may be infinite
+    if (!WHOLE && !turns) {  // not through 0 times a partner that may be infinite
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         o[A * j] = f[A * j] * ca[j];
@@ -142,8 +142,14 @@ void launch_rotary_u(const RotaryProblem &p, hipStream_t s) {
   // a grid dimension holds 2^32 threads
   const int64_t blocks = (a.B * a.L * a.chunks + 3) / 4, rows = (blocks + (1 << 20) - 1) >> 20;
   const dim3 grid((unsigned)((blocks + rows - 1) / rows), (unsigned)rows);
-  if (a.halves) hipLaunchKernelGGL((rotary_kernel<LPH, U, true>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((rotary_kernel<LPH, U, false>), grid, dim3(256), 0, s, a);
+  const bool whole = a.R == a.D && a.D == 16 * LPH;
+#define SQ_ROTARY(HALVES, WHOLE) \
+  hipLaunchKernelGGL((rotary_kernel<LPH, U, HALVES, WHOLE>), grid, dim3(256), 0, s, a)
+  if (a.halves && whole) SQ_ROTARY(true, true);
+  else if (a.halves) SQ_ROTARY(true, false);
+  else if (whole) SQ_ROTARY(false, true);
+  else SQ_ROTARY(false, false);
+#undef SQ_ROTARY
 }
 
 template <int LPH>
