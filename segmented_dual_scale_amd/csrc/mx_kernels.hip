@@ -45,7 +45,7 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(MxQuantArgs a) {
       if (ACT == 1) silu8_hw(f);
       if (ACT == 2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = gelu_hw(f[i]);
+        for (int i = 0; i < 8; ++i) f[i] = gelu_bf16(f[i]);
       }
       x[s] = pack8(f);
     }

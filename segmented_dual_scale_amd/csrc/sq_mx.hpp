@@ -110,14 +110,17 @@ __device__ __forceinline__ uint32_t mx_piece(v4u v, uint32_t &byte) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7fffu, v[j] >> 16 & 0x7fffu));
   byte = mx_scale_byte(quad_max(top) >> 7);
-  const float inv = mx_inverse(byte);
-  float f[8];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    f[2 * j] = bf16_lo(v[j]) * inv;
-    f[2 * j + 1] = bf16_hi(v[j]) * inv;
-  }
-  return mx_codes8(f);
+  // the conversion divides by the power of two in its scale's exponent bits (2^-127
+  // for 0), exactly, and rounds as mx_codes8
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  const float scale = __uint_as_float(byte << 23);
+  const uint32_t x0 = v[0], x1 = v[1], x2 = v[2], x3 = v[3];
+  uint32_t c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(v2bf, x0), scale, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(v2bf, x1), scale, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(v2bf, x2), scale, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(v2bf, x3), scale, 3);
+  return c;
 }
 
 __device__ __forceinline__ void mx_emit8(const MxOut &o, int64_t row, int k, v4u v) {
