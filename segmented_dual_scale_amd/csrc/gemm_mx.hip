@@ -53,27 +53,34 @@ struct MxRowsArgs {
   int32_t kt, ks;
 };
 
-// One tile of x rows, NT tiles of w columns to a workgroup whose waves take the
-// steps of 128 k in turn and add up through LDS: bound by the weight's bytes and,
-// below some megabytes of them, by latency, so a wave has four steps of weights in
-// flight before it looks at x.  FUSED (ACT as in mx_kernels.hip): each workgroup
-// quantises the few rows of z itself, to LDS.
-template <int WAVES, int NT, bool FUSED, int ACT>
+// MT tiles of x rows and NT tiles of w columns to a workgroup, whose waves take
+// the steps of 128 k in turn and add up through LDS: bound by the weight's bytes
+// and, below some megabytes of them, by latency, so a wave has P steps of weights
+// in flight before it looks at x.  FUSED (MT = 1; ACT as in mx_kernels.hip): each
+// workgroup quantises the few rows of z itself, to LDS.
+template <int WAVES, int MT, int NT, bool FUSED, int ACT>
 __global__ __launch_bounds__(64 * WAVES) void mx_rows_kernel(MxRowsArgs a) {
-  constexpr int P = 4;
+  constexpr int P = MT == 1 ? 4 : 3;
   extern __shared__ uint8_t smem[];
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int M = (int)a.p.M, K = (int)a.p.K, nt = (int)(a.p.N >> 4), n0 = blockIdx.x * NT;
-  const uint8_t *w[NT], *sw[NT];
+  const int mt = (M + 15) >> 4, m0 = blockIdx.y * MT;
+  const uint8_t *w[NT], *sw[NT], *x[MT], *sx[MT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int64_t t = min(n0 + j, nt - 1);
     w[j] = a.p.w + ((t * a.kt) << 10) + 16 * lane;
     sw[j] = a.p.w_scale + ((t * a.ks) << 8) + 4 * lane;
   }
-  v4u wt[P][NT], xt[P];
-  uint32_t ws[P][NT], xs[P];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t t = min(m0 + i, mt - 1);
+    x[i] = a.p.x + ((t * a.kt) << 10) + 16 * lane;
+    sx[i] = a.p.x_scale + ((t * a.ks) << 8) + 4 * lane;
+  }
+  v4u wt[P][NT], xt[P][MT];
+  uint32_t ws[P][NT], xs[P][MT];
   // steps u0, u0 + WAVES, ...; past the last one that again
   auto load = [&](int u0) {
 #pragma unroll
@@ -85,8 +92,11 @@ __global__ __launch_bounds__(64 * WAVES) void mx_rows_kernel(MxRowsArgs a) {
         ws[p][j] = *reinterpret_cast<const uint32_t *>(sw[j] + ((u >> 2) << 8));
       }
       if (!FUSED) {
-        xt[p] = *reinterpret_cast<const v4u *>(a.p.x + ((int64_t)u << 10) + 16 * lane);
-        xs[p] = *reinterpret_cast<const uint32_t *>(a.p.x_scale + ((u >> 2) << 8) + 4 * lane);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          xt[p][i] = *reinterpret_cast<const v4u *>(x[i] + ((int64_t)u << 10));
+          xs[p][i] = *reinterpret_cast<const uint32_t *>(sx[i] + ((u >> 2) << 8));
+        }
       }
     }
   };
@@ -115,46 +125,54 @@ __global__ __launch_bounds__(64 * WAVES) void mx_rows_kernel(MxRowsArgs a) {
       }
     __syncthreads();
   }
-  v4f acc[NT];
+  v4f acc[MT][NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   for (int u0 = wave; u0 < a.kt; u0 += P * WAVES) {
     if (u0 != wave) load(u0);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int u = u0 + p * WAVES;
       if (u >= a.kt) break;
-      v4u x = xt[p];
-      uint32_t sx;
-      if (FUSED) {
-        const int kb = 4 * u + g, at = kb * M + r;
-        x = v4u{0u, 0u, 0u, 0u};
-        sx = 0;
-        if (r < M && 32 * kb < K) {
-          x = *reinterpret_cast<const v4u *>(codes + 16 * at);
-          sx = scales[at];
-        }
-      } else {
-        sx = xs[p] >> (8 * (u & 3));
-      }
+      const int shift = 8 * (u & 3);
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        acc[j] = mx_mfma<0>(wt[p][j], ws[p][j] >> (8 * (u & 3)), x, sx, acc[j]);
+      for (int i = 0; i < MT; ++i) {
+        v4u c = xt[p][i];
+        uint32_t s = xs[p][i] >> shift;
+        if (FUSED) {
+          const int kb = 4 * u + g, at = kb * M + r;
+          c = v4u{0u, 0u, 0u, 0u};
+          s = 0;
+          if (r < M && 32 * kb < K) {
+            c = *reinterpret_cast<const v4u *>(codes + 16 * at);
+            s = scales[at];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          acc[i][j] = mx_mfma<0>(wt[p][j], ws[p][j] >> shift, c, s, acc[i][j]);
+      }
     }
   }
   __syncthreads();  // all have read x
   v4f *sums = reinterpret_cast<v4f *>(smem);
 #pragma unroll
-  for (int j = 0; j < NT; ++j) sums[(wave * NT + j) * 64 + lane] = acc[j];
-  __syncthreads();
-  if (wave >= NT) return;
-  v4f y = sums[wave * 64 + lane];
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
-  for (int i = 1; i < WAVES; ++i) y += sums[(i * NT + wave) * 64 + lane];
-  const int n = (n0 + wave) * 16 + 4 * g;
-  if (r < M && n < a.p.N)
-    *reinterpret_cast<v2u *>(a.p.y + r * a.p.ld_y + n) =
-        v2u{cvt_bf16x2(y[0], y[1]), cvt_bf16x2(y[2], y[3])};
+    for (int j = 0; j < NT; ++j) sums[((wave * MT + i) * NT + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  for (int t = wave; t < MT * NT; t += WAVES) {
+    v4f y = sums[t * 64 + lane];
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) y += sums[(i * MT * NT + t) * 64 + lane];
+    const int64_t m = (int64_t)(m0 + t / NT) * 16 + r;
+    const int n = (n0 + t % NT) * 16 + 4 * g;
+    if (m < M && n < a.p.N)
+      *reinterpret_cast<v2u *>(a.p.y + m * a.p.ld_y + n) =
+          v2u{cvt_bf16x2(y[0], y[1]), cvt_bf16x2(y[2], y[3])};
+  }
 }
 
 // ------------------------------------------------ both operands through LDS --
@@ -395,7 +413,7 @@ static hipError_t launch_mx_lds(MxGemmArgs a, hipStream_t s) {
 // chip at once go in further rounds, each of kt steps and what its start and end
 // cost.  step and fixed are fits to measured times from K = 128 to 12288.  A tile
 // that is alone on its CU goes in whole rounds; two on a CU overlap each other's
-// ends, so their rounds count in parts.
+// ends, so their rounds count in parts, and steps are shorter while CUs are free.
 struct MxTile {
   int rows, cols;  // in tiles of 16
   int per_cu;
@@ -404,60 +422,85 @@ struct MxTile {
 
 static float mx_cost(const MxTile &t, const MxGemmArgs &a) {
   const float tiles = (float)((a.mt + t.rows - 1) / t.rows) * (float)((a.nt + t.cols - 1) / t.cols);
+  const float kt = (float)a.kt;
   float rounds = tiles / (256.0f * (float)t.per_cu);
-  if (t.per_cu == 1) rounds = ceilf(rounds);
-  return (rounds < 1.0f ? 1.0f : rounds) * ((float)a.kt * t.step + t.fixed);
+  if (t.per_cu == 1) return ceilf(rounds) * (kt * t.step + t.fixed);
+  if (rounds < 1.0f) return kt * t.step * (0.6f + 0.4f * rounds) + t.fixed;
+  return rounds * (kt * t.step + t.fixed);
+}
+
+// The same by workgroups of 32 x 32 that split K over their waves: 4 KiB a step
+// and workgroup from the L2 at 22 TB/s, and a chain of loads for each of a wave's
+// steps.
+static int mx_rows_waves(int64_t kt) { return kt >= 16 ? 8 : 4; }
+
+static float mx_rows_cost(const MxGemmArgs &a) {
+  const float groups = (float)((a.mt + 1) / 2) * (float)((a.nt + 1) / 2), kt = (float)a.kt;
+  return 2.0f + groups * kt * (4096.0f / 22e6f) + 0.25f * kt / (float)mx_rows_waves(a.kt);
 }
 
 // Measured, each against the next best (us): 9216x4608x12288 224x256 226, 256x256
 // 235, 128x128 265; 8192^3 256x256 239, 224x256 250, 128x256 276, 128x128 282;
 // 4429x4608x1536 128x128 24.9, 192x256 26.8, 256x256 29.7; 4096x1536x6144 128x256
-// 24.1, 128x128 24.6, 256x256 36.3; 1024x1536x1536 64x128 5.3, 128x128 7.0.
+// 24.1, 128x128 24.6, 256x256 36.3; 1024x1536x1536 64x128 5.4, split K 5.8, 128x128
+// 6.8; 256x1536x6144 split K 6.2, 64x128 10.4; 600x4096x4096 128x128 12.3, 64x128
+// 12.6, split K 16.3.
 constexpr MxTile kMxTiles[] = {
     {16, 16, 1, 0.80f, 6.5f}, {14, 16, 1, 0.71f, 6.0f}, {12, 16, 1, 0.62f, 5.5f},
     {8, 16, 1, 0.45f, 4.5f},  {8, 8, 2, 0.49f, 3.5f},   {4, 8, 2, 0.33f, 2.2f},
 };
 
-template <int WAVES, int NT>
-static hipError_t launch_rows(const MxRowsArgs &a, int32_t act, hipStream_t s) {
-  const int64_t nt = a.p.N / 16;
-  const dim3 grid((unsigned)((nt + NT - 1) / NT)), block(64 * WAVES);
-  size_t lds = sizeof(float) * 4 * 64 * NT * WAVES;
-  const size_t codes = (size_t)(a.p.M * (a.p.K / 32) * 17);
-  if (a.z && lds < codes) lds = codes;
-  if (!a.z) hipLaunchKernelGGL((mx_rows_kernel<WAVES, NT, false, 0>), grid, block, lds, s, a);
-  else if (act == 1) hipLaunchKernelGGL((mx_rows_kernel<WAVES, NT, true, 1>), grid, block, lds, s, a);
-  else if (act == 2) hipLaunchKernelGGL((mx_rows_kernel<WAVES, NT, true, 2>), grid, block, lds, s, a);
-  else hipLaunchKernelGGL((mx_rows_kernel<WAVES, NT, true, 0>), grid, block, lds, s, a);
+template <int WAVES, int MT, int NT>
+static hipError_t launch_rows(const MxGemmProblem &p, hipStream_t s) {
+  const MxRowsArgs a{p, nullptr, 0, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K)};
+  const int64_t nt = p.N / 16, mt = mx_row_tiles(p.M);
+  hipLaunchKernelGGL((mx_rows_kernel<WAVES, MT, NT, false, 0>),
+                     dim3((unsigned)((nt + NT - 1) / NT), (unsigned)((mt + MT - 1) / MT)),
+                     dim3(64 * WAVES), sizeof(float) * 4 * 64 * MT * NT * WAVES, s, a);
   return hipGetLastError();
 }
 
 // Up to 16 rows.  Two column tiles a workgroup where that leaves a workgroup per
 // CU; as many waves as leave each two steps of K and the chip about 4096.
-static hipError_t launch_mx_rows(const MxGemmProblem &p, const uint16_t *z, int64_t ld_z,
-                                 int32_t act, hipStream_t s) {
-  const MxRowsArgs a{p, z, ld_z, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K)};
-  const int64_t nt = p.N / 16;
-  if (nt >= 512) return a.kt >= 16 ? launch_rows<8, 2>(a, act, s) : launch_rows<4, 2>(a, act, s);
-  if (a.kt >= 32 && nt <= 256) return launch_rows<16, 1>(a, act, s);
-  return a.kt >= 16 ? launch_rows<8, 1>(a, act, s) : launch_rows<4, 1>(a, act, s);
+static hipError_t launch_one_row_tile(const MxGemmProblem &p, hipStream_t s) {
+  const int64_t nt = p.N / 16, kt = mx_tiles_k(p.K);
+  if (nt >= 512) return kt >= 16 ? launch_rows<8, 1, 2>(p, s) : launch_rows<4, 1, 2>(p, s);
+  if (kt >= 32 && nt <= 256) return launch_rows<16, 1, 1>(p, s);
+  return kt >= 16 ? launch_rows<8, 1, 1>(p, s) : launch_rows<4, 1, 1>(p, s);
+}
+
+template <int WAVES, int NT>
+static hipError_t launch_fused(const MxRowsArgs &a, int32_t act, hipStream_t s) {
+  const dim3 grid((unsigned)((a.p.N / 16 + NT - 1) / NT)), block(64 * WAVES);
+  const size_t codes = (size_t)(a.p.M * (a.p.K / 32) * 17);
+  size_t lds = sizeof(float) * 4 * 64 * NT * WAVES;
+  if (lds < codes) lds = codes;
+  if (act == 1) hipLaunchKernelGGL((mx_rows_kernel<WAVES, 1, NT, true, 1>), grid, block, lds, s, a);
+  else if (act == 2) hipLaunchKernelGGL((mx_rows_kernel<WAVES, 1, NT, true, 2>), grid, block, lds, s, a);
+  else hipLaunchKernelGGL((mx_rows_kernel<WAVES, 1, NT, true, 0>), grid, block, lds, s, a);
+  return hipGetLastError();
 }
 
 // Every workgroup would quantise all of z again.
 bool mx_quantises_inside(int64_t M, int64_t K) { return M <= 16 && M * K <= 8192; }
 
+// Two column tiles a workgroup where that leaves a workgroup per CU.
 hipError_t launch_gemm_mx_bf16(const MxGemmProblem &p, const uint16_t *z, int64_t ld_z, int32_t act,
                                hipStream_t s) {
-  return launch_mx_rows(p, z, ld_z, act, s);
+  const MxRowsArgs a{p, z, ld_z, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K)};
+  if (p.N / 16 >= 512) return a.kt >= 16 ? launch_fused<8, 2>(a, act, s) : launch_fused<4, 2>(a, act, s);
+  return a.kt >= 16 ? launch_fused<8, 1>(a, act, s) : launch_fused<4, 1>(a, act, s);
 }
 
 hipError_t launch_gemm_mx(const MxGemmProblem &p, hipStream_t s) {
-  if (p.M <= 16) return launch_mx_rows(p, nullptr, 0, 0, s);
+  if (p.M <= 16) return launch_one_row_tile(p, s);
   const MxGemmArgs a{p, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K),
                      (int32_t)mx_row_tiles(p.M), (int32_t)mx_row_tiles(p.N), 0, 0};
   int best = 0;
   for (int i = 1; i < (int)(sizeof kMxTiles / sizeof kMxTiles[0]); ++i)
     if (mx_cost(kMxTiles[i], a) < mx_cost(kMxTiles[best], a)) best = i;
+  if (mx_rows_cost(a) < mx_cost(kMxTiles[best], a) && a.mt <= 65535)
+    return mx_rows_waves(a.kt) == 8 ? launch_rows<8, 2, 2>(p, s) : launch_rows<4, 2, 2>(p, s);
   switch (best) {
     case 0: return launch_mx_lds<8, 4, 2, 4>(a, s);
     case 1: return launch_mx_lds<7, 4, 2, 4>(a, s);
