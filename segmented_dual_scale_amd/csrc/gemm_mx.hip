@@ -205,8 +205,7 @@ using lc = std::integral_constant<int, V>;
 
 // A workgroup of WM x WN waves owns 16 (WM RM) rows x 16 (WN RN) columns of y, a
 // wave RM x RN tiles of it.  K goes in stages of 128 through four LDS buffers,
-// filled by 16-byte global->LDS copies; scales in blocks of four stages through
-// two.  While a wave multiplies stage u it reads the operands of stage u + 1, one
+// filled by 16-byte global->LDS copies; the scales of four stages through SCALES more.  While a wave multiplies stage u it reads the operands of stage u + 1, one
 // x tile into the registers its last products have just released and one w tile
 // into a second set, and copies its part of stage u + 3 into the buffer of stage
 // u - 1.  The one barrier of a stage says that stage u + 1 has arrived and that
@@ -218,11 +217,11 @@ using lc = std::integral_constant<int, V>;
 // 8 neighbouring columns of y, and a store fills 64 bytes of each of 16 rows.
 // The copies bring them into that order: every operand is read from LDS at 16
 // bytes a lane.
-template <int RM, int RN, int WM, int WN>
+template <int RM, int RN, int WM, int WN, int SCALES>
 __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a) {
   constexpr int kWaves = WM * WN, kXT = WM * RM, kWT = WN * RN, kTiles = kXT + kWT;
   constexpr int kStage = kTiles * 1024, kCopies = (kTiles + kWaves - 1) / kWaves;
-  constexpr int kXS = (kXT + 3) / 4, kScaleGroups = kXS + kWT / 4, kScales = kScaleGroups * 1024;
+  constexpr int kXS = (kXT + 3) / 4, kScaleGroups = kXS + kWT / 4;
   static_assert(RN % 4 == 0 && kXT % 2 == 0, "tiles");
   extern __shared__ uint8_t smem[];
   uint8_t *const scale_lds = smem + 4 * kStage;
@@ -275,7 +274,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
             (((int64_t)min(tn * kWT + (q - kXS) * 4 + (g & 2) + (r >> 1 & 1), a.nt - 1) * a.ks + s)
              << 8) +
             (r >> 2) * 64 + (r & 1) * 32 + (g & 1) * 16;
-      copy16(p, scale_lds + (s & 1) * kScales + q * 1024);
+      copy16(p, scale_lds + (s % SCALES) * kScaleGroups * 1024 + q * 1024);
     }
   };
   auto x_tile = [&](int buf, int i) {
@@ -286,11 +285,11 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
                                           lane * 16);
   };
   auto x_scale = [&](int s, int i) {
-    return *reinterpret_cast<const uint32_t *>(scale_lds + (s & 1) * kScales +
+    return *reinterpret_cast<const uint32_t *>(scale_lds + (s % SCALES) * kScaleGroups * 1024 +
                                                (wm * RM + i) * 256 + lane * 4);
   };
   auto w_scale = [&](int s, int j) {
-    return *reinterpret_cast<const uint32_t *>(scale_lds + (s & 1) * kScales +
+    return *reinterpret_cast<const uint32_t *>(scale_lds + (s % SCALES) * kScaleGroups * 1024 +
                                                (4 * kXS + wn * RN + j) * 256 + lane * 4);
   };
 
@@ -323,9 +322,9 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
     sw[j] = w_scale(0, j);
   }
 
-  // stage u = 4 s + T.  WHOLE: stages u + 1 .. u + 3 exist, and u + 4 for T = 0.  At
-  // the end of K the operands read for a stage that does not exist are what its
-  // buffer holds, and no product takes them.
+  // stage u = 4 s + T.  WHOLE: stages u + 1 .. u + 3 exist.  At the
+  // end of K the operands read for a stage that does not exist are what its buffer
+  // holds, and no product takes them.
   auto step = [&](int s, auto t_, auto whole_) {
     constexpr int T = decltype(t_)::value;
     constexpr bool WHOLE = decltype(whole_)::value != 0;
@@ -335,7 +334,10 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
     if (WHOLE || u + 2 < kt) wait_vm<kCopies>();
     else wait_vm<0>();
     stage_barrier();
-    if (T == 0 && (WHOLE || u + 4 < kt)) copy_scales(s + 1);
+    // the next block's scales, needed behind the barrier of T = 3, when only the
+    // copies of T = 2 may be left.  Into the buffer of this block's they go once all
+    // waves have used stage T = 0, and so read them
+    if (T == 2 - SCALES && (WHOLE || 4 * s + 4 < kt)) copy_scales(s + 1);
     if (!WHOLE && u + 3 < kt) {
 #pragma unroll
       for (int c = 0; c < kCopies; ++c) copy(c, FREE);
@@ -398,12 +400,12 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
 
 }  // namespace
 
-template <int RM, int RN, int WM, int WN>
+template <int RM, int RN, int WM, int WN, int SCALES>
 static hipError_t launch_mx_lds(MxGemmArgs a, hipStream_t s) {
-  constexpr int kXT = WM * RM, kWT = WN * RN, kLds = 4096 * (kXT + kWT) + 2048 * ((kXT + 3) / 4 + kWT / 4);
+  constexpr int kXT = WM * RM, kWT = WN * RN, kLds = 4096 * (kXT + kWT) + 1024 * SCALES * ((kXT + 3) / 4 + kWT / 4);
   a.tiles_m = (a.mt + kXT - 1) / kXT;
   a.tiles_n = (a.nt + kWT - 1) / kWT;
-  hipLaunchKernelGGL((mx_gemm_lds_kernel<RM, RN, WM, WN>),
+  hipLaunchKernelGGL((mx_gemm_lds_kernel<RM, RN, WM, WN, SCALES>),
                      dim3((unsigned)(a.tiles_m * (int64_t)a.tiles_n)), dim3(64 * WM * WN), kLds, s,
                      a);
   return hipGetLastError();
@@ -412,8 +414,8 @@ static hipError_t launch_mx_lds(MxGemmArgs a, hipStream_t s) {
 // Time of a product in us by tiles of some shape: workgroups beyond what fits the
 // chip at once go in further rounds, each of kt steps and what its start and end
 // cost.  step and fixed are fits to measured times from K = 128 to 12288.  A tile
-// that is alone on its CU goes in whole rounds; two on a CU overlap each other's
-// ends, so their rounds count in parts, and steps are shorter while CUs are free.
+// that is alone on its CU goes in whole rounds; those that share one overlap each
+// other's ends, so half of a part counts, and steps are shorter while CUs are free.
 struct MxTile {
   int rows, cols;  // in tiles of 16
   int per_cu;
@@ -425,8 +427,8 @@ static float mx_cost(const MxTile &t, const MxGemmArgs &a) {
   const float kt = (float)a.kt;
   float rounds = tiles / (256.0f * (float)t.per_cu);
   if (t.per_cu == 1) return ceilf(rounds) * (kt * t.step + t.fixed);
-  if (rounds < 1.0f) return kt * t.step * (0.6f + 0.4f * rounds) + t.fixed;
-  return rounds * (kt * t.step + t.fixed);
+  if (rounds < 1.0f) return kt * t.step * (0.4f + 0.6f * rounds) + t.fixed;
+  return 0.5f * (rounds + ceilf(rounds)) * (kt * t.step + t.fixed);
 }
 
 // The same by workgroups of 32 x 32 that split K over their waves: 4 KiB a step
@@ -446,8 +448,8 @@ static float mx_rows_cost(const MxGemmArgs &a) {
 // 6.8; 256x1536x6144 split K 6.2, 64x128 10.4; 600x4096x4096 128x128 12.3, 64x128
 // 12.6, split K 16.3.
 constexpr MxTile kMxTiles[] = {
-    {16, 16, 1, 0.80f, 6.5f}, {14, 16, 1, 0.71f, 6.0f}, {12, 16, 1, 0.62f, 5.5f},
-    {8, 16, 1, 0.45f, 4.5f},  {8, 8, 2, 0.49f, 3.5f},   {4, 8, 2, 0.33f, 2.2f},
+    {16, 16, 1, 0.80f, 7.5f}, {14, 16, 1, 0.71f, 8.0f}, {12, 16, 1, 0.62f, 6.0f},
+    {8, 16, 1, 0.42f, 4.2f},  {8, 8, 2, 0.49f, 3.8f},   {4, 8, 3, 0.47f, 2.6f},
 };
 
 template <int WAVES, int MT, int NT>
@@ -502,12 +504,12 @@ hipError_t launch_gemm_mx(const MxGemmProblem &p, hipStream_t s) {
   if (mx_rows_cost(a) < mx_cost(kMxTiles[best], a) && a.mt <= 65535)
     return mx_rows_waves(a.kt) == 8 ? launch_rows<8, 2, 2>(p, s) : launch_rows<4, 2, 2>(p, s);
   switch (best) {
-    case 0: return launch_mx_lds<8, 4, 2, 4>(a, s);
-    case 1: return launch_mx_lds<7, 4, 2, 4>(a, s);
-    case 2: return launch_mx_lds<6, 4, 2, 4>(a, s);
-    case 3: return launch_mx_lds<4, 4, 2, 4>(a, s);
-    case 4: return launch_mx_lds<4, 4, 2, 2>(a, s);
-    default: return launch_mx_lds<2, 4, 2, 2>(a, s);
+    case 0: return launch_mx_lds<8, 4, 2, 4, 2>(a, s);
+    case 1: return launch_mx_lds<7, 4, 2, 4, 2>(a, s);
+    case 2: return launch_mx_lds<6, 4, 2, 4, 2>(a, s);
+    case 3: return launch_mx_lds<4, 4, 2, 4, 2>(a, s);
+    case 4: return launch_mx_lds<4, 4, 2, 2, 2>(a, s);
+    default: return launch_mx_lds<2, 4, 2, 2, 1>(a, s);  // three workgroups' LDS fit a CU
   }
 }
 
