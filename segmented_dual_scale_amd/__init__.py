@@ -906,19 +906,19 @@ def segquant_rotary_frequencies(widths: Sequence[int], theta: float = 10000.0):
 
 @functools.lru_cache(maxsize=1024)
 def _stride_array(stride):
-    a = (ctypes.c_int64 * 3)(*stride[:3])
-    return ctypes.addressof(a), a  # the address belongs to the array
+    return (ctypes.c_int64 * 3)(*stride[:3])
 
 
 def _head_strides(t, name: str, shape, at: int):
-    """A [B][L][heads][D] tensor (None: not given) -> its address and strides."""
+    """A [B][L][heads][D] tensor (None: not given) -> its address and its strides
+    (an array, read only: calls share it)."""
     import torch
     if t is None:
         return None, None
     ptr, stride = _want(t, name, torch.bfloat16, shape, at), t.stride()
     if stride[3] != 1 and shape[3] > 1 and t.numel():
         raise ValueError(f"{name} must have unit stride in its last dimension")
-    return ptr, _stride_array(stride)[0]
+    return ptr, _stride_array(stride)
 
 
 def segquant_qk_rotary(q, k, positions, freq, widths: Sequence[int],

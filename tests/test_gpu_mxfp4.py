@@ -152,6 +152,64 @@ def test_product(M, N, K, codes):
     assert torch.equal(again.view(torch.int16), y.view(torch.int16))
 
 
+# every tile shape, K ending in every stage of a block of scales, ragged rows and columns
+FORMS = [(1551, 4656, 960), (1171, 6208, 1088), (1463, 4896, 1216), (3909, 1968, 832),
+         (3480, 3088, 448), (5486, 1824, 576), (5991, 1600, 704), (5892, 1952, 320),
+         (4742, 2656, 960), (2709, 4512, 1088), (2624, 5024, 704), (2585, 4880, 832),
+         (4871, 2848, 448), (5786, 2336, 576), (4719, 2848, 704), (3266, 4368, 320),
+         (4509, 1296, 448), (4101, 1424, 576), (3429, 2048, 192), (4545, 1312, 320),
+         (388, 5136, 448), (4593, 1136, 64), (488, 6272, 192), (1190, 1968, 320),
+         (25, 48, 1472), (188, 80, 64), (29, 96, 192), (378, 16, 320), (160, 1536, 12288)]
+
+
+@pytest.mark.parametrize("M,N,K", FORMS)
+def test_every_form_of_the_product(M, N, K):
+    g = gen(M + N + K)
+    z = (normal(g, M, K) * torch.exp(normal(g, M, 1))).to(BF)
+    w = S.segquant_quantize_weight_mxfp4(normal(g, K, N) * torch.exp(normal(g, 1, N)))
+    mx = S.segquant_quantize_mxfp4(z)
+    ybuf, y = padded(torch.zeros(M, N, device=DEV, dtype=BF), N + 8, 7.0)
+    S.segquant_gemm_mxfp4(None, w, N, K=K, xq=mx, out=y)
+    product_close(y, S.segquant_unpack_mxfp4(mx, M, K), S.segquant_unpack_mxfp4(w, N, K), K)
+    assert (ybuf[:, N:] == 7.0).all()
+    for _ in range(2):  # the same bits again
+        assert torch.equal(S.segquant_gemm_mxfp4(z, w, N), y)
+
+
+def test_rows_far_apart():
+    """Row distances that pass 32 bits, in elements and in bytes."""
+    g = gen(11)
+    M, N, K, far = 4, 64, 192, (1 << 30) + 64
+    z = torch.empty(M * far, device=DEV, dtype=BF).view(M, far)[:, :K]
+    y = torch.empty(M * far, device=DEV, dtype=BF).view(M, far)[:, :N]
+    z.copy_(normal(g, M, K))
+    w = S.segquant_quantize_weight_mxfp4(normal(g, K, N))
+    want = S.segquant_gemm_mxfp4(z.contiguous(), w, N)
+    mx = S.segquant_quantize_mxfp4(z)
+    assert torch.equal(S.segquant_gemm_mxfp4(z, w, N, out=y), want)
+    y.zero_()
+    assert torch.equal(S.segquant_gemm_mxfp4(None, w, N, K=K, xq=mx, out=y), want)
+
+
+def test_calls_at_once_on_two_streams():
+    g = gen(21)
+    N, K = 1536, 1536
+    w = S.segquant_quantize_weight_mxfp4(normal(g, K, N))
+    z = [normal(g, M, K).to(BF) for M in (900, 40)]
+    want = [S.segquant_gemm_mxfp4(x, w, N) for x in z]
+    streams = [torch.cuda.Stream() for _ in z]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(S.segquant_gemm_mxfp4(z[i], w, N))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for y in got[i]:
+            assert torch.equal(y, want[i])
+
+
 @pytest.mark.parametrize("M", [1, 7, 16, 60, 200])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_product_behind_an_activation_is_the_quantiser_s(M, act):
@@ -179,7 +237,7 @@ def test_ones_and_powers_are_exact(M, N, K):
     assert torch.equal(y, want)
 
 
-@pytest.mark.parametrize("M", [4, 40, 400])
+@pytest.mark.parametrize("M", [4, 40, 400, 6000])
 def test_nan_and_infinity_reach_their_rows_only(M):
     g = gen(M)
     K, N = 640, 144
@@ -216,7 +274,7 @@ def test_no_rows():
     assert codes.numel() == scales.numel() == 0
 
 
-@pytest.mark.parametrize("M", [3, 300])
+@pytest.mark.parametrize("M", [3, 300, 3000])
 def test_other_stream_and_two_graphs_on_one_workspace(M):
     g = gen(M)
     N, K = 256, 512

@@ -157,3 +157,14 @@ def test_no_rows_other_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, S.segquant_rmsnorm_quantize(h, branch=branch, x_out=True)[1])
+
+
+def test_rows_far_apart():
+    """Row distances that pass 32 bits, in elements and in bytes."""
+    g = gen(31)
+    M, K, far = 4, 192, (1 << 30) + 64
+    h = torch.empty(M * far, device=DEV, dtype=BF).view(M, far)[:, :K]
+    x = torch.empty(M * far, device=DEV, dtype=BF).view(M, far)[:, :K]
+    h.copy_(normal(g, M, K))
+    S.segquant_rmsnorm_quantize(h, x_out=x)
+    assert torch.equal(x, S.segquant_rmsnorm_quantize(h.contiguous(), x_out=True)[1])

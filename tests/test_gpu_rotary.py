@@ -234,3 +234,20 @@ def test_elements_that_do_not_turn_keep_to_themselves(style):
     out = S.segquant_qk_rotary(q, None, pos, freq, [32], style, norm=False)[0]
     assert torch.equal(out[..., 32:].view(torch.int16), q[..., 32:].view(torch.int16))
     assert not out[..., :32].isnan().any()
+
+
+def test_tokens_and_heads_far_apart():
+    """Strides that pass 32 bits, in elements and in bytes."""
+    g = gen(32)
+    far, D = (1 << 30) + 64, 64
+    freq = S.segquant_rotary_frequencies([64]).to(DEV)
+    for shape, dims in (((1, 3, 2, D), (0, 1, 2)), ((1, 2, 3, D), (0, 2, 1)), ((3, 1, 2, D), (1, 0, 2))):
+        big = torch.empty(3 * far, device=DEV, dtype=BF).view(1, 3, far)[..., :2 * D]
+        q = big.unflatten(2, (2, D)).permute(*dims, 3)
+        assert q.shape == shape
+        q.copy_(normal(g, *shape))
+        pos = torch.randint(0, 99, (shape[1], 1), generator=g, device=DEV, dtype=torch.int32)
+        want = S.segquant_qk_rotary(q.contiguous(), None, pos, freq, [64])[0]
+        S.segquant_qk_rotary(q, None, pos, freq, [64], q_out=q)
+        assert torch.equal(q, want)
+        del big, q
