@@ -751,6 +751,12 @@ def _mx_ptrs(mx, name: str, R: int, K: int, at: int):
         return None, None
     codes, scales = mx
     n, m = segquant_mxfp4_bytes(R, K)
+    u8 = torch.uint8
+    if (codes.dtype is u8 and scales.dtype is u8 and codes.get_device() == at and
+            scales.get_device() == at and codes.dim() == 1 and scales.dim() == 1 and
+            codes.numel() == n and scales.numel() == m and codes.is_contiguous() and
+            scales.is_contiguous()):
+        return codes.data_ptr(), scales.data_ptr()
     return (_want_array(codes, name + " codes", torch.uint8, (n,), at),
             _want_array(scales, name + " scales", torch.uint8, (m,), at))
 
@@ -909,16 +915,15 @@ def _stride_array(stride):
     return (ctypes.c_int64 * 3)(*stride[:3])
 
 
-def _head_strides(t, name: str, shape, at: int):
-    """A [B][L][heads][D] tensor (None: not given) -> its address and its strides
-    (an array, read only: calls share it)."""
-    import torch
-    if t is None:
-        return None, None
-    ptr, stride = _want(t, name, torch.bfloat16, shape, at), t.stride()
+def _head_strides(t, name: str, shape, at: int, dtype):
+    """A [B][L][heads][D] tensor -> its address and its strides (an array, read
+    only: calls share it)."""
+    if t.dtype is not dtype or t.get_device() != at or t.shape != shape:
+        _want(t, name, dtype, shape, at)
+    stride = t.stride()
     if stride[3] != 1 and shape[3] > 1 and t.numel():
         raise ValueError(f"{name} must have unit stride in its last dimension")
-    return ptr, _stride_array(stride)
+    return t.data_ptr(), _stride_array(stride)
 
 
 def segquant_qk_rotary(q, k, positions, freq, widths: Sequence[int],
@@ -934,35 +939,37 @@ def segquant_qk_rotary(q, k, positions, freq, widths: Sequence[int],
     tensors allocated here."""
     import torch
     fn = load_library().segquant_qk_rotary
-    if q.dim() != 4 or q.dtype is not torch.bfloat16:
+    bf, f32 = torch.bfloat16, torch.float32
+    if q.dim() != 4 or q.dtype is not bf:
         raise ValueError(f"q must be bfloat16 [B][L][heads][D], got {q.dtype} {tuple(q.shape)}")
-    B, L, Hq, D = q.shape
+    q_shape = q.shape
+    B, L, Hq, D = q_shape
     at = q.get_device()
     n, axes, R, _ = _axes(tuple(map(int, widths)))
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    k_shape, Hk = None, 0
+        q_out = torch.empty(q_shape, dtype=bf, device=q.device)
+    q_args = _head_strides(q, "q", q_shape, at, bf)
+    q_out_args = _head_strides(q_out, "q_out", q_shape, at, bf)
     if k is not None:
         if k.dim() != 4:
             raise ValueError(f"k must be bfloat16 [B][L][heads][D], got {tuple(k.shape)}")
         Hk = k.shape[2]
         k_shape = (B, L, Hk, D)
         if k_out is None:
-            k_out = torch.empty(k_shape, dtype=q.dtype, device=q.device)
+            k_out = torch.empty(k_shape, dtype=bf, device=q.device)
+        k_args = _head_strides(k, "k", k_shape, at, bf)
+        k_out_args = _head_strides(k_out, "k_out", k_shape, at, bf)
     elif k_out is not None or k_gamma is not None:
         raise ValueError("k_out or k_gamma without k")
+    else:
+        Hk, k_args, k_out_args = 0, (None, None), (None, None)
     if positions.dim() == 3:
         pos, per = _want_array(positions, "positions", torch.int32, (B, L, n), at), L * n
     else:
         pos, per = _want_array(positions, "positions", torch.int32, (L, n), at), 0
-    f32 = torch.float32
-    q_ptr, q_stride = _head_strides(q, "q", q.shape, at)
-    k_ptr, k_stride = _head_strides(k, "k", k_shape, at)
-    _check(_on(at, fn, B, L, D, q_ptr, Hq, q_stride, *_head_strides(q_out, "q_out", q.shape, at),
-               k_ptr, Hk, k_stride, *_head_strides(k_out, "k_out", k_shape, at), int(bool(norm)), eps,
-               _want_array(q_gamma, "q_gamma", f32, (D,), at),
+    _check(_on(at, fn, B, L, D, q_args[0], Hq, q_args[1], *q_out_args, k_args[0], Hk, k_args[1],
+               *k_out_args, 1 if norm else 0, eps, _want_array(q_gamma, "q_gamma", f32, (D,), at),
                _want_array(k_gamma, "k_gamma", f32, (D,), at), pos, per, n, axes,
                _want_array(freq, "freq", torch.float64, (R // 2,), at), style),
            "segquant_qk_rotary")
     return q_out, k_out
-

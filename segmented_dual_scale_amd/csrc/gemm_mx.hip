@@ -483,15 +483,24 @@ static hipError_t launch_fused(const MxRowsArgs &a, int32_t act, hipStream_t s) 
   return hipGetLastError();
 }
 
-// Every workgroup would quantise all of z again.
-bool mx_quantises_inside(int64_t M, int64_t K) { return M <= 16 && M * K <= 8192; }
+// Every workgroup quantises all of z again: up to 32 values a thread.  In a
+// captured graph, where a second launch costs least, with no activation / SiLU /
+// GELU: 4 x 1536 (24 values) 3.9 / 4.8 / 5.9 us against 5.3 / 5.8 / 6.3 in two
+// launches, 8 x 1536 (48) 5.0 / 6.8 / 8.8 against 5.3 / 5.7 / 6.3 (N = 9216); a
+// second launch from the host costs 5 us more.
+static int fused_waves(int64_t K) { return mx_tiles_k(K) >= 16 ? 8 : 4; }
+
+bool mx_quantises_inside(int64_t M, int64_t K) {
+  return M <= 16 && M * K <= 32 * 64 * fused_waves(K);
+}
 
 // Two column tiles a workgroup where that leaves a workgroup per CU.
 hipError_t launch_gemm_mx_bf16(const MxGemmProblem &p, const uint16_t *z, int64_t ld_z, int32_t act,
                                hipStream_t s) {
   const MxRowsArgs a{p, z, ld_z, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K)};
-  if (p.N / 16 >= 512) return a.kt >= 16 ? launch_fused<8, 2>(a, act, s) : launch_fused<4, 2>(a, act, s);
-  return a.kt >= 16 ? launch_fused<8, 1>(a, act, s) : launch_fused<4, 1>(a, act, s);
+  const bool eight = fused_waves(p.K) == 8;
+  if (p.N / 16 >= 512) return eight ? launch_fused<8, 2>(a, act, s) : launch_fused<4, 2>(a, act, s);
+  return eight ? launch_fused<8, 1>(a, act, s) : launch_fused<4, 1>(a, act, s);
 }
 
 hipError_t launch_gemm_mx(const MxGemmProblem &p, hipStream_t s) {

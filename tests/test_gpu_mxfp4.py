@@ -222,6 +222,21 @@ def test_product_behind_an_activation_is_the_quantiser_s(M, act):
                   1600)
 
 
+@pytest.mark.parametrize("M,N,K", [(4, 9216, 1536), (5, 96, 1600), (4, 48, 4096), (1, 32, 16384),
+                                   (8, 8208, 2048), (16, 16, 512), (3, 16, 64), (2, 8192, 192)])
+@pytest.mark.parametrize("act", list(ACTS))
+def test_few_rows_are_quantised_inside(M, N, K, act):
+    assert S.segquant_gemm_mxfp4_workspace_bytes(M, N, K) == 0
+    g = gen(M + K)
+    z = (2 * normal(g, M, K) * torch.exp(normal(g, M, 1))).to(BF)
+    z[0, :64] = 0
+    _, z = padded(z, K + 8, float("nan"))
+    w = S.segquant_quantize_weight_mxfp4(normal(g, K, N))
+    mx = S.segquant_quantize_mxfp4(z, ACTS[act])
+    y = S.segquant_gemm_mxfp4(z, w, N, act_kind=ACTS[act], workspace=None)
+    product_close(y, S.segquant_unpack_mxfp4(mx, M, K), S.segquant_unpack_mxfp4(w, N, K), K)
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 64, 256), (200, 128, 192), (700, 1024, 512)])
 def test_ones_and_powers_are_exact(M, N, K):
     """Small integers and powers of two: every sum is exact in fp32."""
