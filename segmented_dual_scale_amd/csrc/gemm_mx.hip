@@ -214,7 +214,7 @@ using lc = std::integral_constant<int, V>;
 //
 // Of two neighbouring w tiles, instruction q takes rows 4 q .. 4 q + 3 and 8 + 4 q
 // .. 11 + 4 q of each, so that its results in a lane, with those of the other, are
-// 8 neighbouring columns of y, and a store fills 64 bytes of each of 16 rows.
+// 8 neighbouring columns of y.
 // The copies bring them into that order: every operand is read from LDS at 16
 // bytes a lane.
 template <int RM, int RN, int WM, int WN, int SCALES>
@@ -381,20 +381,30 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
     if (4 * s + 2 < kt) step(s, lc<2>{}, lc<0>{});
     if (4 * s + 3 < kt) step(s, lc<3>{}, lc<0>{});
   }
-  // lane (g, j) of x tile i: row j, columns 8 g .. 8 g + 7 of every 32
+  // Lane (g, j) of x tile i has columns 8 g .. 8 g + 7 of every 32 of row j.  Through
+  // LDS, a wave's part to itself, eight lanes take a row's 128 bytes, so that stores
+  // fill whole cache lines.  Piece c of a row stands at c ^ (row % 8): neither side
+  // meets in a bank more than twice.
+  static_assert(RN == 4 && 16 * RM * 128 * kWaves <= 4 * kStage, "the results' rows");
+  stage_barrier();  // all waves have read the last stage
+  uint8_t *const rows = smem + wave * (16 * RM * 128);
 #pragma unroll
-  for (int i = 0; i < RM; ++i) {
-    const int64_t m = (int64_t)(tm * kXT + wm * RM + i) * 16 + r;
-    if (m >= a.p.M) continue;
+  for (int i = 0; i < RM; ++i)
 #pragma unroll
     for (int j = 0; j < RN; j += 2) {
-      const int n = (tn * kWT + wn * RN + j) * 16 + 8 * g;
-      if (n >= a.p.N) continue;
       const v4f &lo = acc[i][j], &hi = acc[i][j + 1];
-      *reinterpret_cast<v4u *>(a.p.y + m * a.p.ld_y + n) =
+      *reinterpret_cast<v4u *>(rows + (16 * i + r) * 128 + ((2 * j + g) ^ (r & 7)) * 16) =
           v4u{cvt_bf16x2(lo[0], lo[1]), cvt_bf16x2(lo[2], lo[3]), cvt_bf16x2(hi[0], hi[1]),
               cvt_bf16x2(hi[2], hi[3])};
     }
+  const int row = lane >> 3, n = (tn * kWT + wn * RN) * 16 + 8 * (lane & 7);
+  const int64_t m0 = (int64_t)(tm * kXT + wm * RM) * 16 + row;
+  uint16_t *const y = a.p.y + m0 * a.p.ld_y + n;
+#pragma unroll
+  for (int i = 0; i < 2 * RM; ++i) {
+    const v4u v = *reinterpret_cast<const v4u *>(rows + (8 * i + row) * 128 +
+                                                 ((lane & 7) ^ (row & 7)) * 16);
+    if (m0 + 8 * i < a.p.M && n < a.p.N) *reinterpret_cast<v4u *>(y + 8 * i * a.p.ld_y) = v;
   }
 }
 
@@ -427,7 +437,7 @@ static float mx_cost(const MxTile &t, const MxGemmArgs &a) {
   const float kt = (float)a.kt;
   float rounds = tiles / (256.0f * (float)t.per_cu);
   if (t.per_cu == 1) return ceilf(rounds) * (kt * t.step + t.fixed);
-  if (rounds < 1.0f) return kt * t.step * (0.4f + 0.6f * rounds) + t.fixed;
+  if (rounds < 1.0f) return kt * t.step * (0.5f + 0.5f * rounds) + t.fixed;
   return 0.5f * (rounds + ceilf(rounds)) * (kt * t.step + t.fixed);
 }
 
@@ -441,15 +451,14 @@ static float mx_rows_cost(const MxGemmArgs &a) {
   return 2.0f + groups * kt * (4096.0f / 22e6f) + 0.25f * kt / (float)mx_rows_waves(a.kt);
 }
 
-// Measured, each against the next best (us): 9216x4608x12288 224x256 226, 256x256
-// 235, 128x128 265; 8192^3 256x256 239, 224x256 250, 128x256 276, 128x128 282;
-// 4429x4608x1536 128x128 24.9, 192x256 26.8, 256x256 29.7; 4096x1536x6144 128x256
-// 24.1, 128x128 24.6, 256x256 36.3; 1024x1536x1536 64x128 5.4, split K 5.8, 128x128
-// 6.8; 256x1536x6144 split K 6.2, 64x128 10.4; 600x4096x4096 128x128 12.3, 64x128
-// 12.6, split K 16.3.
+// Measured, the chosen one against the next best (us): 9216x4608x12288 224x256 220,
+// 256x256 228, 192x256 242; 8192^3 256x256 232, 224x256 244; 4429x4608x1536 128x128
+// 24.8, 192x256 25.9; 3000x3200x2560 192x256 18.8, 224x256 20.0; 4096x1536x6144
+// 128x256 23.5, 128x128 24.4; 1024x1536x1536 64x128 5.2, split K 5.8, 128x128 6.5;
+// 256x1536x6144 split K 6.2, 64x128 10.4.
 constexpr MxTile kMxTiles[] = {
-    {16, 16, 1, 0.80f, 7.5f}, {14, 16, 1, 0.71f, 8.0f}, {12, 16, 1, 0.62f, 6.0f},
-    {8, 16, 1, 0.42f, 4.2f},  {8, 8, 2, 0.49f, 3.8f},   {4, 8, 3, 0.47f, 2.6f},
+    {16, 16, 1, 0.78f, 5.5f}, {14, 16, 1, 0.69f, 6.5f}, {12, 16, 1, 0.59f, 5.6f},
+    {8, 16, 1, 0.41f, 3.6f},  {8, 8, 2, 0.49f, 3.3f},   {4, 8, 3, 0.47f, 2.6f},
 };
 
 template <int WAVES, int MT, int NT>

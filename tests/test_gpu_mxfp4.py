@@ -159,7 +159,10 @@ FORMS = [(1551, 4656, 960), (1171, 6208, 1088), (1463, 4896, 1216), (3909, 1968,
          (4871, 2848, 448), (5786, 2336, 576), (4719, 2848, 704), (3266, 4368, 320),
          (4509, 1296, 448), (4101, 1424, 576), (3429, 2048, 192), (4545, 1312, 320),
          (388, 5136, 448), (4593, 1136, 64), (488, 6272, 192), (1190, 1968, 320),
-         (25, 48, 1472), (188, 80, 64), (29, 96, 192), (378, 16, 320), (160, 1536, 12288)]
+         (25, 48, 1472), (188, 80, 64), (29, 96, 192), (378, 16, 320), (160, 1536, 12288),
+         (4857, 2352, 1472), (3663, 3168, 1600), (4578, 2576, 1728), (4844, 2336, 1856),
+         (642, 3408, 448), (871, 6080, 64), (3173, 1008, 192), (2532, 1008, 320),
+         (962, 6192, 192), (1924, 3760, 576), (1199, 5680, 704)]
 
 
 @pytest.mark.parametrize("M,N,K", FORMS)
