@@ -942,16 +942,19 @@ static bool heads_meet(const Heads &x, const Heads &y, int64_t B, int64_t L, int
   // two columns of one matrix per sample: offsets of a token of y from one of x
   const I128 d = ((I128)reinterpret_cast<uintptr_t>(y.p) - (I128)reinterpret_cast<uintptr_t>(x.p));
   const I128 wx = 2 * (I128)x.heads * D, wy = 2 * (I128)y.heads * D;
-  const I128 sb = 2 * (I128)x.stride[0], sl = 2 * (I128)x.stride[1];
-  for (int64_t b = 1 - B; b < B; ++b) {
-    const I128 at = d + b * sb;  // at + l sl inside (-wy, wx) for some |l| < L?
-    if (L == 1 || sl == 0) {
+  // walk the shorter of the two dimensions, at most 2^15 either way
+  const int walk = B <= L ? 0 : 1;
+  const int64_t n = walk ? L : B, other = walk ? B : L;
+  const I128 step = 2 * (I128)x.stride[walk], ld = 2 * (I128)x.stride[1 - walk];
+  for (int64_t i = 1 - n; i < n; ++i) {
+    const I128 at = d + i * step;  // at + j ld inside (-wy, wx) for some |j| < other?
+    if (other == 1 || ld == 0) {
       if (at > -wy && at < wx) return true;
       continue;
     }
-    I128 first = floor_div(-wy - at, sl) + 1, last = floor_div(wx - 1 - at, sl);
-    if (first < 1 - L) first = 1 - L;
-    if (last > L - 1) last = L - 1;
+    I128 first = floor_div(-wy - at, ld) + 1, last = floor_div(wx - 1 - at, ld);
+    if (first < 1 - other) first = 1 - other;
+    if (last > other - 1) last = other - 1;
     if (first <= last) return true;
   }
   return false;

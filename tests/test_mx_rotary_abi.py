@@ -3,6 +3,7 @@ without a GPU: the documented status before any HIP call, through the C ABI with
 fake device addresses, and the Python binding's own checks."""
 import ctypes
 import random
+import time
 
 import numpy as np
 import pytest
@@ -262,6 +263,24 @@ def test_every_overlap_of_q_and_k_in_one_buffer_is_found():
         assert (r == S.SEGQ_ERR_SHAPE) == want, (B, L, Hq, Hk, row, sample, at, S.segquant_last_error())
         both[want] += 1
     assert min(both) > 200
+
+
+@pytest.mark.parametrize("B,L", [(1 << 28, 2), (2, 1 << 28)])
+def test_overlap_of_many_samples_or_tokens_is_found_at_once(B, L):
+    """Two columns of one matrix whose rows are not evenly spaced: the two share
+    only bytes of the last sample and token, or none, and the host says so
+    without a walk over all of them."""
+    n, far = max(B, L), 24 * max(B, L) + 8  # elements between the two long runs
+    st = (24, far, 8) if B == n else (far, 24, 8)
+    at = 1 << 44
+    end = 2 * (far + 24 * (n - 1))  # bytes from the first row to the last
+    began = time.perf_counter()
+    for off, status in [(-end, S.SEGQ_ERR_SHAPE), (-end - 16, S.SEGQ_ERR_HIP),
+                        (16, S.SEGQ_ERR_HIP), (end, S.SEGQ_ERR_SHAPE)]:
+        got = rotary(B=B, L=L, D=8, Hq=1, Hk=1, widths=[0], q=at, q_out=at, k=at + off,
+                     k_out=at + off, qs=st, qos=st, ks=st, kos=st)
+        assert got == status, (off, S.segquant_last_error())
+    assert time.perf_counter() - began < 5.0
 
 
 def test_frequencies():
