@@ -642,7 +642,8 @@ int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
 
 // ------------------------------------------- MXFP4, norm before, rotary behind --
 static int mx_sizes(int64_t R, int64_t K, int64_t max_rows = 1 << 27) {
-  if (R < 0 || K < 1) return fail(SEGQ_ERR_SHAPE, "bad shape %lld x %lld", (long long)R, (long long)K);
+  if (R < 0 || K < 1)
+    return fail(SEGQ_ERR_SHAPE, "bad shape %lld x %lld", (long long)R, (long long)K);
   if (K % 64) return fail(SEGQ_ERR_ALIGN, "MXFP4 needs K %% 64 == 0 (K=%lld)", (long long)K);
   if (R > max_rows || K > (1 << 22))
     return fail(SEGQ_ERR_UNSUPPORTED, "%lld rows > %lld or K %lld > 2^22", (long long)R,

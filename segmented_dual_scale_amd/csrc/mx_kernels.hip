@@ -22,7 +22,9 @@ struct MxQuantArgs {
 
 // One workgroup per scale tile: 16 rows x 512 k, 16 lanes a row, so that a
 // load takes 256 neighbouring bytes of each of four rows and the tile's code
-// tiles and its 256 bytes of scales are written whole.
+// tiles and its 256 bytes of scales are written whole.  4429x1536 5.3 us (3.2 TB/s);
+// behind GELU, whose issue slots bound it, 4096x6144 20.3 us (3.1 TB/s) and
+// 9216x12288 74 us (3.9 TB/s).
 template <int ACT>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(MxQuantArgs a) {
   const int j = threadIdx.x >> 4, col = threadIdx.x & 15, g = col >> 2, q = col & 3;

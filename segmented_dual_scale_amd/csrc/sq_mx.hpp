@@ -30,7 +30,9 @@ __host__ __device__ inline int64_t mx_scale_tiles_k(int64_t K) {
   return (K + kMxScaleK - 1) / kMxScaleK;
 }
 inline int64_t mx_row_tiles(int64_t R) { return (R + kMxTileRows - 1) / kMxTileRows; }
-inline int64_t mx_code_bytes(int64_t R, int64_t K) { return mx_row_tiles(R) * mx_tiles_k(K) * 1024; }
+inline int64_t mx_code_bytes(int64_t R, int64_t K) {
+  return mx_row_tiles(R) * mx_tiles_k(K) * 1024;
+}
 inline int64_t mx_scale_bytes(int64_t R, int64_t K) {
   return mx_row_tiles(R) * mx_scale_tiles_k(K) * 256;
 }

@@ -1,6 +1,6 @@
 // sq_pieces.hpp -- device helpers of the kernels that walk rows of bf16 in
 // pieces of 8 elements (16 bytes): norm_kernels.hip, rmsnorm_kernels.hip,
-// rotary_kernels.hip and mx_kernels.hip.
+// rotary_kernels.hip, mx_kernels.hip and gemm_mx.hip.
 #pragma once
 
 #include "sq_rows.hpp"

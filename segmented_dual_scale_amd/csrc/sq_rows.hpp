@@ -1,7 +1,8 @@
 // sq_rows.hpp -- what the kernels around the layer share: norm_kernels.hip and
-// rmsnorm_kernels.hip (the normalisations that feed it), rotary_kernels.hip
-// (q and k behind it) and adapter_kernels.hip (the low-rank adapters beside it).  First the host-side launch interface of the C-ABI front
-// end (api.cpp), whose arguments are already validated; then device helpers.
+// rmsnorm_kernels.hip (the normalisations that feed it), rotary_kernels.hip (q
+// and k behind it) and adapter_kernels.hip (the low-rank adapters beside it).
+// First the host-side launch interface of the C-ABI front end (api.cpp), whose
+// arguments are already validated; then device helpers.
 #pragma once
 
 #include "sq_device.hpp"
