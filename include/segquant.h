@@ -307,7 +307,7 @@ size_t segquant_mxfp4_scale_bytes(int64_t R, int64_t K);
  *   z_bf16      device bf16 [M][ld_z]
  *   codes, scales  device, the arrays of M rows and K columns, 16- and 4-byte
  *               aligned; they must not overlap each other or z_bf16
- * One launch per 2^20 rows.  Requires K % 64 == 0, z_bf16 16-byte aligned, ld_z a
+ * One launch per 1048544 rows.  Requires K % 64 == 0, z_bf16 16-byte aligned, ld_z a
  * multiple of 8, M <= 2^27, K <= 2^22.  M may be 0.
  */
 int segquant_quantize_mxfp4(const uint16_t *z_bf16, int64_t M, int64_t K, int64_t ld_z,

@@ -20,15 +20,46 @@ struct MxQuantArgs {
   MxOut out;
 };
 
-// One workgroup per scale tile: 16 rows x 512 k, 16 lanes a row, so that a
-// load takes 256 neighbouring bytes of each of four rows and the tile's code
-// tiles and its 256 bytes of scales are written whole.  4429x1536 5.3 us (3.2 TB/s);
-// behind GELU, whose issue slots bound it, 4096x6144 20.3 us (3.1 TB/s) and
-// 9216x12288 74 us (3.9 TB/s).
+// gelu_bf16's E of every bf16 magnitude from 2^-11 to below 16, in LDS.  Below, where
+// GELU rounds to z / 2, E of 0 gives that too, and above, E is 0: the result of every
+// bf16 value is gelu_bf16's, bit for bit.
+constexpr int kGeluFirst = 0x3a00, kGeluCount = 0x4180 - kGeluFirst;
+
+template <int THREADS>
+__device__ __forceinline__ void gelu_table(float *table) {
+  for (int i = threadIdx.x; i < kGeluCount; i += THREADS)
+    table[i] = gelu_bf16_e(i ? __uint_as_float((uint32_t)(kGeluFirst + i) << 16) : 0.0f);
+}
+
+// Two values; their places in the table (in bytes) are found in both halves at once.
+__device__ __forceinline__ uint32_t gelu_pair(uint32_t z, const float *table) {
+  typedef unsigned short v2s __attribute__((ext_vector_type(2)));
+  v2s at = __builtin_bit_cast(v2s, z & 0x7fff7fffu);
+  at = __builtin_elementwise_sub_sat(at, v2s{kGeluFirst, kGeluFirst});
+  at = __builtin_elementwise_min(at, v2s{kGeluCount - 1, kGeluCount - 1}) << 2;
+  const uint32_t both = __builtin_bit_cast(uint32_t, at);
+  const char *t = reinterpret_cast<const char *>(table);
+  const float lo = *reinterpret_cast<const float *>(t + (both & 0xffffu));
+  const float hi = *reinterpret_cast<const float *>(t + (both >> 16));
+  return cvt_bf16x2(gelu_bf16_of(bf16_lo(z), lo), gelu_bf16_of(bf16_hi(z), hi));
+}
+
+// A scale tile, 16 rows x 512 k, to 256 threads: 16 lanes a row, so that a load
+// takes 256 neighbouring bytes of each of four rows and the tile's code tiles and its
+// 256 bytes of scales are written whole.  4429x1536 5.3 us (3.2 TB/s).  GELU (ACT 2) by
+// the table, which two tiles share: computed it took 24 issue slots a value and was
+// bound by them, 9216x12288 68 us and 4096x6144 19.7 in a graph; by the table 47
+// (6.2 TB/s) and 13.3 (one or four tiles 47 and 49, 14.0 and 14.2).  The smallest
+// sizes pay 0.2 us for it.
+constexpr int kGeluTiles = 2;
+
 template <int ACT>
-__global__ __launch_bounds__(256) void mx_quantize_kernel(MxQuantArgs a) {
-  const int j = threadIdx.x >> 4, col = threadIdx.x & 15, g = col >> 2, q = col & 3;
-  const int64_t tile = blockIdx.y, row = tile * 16 + j;
+__global__ __launch_bounds__(ACT == 2 ? 256 * kGeluTiles : 256) void mx_quantize_kernel(
+    MxQuantArgs a) {
+  constexpr int TILES = ACT == 2 ? kGeluTiles : 1;
+  __shared__ float table[ACT == 2 ? kGeluCount : 1];
+  const int lane = threadIdx.x & 255, j = lane >> 4, col = lane & 15, g = col >> 2, q = col & 3;
+  const int64_t tile = (int64_t)blockIdx.y * TILES + (threadIdx.x >> 8), row = tile * 16 + j;
   const int k0 = blockIdx.x * kMxScaleK;
   v4u x[4];
 #pragma unroll
@@ -37,19 +68,24 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(MxQuantArgs a) {
     x[s] = v4u{0u, 0u, 0u, 0u};
     if (row < a.M && k < a.K) x[s] = *reinterpret_cast<const v4u *>(a.x + row * a.ld_x + k);
   }
+  if (ACT == 2) {  // under the loads
+    gelu_table<256 * TILES>(table);
+    __syncthreads();
+    if (tile * 16 >= a.M) return;  // whole waves; no barrier follows
+  }
   uint32_t scales = 0;
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     if (k0 + s * kMxTileK >= a.K) break;
-    if (ACT) {
+    if (ACT == 1) {
       float f[8];
       unpack8(x[s], f);
-      if (ACT == 1) silu8_hw(f);
-      if (ACT == 2) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = gelu_bf16(f[i]);
-      }
+      silu8_hw(f);
       x[s] = pack8(f);
+    }
+    if (ACT == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[s][i] = gelu_pair(x[s][i], table);
     }
     uint32_t byte;
     const uint32_t c = mx_piece(x[s], byte);
@@ -121,17 +157,22 @@ hipError_t launch_quantize_mx(const uint16_t *x, int64_t M, int64_t K, int64_t l
                               uint8_t *codes, uint8_t *scales, hipStream_t s) {
   const MxQuantArgs a{x, M, ld_x, (int32_t)K, {codes, scales, mx_tiles_k(K), mx_scale_tiles_k(K)}};
   // grid.y holds 65535 row tiles; more rows go in further launches
-  for (int64_t r = 0; r < M; r += 65535ll * kMxTileRows) {
+  constexpr int64_t kMost = 65534;
+  for (int64_t r = 0; r < M; r += kMost * kMxTileRows) {
     MxQuantArgs p = a;
-    const int64_t tiles = mx_row_tiles(M - r) < 65535 ? mx_row_tiles(M - r) : 65535;
+    const int64_t tiles = mx_row_tiles(M - r) < kMost ? mx_row_tiles(M - r) : kMost;
     p.x += r * ld_x;
     p.M -= r;
     p.out.codes += (r / kMxTileRows * a.out.kt) << 10;
     p.out.scales += (r / kMxTileRows * a.out.ks) << 8;
-    const dim3 grid((unsigned)a.out.ks, (unsigned)tiles);
-    if (act == 1) hipLaunchKernelGGL(mx_quantize_kernel<1>, grid, dim3(256), 0, s, p);
-    else if (act == 2) hipLaunchKernelGGL(mx_quantize_kernel<2>, grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL(mx_quantize_kernel<0>, grid, dim3(256), 0, s, p);
+    const unsigned ks = (unsigned)a.out.ks, all = (unsigned)tiles;
+    if (act == 1)
+      hipLaunchKernelGGL(mx_quantize_kernel<1>, dim3(ks, all), dim3(256), 0, s, p);
+    else if (act == 2)
+      hipLaunchKernelGGL(mx_quantize_kernel<2>, dim3(ks, (all + kGeluTiles - 1) / kGeluTiles),
+                         dim3(256 * kGeluTiles), 0, s, p);
+    else
+      hipLaunchKernelGGL(mx_quantize_kernel<0>, dim3(ks, all), dim3(256), 0, s, p);
   }
   return hipGetLastError();
 }

@@ -111,14 +111,11 @@ __device__ __forceinline__ float gelu_hw(float z) {
   return 0.5f * z * (z < 0.0f ? E : 2.0f - E);
 }
 
-// GELU of a bf16 value (its square is exact in fp32) for the kernels that quantise
-// it: gelu_hw's Q(t) with the half of z/2 in it, z^2 log2 e / 2 by a constant in
-// two parts, and max(z, 0) - |z| E for both signs: 23 issue slots against 28, where
-// the quantisation of 4096x6144 is bound by them.  The large part of the constant
-// is rounded down, so both products are of one sign and an overflowing z^2 gives
-// E = 0.  Infinities and NaN give NaN.  Within 2^-17 of the true value, relative, down to
-// 2^-125 (swept on the CPU with the hardware's errors injected).
-__device__ __forceinline__ float gelu_bf16(float z) {
+// E of gelu_bf16 below: erfc(|z| / sqrt 2) / 2, the share of |z| that it loses.  gelu_hw's
+// Q(t) with the half of z/2 in it, and z^2 log2 e / 2 by a constant in two parts.  The
+// large part is rounded down, so both products are of one sign and an overflowing
+// z^2 gives E = 0.
+__device__ __forceinline__ float gelu_bf16_e(float z) {
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(z), 0.35355339f, 1.0f));
   float Q = __builtin_fmaf(t, -0.26787168f, 1.0716369f);
   Q = __builtin_fmaf(t, Q, -1.4226438f);
@@ -129,9 +126,19 @@ __device__ __forceinline__ float gelu_bf16(float z) {
   Q = __builtin_fmaf(t, Q, -2.82572f);
   const float s = z * z;
   Q = __builtin_fmaf(s, -9.629815e-9f, Q);
-  const float E = t * __builtin_amdgcn_exp2f(__builtin_fmaf(s, -0x1.715476p-1f, Q));
-  // the middle of z, 0 and infinity: max(z, 0) in one instruction (fmaxf takes two)
-  return __builtin_fmaf(-fabsf(z), E, __builtin_amdgcn_fmed3f(z, 0.0f, __builtin_inff()));
+  return t * __builtin_amdgcn_exp2f(__builtin_fmaf(s, -0x1.715476p-1f, Q));
 }
+
+// max(z, 0) - |z| E, for both signs; the middle of z, 0 and the largest value is
+// max(z, 0) in one instruction (fmaxf takes two).
+__device__ __forceinline__ float gelu_bf16_of(float z, float e) {
+  return __builtin_fmaf(-fabsf(z), e, __builtin_amdgcn_fmed3f(z, 0.0f, 0x1.fffffep127f));
+}
+
+// GELU of a bf16 value (its square is exact in fp32) for the kernels that quantise
+// it: 23 issue slots against gelu_hw's 28.  Infinities and NaN give NaN.  Within
+// 2^-17 of the true value, relative, down to 2^-125 (swept on the CPU with the
+// hardware's errors injected).
+__device__ __forceinline__ float gelu_bf16(float z) { return gelu_bf16_of(z, gelu_bf16_e(z)); }
 
 }  // namespace sq

@@ -112,6 +112,28 @@ def test_quantize_behind_an_activation(act):
     assert same > 1 - 2.0 ** -9, float(same)
 
 
+@pytest.mark.parametrize("rows,power", [([0, 1, 2, 3, 16, 17, 18, 19], 100.0),
+                                        ([4, 5, 6, 7, 20, 21, 22, 23], 0.0),
+                                        ([8, 9, 10, 11, 24, 25, 26, 27], 0.0),
+                                        ([12, 13, 14, 15, 28, 29, 30, 31], 0.0)])
+def test_gelu_of_every_value_in_both_forms(rows, power):
+    """Every finite bf16 value behind GELU, blocks of 32 neighbours: the quantiser
+    against the product that quantises its rows itself, read off a weight with one
+    power of two in each column, so that each y is one value, exactly."""
+    K = 2048
+    bits = torch.arange(65536, device=DEV, dtype=torch.int32).view(32, K)[rows]
+    bits = torch.where((bits & 0x7f80) == 0x7f80, torch.zeros_like(bits), bits)
+    z = (bits << 16).view(torch.float32).to(BF)
+    got = S.segquant_unpack_mxfp4(S.segquant_quantize_mxfp4(z, S.SEGQ_ACT_GELU), 8, K)
+    assert S.segquant_gemm_mxfp4_workspace_bytes(8, K, K) == 0
+    w = S.segquant_quantize_weight_mxfp4(2.0 ** power * torch.eye(K, device=DEV))
+    y = S.segquant_gemm_mxfp4(z, w, K, act_kind=S.SEGQ_ACT_GELU)
+    assert torch.equal(y.double(), got.double() * 2.0 ** power)
+    want = act_ref(z.double().cpu(), "gelu").to(BF)
+    same = (got.cpu().double() == mx_ref(want)).double().mean()
+    assert same > 1 - 2.0 ** -9, float(same)  # as above
+
+
 @pytest.mark.parametrize("K,N", [(64, 16), (128, 48), (192, 80), (1536, 144), (2112, 32)])
 def test_quantize_weight(K, N):
     g = gen(K + N)
