@@ -184,7 +184,9 @@ FORMS = [(1551, 4656, 960), (1171, 6208, 1088), (1463, 4896, 1216), (3909, 1968,
          (25, 48, 1472), (188, 80, 64), (29, 96, 192), (378, 16, 320), (160, 1536, 12288),
          (4857, 2352, 1472), (3663, 3168, 1600), (4578, 2576, 1728), (4844, 2336, 1856),
          (642, 3408, 448), (871, 6080, 64), (3173, 1008, 192), (2532, 1008, 320),
-         (962, 6192, 192), (1924, 3760, 576), (1199, 5680, 704)]
+         (962, 6192, 192), (1924, 3760, 576), (1199, 5680, 704), (4526, 1344, 1024),
+         (4590, 1312, 640), (1525, 4000, 1728), (3472, 1712, 1408), (5136, 1568, 448),
+         (4642, 1712, 576), (1897, 5280, 192), (2370, 3392, 320), (2990, 3184, 1088)]
 
 
 @pytest.mark.parametrize("M,N,K", FORMS)
