@@ -222,12 +222,11 @@ using lc = std::integral_constant<int, V>;
 // all waves have multiplied stage u - 1, and so read it: reads in flight need
 // not end before it.
 //
-// A stage of 256x256 is 1024 clocks of products, as many of LDS (96 KB read, 32 KB
-// written) and 560 of L2, and takes about 1230, by operands of zeros; 128x256 is 512,
-// 704 and 420, and takes 780.  With more of one there was less of all: four waves of
-// twice the tile, which read a quarter less (8192^3: 268 us against 227), and half of
-// w straight to registers, two thirds of the LDS's traffic for one and a half times
-// the L2's (9216x4608x12288: 229 us against 216), are slower.
+// At 9216x4608x12288 the matrix cores are busy in 65 % of the clocks (counters) and the
+// clock is held to 1.8 GHz; the LDS's reads take 30 %.  What reads less of it is
+// slower: four waves of twice the tile each (8192^3: 268 us against 227), one to a
+// SIMD; half of w straight to registers, which both waves of a column then load
+// (229 us against 216).
 //
 // Of two neighbouring w tiles, instruction q takes rows 4 q .. 4 q + 3 and 8 + 4 q
 // .. 11 + 4 q of each, so that its results in a lane, with those of the other, are
