@@ -59,13 +59,14 @@ struct MxRowsArgs {
   const uint16_t *z;  // bf16 input (FUSED)
   int64_t ld_z;
   int32_t kt, ks;
+  uint32_t per_row;  // e * per_row >> 32 = e / (K / 8) for the e of FUSED, below 2^16
 };
 
 // MT tiles of x rows and NT tiles of w columns to a workgroup, whose waves take
 // the steps of 128 k in turn and add up through LDS: bound by the weight's bytes
 // and, below some megabytes of them, by latency, so a wave has P steps of weights
 // in flight before it looks at x.  FUSED (MT = 1; ACT as in mx_kernels.hip): each
-// workgroup quantises the few rows of z itself, to LDS.  2x9216x1536 behind SiLU 4.5
+// workgroup quantises the few rows of z itself, to LDS.  2x9216x1536 behind SiLU 4.4
 // us, 1.7 TB/s; 77x4608x1536 4.5 us.
 template <int WAVES, int MT, int NT, bool FUSED, int ACT>
 __global__ __launch_bounds__(64 * WAVES) void mx_rows_kernel(MxRowsArgs a) {
@@ -109,30 +110,49 @@ __global__ __launch_bounds__(64 * WAVES) void mx_rows_kernel(MxRowsArgs a) {
       }
     }
   };
-  load(wave);
   // block kb of row m at 16 (kb M + m), its scale behind all of them
   uint8_t *const codes = smem, *const scales = smem + (K >> 5) * M * 16;
   if (FUSED) {
-    for (int m = 0; m < M; ++m)
-      for (int k = 8 * threadIdx.x; k < K; k += 8 * 64 * WAVES) {
-        v4u v = *reinterpret_cast<const v4u *>(a.z + m * a.ld_z + k);
+    // 8 values at a time; all of a thread's, up to Z, are asked for before any is waited
+    // for, and before the weights: loads come back in order
+    constexpr int Z = 4, kThreads = 64 * WAVES;
+    const uint32_t per = (uint32_t)K >> 3, all = M * per;
+    v4u v[Z];
+    auto ask = [&](uint32_t first) {
+#pragma unroll
+      for (int i = 0; i < Z; ++i) {
+        const uint32_t e = min(first + i * kThreads, all - 1), m = __umulhi(e, a.per_row);
+        v[i] = *reinterpret_cast<const v4u *>(a.z + m * a.ld_z + 8 * (e - m * per));
+      }
+    };
+    ask(threadIdx.x);
+    load(wave);
+    for (uint32_t first = threadIdx.x; first < all; first += Z * kThreads) {
+      if (first != threadIdx.x) ask(first);
+#pragma unroll
+      for (int i = 0; i < Z; ++i) {
+        const uint32_t e = first + i * kThreads, m = __umulhi(e, a.per_row), k8 = e - m * per;
+        if (e >= all) break;
         if (ACT) {
           float f[8];
-          unpack8(v, f);
+          unpack8(v[i], f);
           if (ACT == 1) silu8_hw(f);
           if (ACT == 2) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = gelu_bf16(f[i]);
+            for (int j = 0; j < 8; ++j) f[j] = gelu_bf16(f[j]);
           }
-          v = pack8(f);
+          v[i] = pack8(f);
         }
         uint32_t byte;
-        const uint32_t c = mx_piece(v, byte);
-        const int at = (k >> 5) * M + m, q = k >> 3 & 3;
+        const uint32_t c = mx_piece(v[i], byte);
+        const int at = (k8 >> 2) * M + m, q = k8 & 3;
         *reinterpret_cast<uint32_t *>(codes + 16 * at + 4 * q) = c;
         if (q == 0) scales[at] = (uint8_t)byte;
       }
+    }
     __syncthreads();
+  } else {
+    load(wave);
   }
   v4f acc[MT][NT];
 #pragma unroll
@@ -482,7 +502,7 @@ constexpr MxTile kMxTiles[] = {
 
 template <int WAVES, int MT, int NT>
 static hipError_t launch_rows(const MxGemmProblem &p, hipStream_t s) {
-  const MxRowsArgs a{p, nullptr, 0, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K)};
+  const MxRowsArgs a{p, nullptr, 0, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K), 0};
   const int64_t nt = p.N / 16, mt = mx_row_tiles(p.M);
   hipLaunchKernelGGL((mx_rows_kernel<WAVES, MT, NT, false, 0>),
                      dim3((unsigned)((nt + NT - 1) / NT), (unsigned)((mt + MT - 1) / MT)),
@@ -514,21 +534,23 @@ static hipError_t launch_fused(const MxRowsArgs &a, int32_t act, hipStream_t s) 
   return hipGetLastError();
 }
 
-// Every workgroup quantises all of z again: up to 32 values a thread.  In a
+// Every workgroup quantises all of z again: up to 48 values a thread.  In a
 // captured graph, where a second launch costs least, with no activation / SiLU /
-// GELU: 4 x 1536 (24 values) 3.9 / 4.8 / 5.9 us against 5.3 / 5.8 / 6.3 in two
-// launches, 8 x 1536 (48) 5.0 / 6.8 / 8.8 against 5.3 / 5.7 / 6.3 (N = 9216); a
-// second launch from the host costs 5 us more.
+// GELU: 4 x 1536 (24 values) 3.8 / 4.6 / 5.3 us against 5.3 / 5.8 / 6.3 in two
+// launches, 8 x 1536 (48) 4.6 / 6.1 / 7.6 against 5.4 / 6.2 / 6.2, 16 x 1536 (96)
+// 5.8 / 8.8 / 11.8 against 5.6 / 6.2 / 6.3 (N = 9216); from the host the second
+// launch costs 3 us more.
 static int fused_waves(int64_t K) { return mx_tiles_k(K) >= 16 ? 8 : 4; }
 
 bool mx_quantises_inside(int64_t M, int64_t K) {
-  return M <= 16 && M * K <= 32 * 64 * fused_waves(K);
+  return M <= 16 && M * K <= 48 * 64 * fused_waves(K);
 }
 
 // Two column tiles a workgroup where that leaves a workgroup per CU.
 hipError_t launch_gemm_mx_bf16(const MxGemmProblem &p, const uint16_t *z, int64_t ld_z, int32_t act,
                                hipStream_t s) {
-  const MxRowsArgs a{p, z, ld_z, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K)};
+  const MxRowsArgs a{p, z, ld_z, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K),
+                     (uint32_t)((1ll << 32) / (p.K / 8) + 1)};
   const bool eight = fused_waves(p.K) == 8;
   if (p.N / 16 >= 512) return eight ? launch_fused<8, 2>(a, act, s) : launch_fused<4, 2>(a, act, s);
   return eight ? launch_fused<8, 1>(a, act, s) : launch_fused<4, 1>(a, act, s);

@@ -249,7 +249,8 @@ def test_product_behind_an_activation_is_the_quantiser_s(M, act):
                   1600)
 
 
-@pytest.mark.parametrize("M,N,K", [(4, 9216, 1536), (5, 96, 1600), (4, 48, 4096), (1, 32, 16384),
+@pytest.mark.parametrize("M,N,K", [(8, 9216, 1536), (4, 64, 6144), (12, 8208, 1024), (3, 80, 8192),
+                                   (4, 9216, 1536), (5, 96, 1600), (4, 48, 4096), (1, 32, 16384),
                                    (8, 8208, 2048), (16, 16, 512), (3, 16, 64), (2, 8192, 192)])
 @pytest.mark.parametrize("act", list(ACTS))
 def test_few_rows_are_quantised_inside(M, N, K, act):
