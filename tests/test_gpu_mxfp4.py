@@ -218,6 +218,25 @@ def test_rows_far_apart():
     assert torch.equal(S.segquant_gemm_mxfp4(None, w, N, K=K, xq=mx, out=y), want)
 
 
+@pytest.mark.parametrize("act", list(ACTS))
+def test_more_rows_than_a_launch_takes(act):
+    """1048544 rows fill one launch of the quantiser; its rows and the product's, on
+    both sides of the border, are those of a call on them alone."""
+    g = gen(12)
+    M, N, K, border = 1048544 + 41, 48, 64, 1048544
+    z = normal(g, M, K).to(BF)
+    codes, scales = S.segquant_quantize_mxfp4(z, ACTS[act])
+    w = S.segquant_quantize_weight_mxfp4(normal(g, K, N))
+    y = S.segquant_gemm_mxfp4(z, w, N, act_kind=ACTS[act])
+    for first, last in [(0, 64), (border - 32, border + 32), (border, M)]:
+        c, s = S.segquant_quantize_mxfp4(z[first:last], ACTS[act])
+        assert torch.equal(codes[first * 64:][:c.numel()], c)
+        assert torch.equal(scales[first * 16:][:s.numel()], s)
+        # K = 64 is one instruction: every form of the product gives the same bits
+        assert torch.equal(S.segquant_gemm_mxfp4(z[first:last], w, N, act_kind=ACTS[act]),
+                           y[first:last])
+
+
 def test_calls_at_once_on_two_streams():
     g = gen(21)
     N, K = 1536, 1536
