@@ -489,15 +489,16 @@ static float mx_rows_cost(const MxGemmArgs &a) {
 }
 
 // Measured, the chosen one against the next best (us): 9216x4608x12288 224x256 220,
-// 256x256 228, 192x256 242; 8192^3 256x256 232, 224x256 244; 3000x3200x2560 160x256
-// 16.4, 192x256 17.3; 2048x4608x1536 160x256 12.1, 192x256 12.7; 4429x4608x1536
-// 160x256 21.3, 128x128 21.7; 4096x1536x6144 128x256 23.5, 128x128 24.4;
-// 1024x1536x1536 64x128 5.2, split K 5.8, 128x128 6.5; 256x1536x6144 split K 6.2,
-// 64x128 10.4.
+// 256x256 228, 192x256 242; 8192^3 256x256 232, 224x256 244; 4429x4608x1536 128x128
+// 24.8, 192x256 25.9; 3000x3200x2560 192x256 18.8, 224x256 20.0; 4096x1536x6144
+// 128x256 23.5, 128x128 24.4; 1024x1536x1536 64x128 5.2, split K 5.8, 128x128 6.5;
+// 256x1536x6144 split K 6.2, 64x128 10.4.  160x256 was left out: 3000x3200x2560 16.4
+// and 2048x4608x1536 12.1 against 12.7 with operands in the caches, but with operands
+// from memory, behind the norm and before the rotary positions, 4429x4608x1536 took 54
+// us in all against 47.
 constexpr MxTile kMxTiles[] = {
     {16, 16, 1, 0.78f, 5.5f}, {14, 16, 1, 0.69f, 6.5f}, {12, 16, 1, 0.59f, 5.6f},
-    {10, 16, 1, 0.49f, 4.8f}, {8, 16, 1, 0.41f, 3.6f},  {8, 8, 2, 0.49f, 3.3f},
-    {4, 8, 3, 0.47f, 2.6f},
+    {8, 16, 1, 0.41f, 3.6f},  {8, 8, 2, 0.49f, 3.3f},   {4, 8, 3, 0.47f, 2.6f},
 };
 
 template <int WAVES, int MT, int NT>
@@ -569,9 +570,8 @@ hipError_t launch_gemm_mx(const MxGemmProblem &p, hipStream_t s) {
     case 0: return launch_mx_lds<8, 4, 2, 4, 2>(a, s);
     case 1: return launch_mx_lds<7, 4, 2, 4, 2>(a, s);
     case 2: return launch_mx_lds<6, 4, 2, 4, 2>(a, s);
-    case 3: return launch_mx_lds<5, 4, 2, 4, 2>(a, s);
-    case 4: return launch_mx_lds<4, 4, 2, 4, 2>(a, s);
-    case 5: return launch_mx_lds<4, 4, 2, 2, 2>(a, s);
+    case 3: return launch_mx_lds<4, 4, 2, 4, 2>(a, s);
+    case 4: return launch_mx_lds<4, 4, 2, 2, 2>(a, s);
     default: return launch_mx_lds<2, 4, 2, 2, 1>(a, s);  // three workgroups' LDS fit a CU
   }
 }
