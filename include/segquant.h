@@ -343,8 +343,8 @@ int segquant_unpack_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t R
  *               given (SEGQ_ERR_UNSUPPORTED with fewer), contents undefined
  *               afterwards; calls that share one must be ordered.  NULL where
  *               that size is 0.
- * One launch, or quantisation and product where a workspace is asked for.  The
- * order of every sum is fixed.  y_bf16 and the workspace must not overlap each
+ * One launch, or quantisation and product where a workspace is asked for (some of
+ * those calls leave it unused).  The order of every sum is fixed.  y_bf16 and the workspace must not overlap each
  * other or an input: SEGQ_ERR_SHAPE.  Requires K % 64 == 0, N % 16 == 0, 16-byte
  * aligned pointers (scales 4), ld_z and ld_y multiples of 8, M and N <= 2^27,
  * K <= 2^22, M * N <= 2^37.  M may be 0.

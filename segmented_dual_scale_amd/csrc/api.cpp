@@ -780,7 +780,7 @@ int segquant_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint16_t *z_bf16,
                          {"w_scales", one_run(w_scales, sq::mx_scale_bytes(N, K))}};
   if ((st = check_apart(outs, ins))) return st;
   sq::MxGemmProblem p{M, N, K, x_codes, x_scales, w_codes, w_scales, y_bf16, ld_y};
-  if (z_bf16 && !need)
+  if (z_bf16 && (!need || (act_kind == SEGQ_ACT_NONE && sq::mx_rows_inside(M, N, K))))
     return hip_status(sq::launch_gemm_mx_bf16(p, z_bf16, ld_z, act_kind, (hipStream_t)stream),
                       "gemm_mxfp4 launch");
   if (z_bf16) {

@@ -65,12 +65,12 @@ struct MxRowsArgs {
 // MT tiles of x rows and NT tiles of w columns to a workgroup, whose waves take
 // the steps of 128 k in turn and add up through LDS: bound by the weight's bytes
 // and, below some megabytes of them, by latency, so a wave has P steps of weights
-// in flight before it looks at x.  FUSED (MT = 1; ACT as in mx_kernels.hip): each
-// workgroup quantises the few rows of z itself, to LDS.  2x9216x1536 behind SiLU 4.4
+// in flight before it looks at x.  FUSED (ACT as in mx_kernels.hip): each
+// workgroup quantises its rows of z itself, to LDS.  2x9216x1536 behind SiLU 4.4
 // us, 1.7 TB/s; 77x4608x1536 4.5 us.
 template <int WAVES, int MT, int NT, bool FUSED, int ACT>
 __global__ __launch_bounds__(64 * WAVES) void mx_rows_kernel(MxRowsArgs a) {
-  constexpr int P = MT == 1 ? 4 : 3;
+  constexpr int P = FUSED && MT > 1 ? 2 : MT == 1 ? 4 : 3;
   extern __shared__ uint8_t smem[];
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -110,19 +110,21 @@ __global__ __launch_bounds__(64 * WAVES) void mx_rows_kernel(MxRowsArgs a) {
       }
     }
   };
-  // block kb of row m at 16 (kb M + m), its scale behind all of them
-  uint8_t *const codes = smem, *const scales = smem + (K >> 5) * M * 16;
+  // block kb of the m-th of these rows at 16 (kb rows + m), its scale behind all of them
+  const int rows = min(16 * MT, M - 16 * m0);
+  uint8_t *const codes = smem, *const scales = smem + (K >> 5) * rows * 16;
   if (FUSED) {
     // 8 values at a time; all of a thread's, up to Z, are asked for before any is waited
     // for, and before the weights: loads come back in order
     constexpr int Z = 4, kThreads = 64 * WAVES;
-    const uint32_t per = (uint32_t)K >> 3, all = M * per;
+    const uint32_t per = (uint32_t)K >> 3, all = rows * per;
+    const uint16_t *const z = a.z + 16 * m0 * a.ld_z;
     v4u v[Z];
     auto ask = [&](uint32_t first) {
 #pragma unroll
       for (int i = 0; i < Z; ++i) {
         const uint32_t e = min(first + i * kThreads, all - 1), m = __umulhi(e, a.per_row);
-        v[i] = *reinterpret_cast<const v4u *>(a.z + m * a.ld_z + 8 * (e - m * per));
+        v[i] = *reinterpret_cast<const v4u *>(z + m * a.ld_z + 8 * (e - m * per));
       }
     };
     ask(threadIdx.x);
@@ -145,7 +147,7 @@ __global__ __launch_bounds__(64 * WAVES) void mx_rows_kernel(MxRowsArgs a) {
         }
         uint32_t byte;
         const uint32_t c = mx_piece(v[i], byte);
-        const int at = (k8 >> 2) * M + m, q = k8 & 3;
+        const int at = (k8 >> 2) * rows + m, q = k8 & 3;
         *reinterpret_cast<uint32_t *>(codes + 16 * at + 4 * q) = c;
         if (q == 0) scales[at] = (uint8_t)byte;
       }
@@ -171,10 +173,10 @@ __global__ __launch_bounds__(64 * WAVES) void mx_rows_kernel(MxRowsArgs a) {
         v4u c = xt[p][i];
         uint32_t s = xs[p][i] >> shift;
         if (FUSED) {
-          const int kb = 4 * u + g, at = kb * M + r;
+          const int kb = 4 * u + g, at = kb * rows + 16 * i + r;
           c = v4u{0u, 0u, 0u, 0u};
           s = 0;
-          if (r < M && 32 * kb < K) {
+          if (16 * i + r < rows && 32 * kb < K) {
             c = *reinterpret_cast<const v4u *>(codes + 16 * at);
             s = scales[at];
           }
@@ -481,11 +483,9 @@ static float mx_cost(const MxTile &t, const MxGemmArgs &a) {
 // The same by workgroups of 32 x 32 that split K over their waves: 4 KiB a step
 // and workgroup from the L2 at 22 TB/s, and a chain of loads for each of a wave's
 // steps.
-static int mx_rows_waves(int64_t kt) { return kt >= 16 ? 8 : 4; }
-
 static float mx_rows_cost(const MxGemmArgs &a) {
   const float groups = (float)((a.mt + 1) / 2) * (float)((a.nt + 1) / 2), kt = (float)a.kt;
-  return 2.0f + groups * kt * (4096.0f / 22e6f) + 0.25f * kt / (float)mx_rows_waves(a.kt);
+  return 2.0f + groups * kt * (4096.0f / 22e6f) + 0.25f * kt / (a.kt >= 16 ? 8.0f : 4.0f);
 }
 
 // Measured, the chosen one against the next best (us): 9216x4608x12288 224x256 220,
@@ -520,22 +520,43 @@ static hipError_t launch_one_row_tile(const MxGemmProblem &p, hipStream_t s) {
   return kt >= 16 ? launch_rows<8, 1, 1>(p, s) : launch_rows<4, 1, 1>(p, s);
 }
 
-template <int WAVES, int NT>
+template <int WAVES, int MT, int NT>
 static hipError_t launch_fused(const MxRowsArgs &a, int32_t act, hipStream_t s) {
-  const dim3 grid((unsigned)((a.p.N / 16 + NT - 1) / NT)), block(64 * WAVES);
-  const size_t codes = (size_t)(a.p.M * (a.p.K / 32) * 17);
-  size_t lds = sizeof(float) * 4 * 64 * NT * WAVES;
+  const int64_t mt = mx_row_tiles(a.p.M), rows = a.p.M < 16 * MT ? a.p.M : 16 * MT;
+  const dim3 grid((unsigned)((a.p.N / 16 + NT - 1) / NT), (unsigned)((mt + MT - 1) / MT));
+  const dim3 block(64 * WAVES);
+  const size_t codes = (size_t)(rows * (a.p.K / 32) * 17);
+  size_t lds = sizeof(float) * 4 * 64 * MT * NT * WAVES;
   if (lds < codes) lds = codes;
 #define SQ_ROWS(ACT) \
-  hipLaunchKernelGGL((mx_rows_kernel<WAVES, 1, NT, true, ACT>), grid, block, lds, s, a)
-  if (act == 1) SQ_ROWS(1);
-  else if (act == 2) SQ_ROWS(2);
-  else SQ_ROWS(0);
+  hipLaunchKernelGGL((mx_rows_kernel<WAVES, MT, NT, true, ACT>), grid, block, lds, s, a)
+  if constexpr (MT == 1) {
+    if (act == 1) SQ_ROWS(1);
+    else if (act == 2) SQ_ROWS(2);
+    else SQ_ROWS(0);
+  } else {
+    SQ_ROWS(0);
+  }
 #undef SQ_ROWS
   return hipGetLastError();
 }
 
-// Every workgroup quantises all of z again: up to 48 values a thread.  In a
+// Workgroups of two row tiles and NT column tiles.
+static int64_t mx_groups(int64_t M, int64_t N, int nt) {
+  return ((N / 16 + nt - 1) / nt) * ((mx_row_tiles(M) + 1) / 2);
+}
+
+// More than 16 rows of bf16 without an activation: each workgroup quantises its 32 rows,
+// up to 96 values a thread, where one workgroup a CU or fewer do that.  In a captured
+// graph against two launches: 77x1536x1536 5.6 us against 6.2, 77x1536x512 3.7 against
+// 5.0, 77x4608x1536 6.7 against 6.4 (at two a CU 9.5 against 6.7); from the host the
+// second launch costs 3 us more.  An activation on top costs more than it: SiLU
+// 77x1536x1536 8.7 against 6.9.
+static bool mx_few_rows(int64_t M, int64_t N, int64_t K) {
+  return 32 * K <= 96 * 512 && mx_groups(M, N, 4) <= 256;
+}
+
+// Up to 16 rows: every workgroup quantises all of z, up to 48 values a thread.  In a
 // captured graph, where a second launch costs least, with no activation / SiLU /
 // GELU: 4 x 1536 (24 values) 3.8 / 4.6 / 5.3 us against 5.3 / 5.8 / 6.3 in two
 // launches, 8 x 1536 (48) 4.6 / 6.1 / 7.6 against 5.4 / 6.2 / 6.2, 16 x 1536 (96)
@@ -552,20 +573,46 @@ hipError_t launch_gemm_mx_bf16(const MxGemmProblem &p, const uint16_t *z, int64_
                                hipStream_t s) {
   const MxRowsArgs a{p, z, ld_z, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K),
                      (uint32_t)((1ll << 32) / (p.K / 8) + 1)};
+  if (p.M > 16)
+    return mx_groups(p.M, p.N, 2) <= 256 ? launch_fused<8, 2, 2>(a, act, s)
+                                         : launch_fused<8, 2, 4>(a, act, s);
   const bool eight = fused_waves(p.K) == 8;
-  if (p.N / 16 >= 512) return eight ? launch_fused<8, 2>(a, act, s) : launch_fused<4, 2>(a, act, s);
-  return eight ? launch_fused<8, 1>(a, act, s) : launch_fused<4, 1>(a, act, s);
+  if (p.N / 16 >= 512)
+    return eight ? launch_fused<8, 1, 2>(a, act, s) : launch_fused<4, 1, 2>(a, act, s);
+  return eight ? launch_fused<8, 1, 1>(a, act, s) : launch_fused<4, 1, 1>(a, act, s);
+}
+
+// The cheapest tile shape, or -1 for the kernel that splits K over its waves.
+static int mx_choice(const MxGemmArgs &a) {
+  int best = 0;
+  for (int i = 1; i < (int)(sizeof kMxTiles / sizeof kMxTiles[0]); ++i)
+    if (mx_cost(kMxTiles[i], a) < mx_cost(kMxTiles[best], a)) best = i;
+  return mx_rows_cost(a) < mx_cost(kMxTiles[best], a) && a.mt <= 65535 ? -1 : best;
+}
+
+static MxGemmArgs mx_args(const MxGemmProblem &p) {
+  return {p, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K), (int32_t)mx_row_tiles(p.M),
+          (int32_t)mx_row_tiles(p.N), 0, 0};
+}
+
+bool mx_rows_inside(int64_t M, int64_t N, int64_t K) {
+  if (M <= 16 || !mx_few_rows(M, N, K)) return false;
+  MxGemmProblem p{};
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  return mx_choice(mx_args(p)) < 0;
 }
 
 hipError_t launch_gemm_mx(const MxGemmProblem &p, hipStream_t s) {
   if (p.M <= 16) return launch_one_row_tile(p, s);
-  const MxGemmArgs a{p, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K),
-                     (int32_t)mx_row_tiles(p.M), (int32_t)mx_row_tiles(p.N), 0, 0};
-  int best = 0;
-  for (int i = 1; i < (int)(sizeof kMxTiles / sizeof kMxTiles[0]); ++i)
-    if (mx_cost(kMxTiles[i], a) < mx_cost(kMxTiles[best], a)) best = i;
-  if (mx_rows_cost(a) < mx_cost(kMxTiles[best], a) && a.mt <= 65535)
-    return mx_rows_waves(a.kt) == 8 ? launch_rows<8, 2, 2>(p, s) : launch_rows<4, 2, 2>(p, s);
+  const MxGemmArgs a = mx_args(p);
+  const int best = mx_choice(a);
+  // eight waves where the product of bf16 input has them, so that both give the same
+  // bits (of up to four steps the order is the same); otherwise by time
+  if (best < 0)
+    return a.kt >= 16 || (a.kt > 4 && mx_few_rows(p.M, p.N, p.K)) ? launch_rows<8, 2, 2>(p, s)
+                                                                  : launch_rows<4, 2, 2>(p, s);
   switch (best) {
     case 0: return launch_mx_lds<8, 4, 2, 4, 2>(a, s);
     case 1: return launch_mx_lds<7, 4, 2, 4, 2>(a, s);

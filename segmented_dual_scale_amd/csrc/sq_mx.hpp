@@ -54,9 +54,10 @@ struct MxGemmProblem {
 };
 
 hipError_t launch_gemm_mx(const MxGemmProblem &p, hipStream_t s);
-// Whether the product of bf16 input of this size quantises it itself, and that
-// product (x and x_scale of the problem unused).
+// Whether the product of bf16 input of this size quantises it itself: with any
+// activation; with none.  And that product (x and x_scale of the problem unused).
 bool mx_quantises_inside(int64_t M, int64_t K);
+bool mx_rows_inside(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_mx_bf16(const MxGemmProblem &p, const uint16_t *z, int64_t ld_z, int32_t act,
                                hipStream_t s);
 

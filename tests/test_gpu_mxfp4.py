@@ -284,6 +284,26 @@ def test_few_rows_are_quantised_inside(M, N, K, act):
     product_close(y, S.segquant_unpack_mxfp4(mx, M, K), S.segquant_unpack_mxfp4(w, N, K), K)
 
 
+@pytest.mark.parametrize("M,N,K", [(17, 48, 64), (31, 2064, 1472), (32, 16, 128), (33, 80, 192),
+                                   (48, 4624, 1536), (77, 1536, 1536), (77, 4608, 1536),
+                                   (250, 512, 640), (345, 176, 320), (1000, 64, 576)])
+def test_rows_without_an_activation_give_the_bits_of_their_codes(M, N, K):
+    g = gen(M + N + K)
+    z = (normal(g, M, K) * torch.exp(normal(g, M, 1))).to(BF)
+    z[M // 2, K // 2:] = 0
+    z[M - 1, 3] = float("inf")  # a row of NaN
+    _, z = padded(z, K + 8, float("nan"))
+    w = S.segquant_quantize_weight_mxfp4(normal(g, K, N))
+    mx = S.segquant_quantize_mxfp4(z)
+    ybuf, y = padded(torch.zeros(M, N, device=DEV, dtype=BF), N + 8, 7.0)
+    S.segquant_gemm_mxfp4(z, w, N, out=y)
+    want = S.segquant_gemm_mxfp4(None, w, N, K=K, xq=mx, M=M)
+    assert torch.isnan(y[-1]).all() and torch.isnan(want[-1]).all()
+    assert torch.equal(y[:-1], want[:-1])
+    product_close(y[:-1], S.segquant_unpack_mxfp4(mx, M, K)[:-1], S.segquant_unpack_mxfp4(w, N, K), K)
+    assert (ybuf[:, N:] == 7.0).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 64, 256), (200, 128, 192), (700, 1024, 512)])
 def test_ones_and_powers_are_exact(M, N, K):
     """Small integers and powers of two: every sum is exact in fp32."""
