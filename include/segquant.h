@@ -375,8 +375,8 @@ size_t segquant_gemm_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * At least one of h_out, q_out, x_out and mx_codes.  One launch, no workspace;
  * the order of every sum is fixed.  Alignment as segquant_adanorm_quantize
  * (mx_codes 16, mx_scales 4).  M may be 0.  Outputs must not overlap each other
- * or, but for h_out as there, inputs: SEGQ_ERR_SHAPE.  Values above about 2^60
- * in magnitude overflow the fp32 squares.
+ * or, but for h_out as there, inputs: SEGQ_ERR_SHAPE.  Any finite h' will do: where
+ * its squares overflow fp32, the row is summed once more with smaller values.
  */
 int segquant_rmsnorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int64_t ld_h,
                               const uint16_t *branch, int64_t ld_b, uint16_t *h_out, int64_t ld_ho,

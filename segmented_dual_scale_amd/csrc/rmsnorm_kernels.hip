@@ -43,6 +43,19 @@ __device__ __forceinline__ void rms_pad(const RmsNormProblem &a, int64_t r, int 
   a.mx.scales[mx_scale_at(a.mx, r, kb)] = 0;
 }
 
+// s and the squares of a piece.  SMALL: of its values times 2^-80.
+template <bool SMALL>
+__device__ __forceinline__ float add_squares(v4u h, float s) {
+  float f[8];
+  unpack8(h, f);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (SMALL) f[j] *= kSmall;
+    s = __builtin_fmaf(f[j], f[j], s);
+  }
+  return s;
+}
+
 template <int TPR, int NCH, bool TAIL>
 __global__ __launch_bounds__(256) void rmsnorm_kernel(RmsNormProblem a) {
   __shared__ float lds[4];
@@ -97,13 +110,15 @@ __global__ __launch_bounds__(256) void rmsnorm_kernel(RmsNormProblem a) {
     if (TAIL) h[NCH - 1] = keep8<TAIL>(h[NCH - 1], n_last);
     float s = 0.0f;
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      float f[8];
-      unpack8(h[c], f);
+    for (int c = 0; c < NCH; ++c) s = add_squares<false>(h[c], s);
+    const float mean = row_sum<TPR>(s, lds) * inv_k + a.eps;
+    float rstd = __builtin_amdgcn_rsqf(mean);
+    if (__builtin_expect(mean == INFINITY, 0)) {  // the same in all threads of the row
+      s = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s = __builtin_fmaf(f[j], f[j], s);
+      for (int c = 0; c < NCH; ++c) s = add_squares<true>(h[c], s);
+      rstd = small_rsq(row_sum<TPR>(s, lds) * inv_k, a.eps);
     }
-    const float rstd = __builtin_amdgcn_rsqf(row_sum<TPR>(s, lds) * inv_k + a.eps);
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       if (c == NCH - 1 && n_last == 0) continue;
@@ -140,13 +155,16 @@ __global__ __launch_bounds__(256) void rmsnorm_long_kernel(RmsNormProblem a) {
       return keep8<true>(v, n);
     };
     float s = 0.0f;
-    for (int64_t k = 8 * threadIdx.x; k < a.K; k += 8 * 256) {
-      float f[8];
-      unpack8(piece(k, (int)min((int64_t)8, a.K - k)), f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s = __builtin_fmaf(f[j], f[j], s);
+    for (int64_t k = 8 * threadIdx.x; k < a.K; k += 8 * 256)
+      s = add_squares<false>(piece(k, (int)min((int64_t)8, a.K - k)), s);
+    const float mean = row_sum<256>(s, lds) / (float)a.K + a.eps;
+    float rstd = __builtin_amdgcn_rsqf(mean);
+    if (mean == INFINITY) {
+      s = 0.0f;
+      for (int64_t k = 8 * threadIdx.x; k < a.K; k += 8 * 256)
+        s = add_squares<true>(piece(k, (int)min((int64_t)8, a.K - k)), s);
+      rstd = small_rsq(row_sum<256>(s, lds) / (float)a.K, a.eps);
     }
-    const float rstd = __builtin_amdgcn_rsqf(row_sum<256>(s, lds) / (float)a.K + a.eps);
     for (int64_t k = 8 * threadIdx.x; k < a.K; k += 8 * 256) {
       const int n = (int)min((int64_t)8, a.K - k);
       const v4u v = piece(k, n);  // before h' is stored, which may be where h or branch is

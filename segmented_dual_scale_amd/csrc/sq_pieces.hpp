@@ -3,6 +3,8 @@
 // rotary_kernels.hip, mx_kernels.hip and gemm_mx.hip.
 #pragma once
 
+#include <cmath>
+
 #include "sq_rows.hpp"
 
 namespace sq {
@@ -101,6 +103,17 @@ __device__ __forceinline__ void load8f(const float *p, int n, float dflt, float 
     for (int j = 0; j < 8; ++j)
       if (j < n) f[j] = p[j];
   }
+}
+
+// A row of finite values whose squares overflow is summed once more, its values
+// times kSmall: the largest square is then 2^96, and what the sum of those that
+// vanish could add is below 2^-63 of it.  1 / sqrt(mean + eps) from the mean of such
+// squares; below 2^-126, where the values are near the largest of all, its last bit
+// is 2^-21 of it.
+constexpr float kSmall = 0x1p-80f;
+
+__device__ __forceinline__ float small_rsq(float mean, float eps) {
+  return __builtin_amdgcn_rsqf(mean + eps * kSmall * kSmall) * kSmall;
 }
 
 // Inverse scales of the K-segment that holds column k (every boundary is a
