@@ -110,8 +110,19 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryProblem a) {
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < 16; ++j) s = __builtin_fmaf(f[j], f[j], s);
-    s = __builtin_amdgcn_rsqf(part_sum(s, LPH) * inv_d + a.eps);
-    const float rstd = a.norm ? s : 1.0f;
+    const float mean = part_sum(s, LPH) * inv_d + a.eps;
+    float rstd = a.norm ? __builtin_amdgcn_rsqf(mean) : 1.0f;
+    const bool large = a.norm && mean == INFINITY;
+    if (__builtin_expect(__any(large), 0)) {
+      s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float v = f[j] * kSmall;
+        s = __builtin_fmaf(v, v, s);
+      }
+      s = small_rsq(part_sum(s, LPH) * inv_d, a.eps);
+      rstd = large ? s : rstd;
+    }
 #pragma unroll
     for (int j = 0; j < 16; ++j) f[j] *= rstd;
     float o[16];

@@ -107,3 +107,40 @@ def test_infinities_are_still_their_rows():
     hit[5] = hit[290] = True
     assert torch.equal(x[~hit], clean[~hit])
     assert x[5, 3].isnan() and x[290].isnan().all()
+
+
+@pytest.mark.parametrize("B,L,Hq,Hk,D,R", [(1, 7, 3, 1, 16, 16), (2, 50, 7, 2, 40, 32),
+                                           (1, 33, 24, 24, 64, 64), (1, 700, 24, 12, 64, 64),
+                                           (1, 900, 16, 16, 128, 128), (1, 300, 40, 10, 72, 48),
+                                           (1, 6, 4, 2, 256, 64), (1, 5, 3, 2, 512, 512)])
+@pytest.mark.parametrize("style", [S.SEGQ_ROTARY_PAIRS, S.SEGQ_ROTARY_HALVES])
+def test_heads_whose_squares_overflow(B, L, Hq, Hk, D, R, style):
+    """The norm's factor is off by less than 2^-19 (21 * 2^-24 of the sum, halved by the
+    root, that root's 2^-22 and a few roundings), sine and cosine by less than 2^-22:
+    2^-18 (|a| + |b|) of a pair, besides the rounding to bf16."""
+    g = gen(D + L)
+    pos = torch.randint(-5000, 20000, (L, 1), generator=g, device=DEV, dtype=torch.int32)
+    freq = S.segquant_rotary_frequencies([R]).to(DEV)
+    q, k = (rows(g, B * L * H, D).view(B, L, H, D) for H in (Hq, Hk))
+    gq, gk = 1 + 0.3 * normal(g, D), 1 + 0.3 * normal(g, D)
+    got = S.segquant_qk_rotary(q, k, pos, freq, [R], style, gq, gk)
+    u = pos.double() * freq
+    c, s = torch.cos(u)[:, None], torch.sin(u)[:, None]
+    for t, gamma, y in ((q, gq, got[0]), (k, gk, got[1])):
+        t = norm_ref(t, gamma, 1e-6)
+        out, size = t.clone(), t.abs()
+        a, b = ((slice(0, R, 2), slice(1, R, 2)) if style == S.SEGQ_ROTARY_PAIRS
+                else (slice(0, R // 2), slice(R // 2, R)))
+        out[..., a] = t[..., a] * c - t[..., b] * s
+        out[..., b] = t[..., b] * c + t[..., a] * s
+        size[..., a] = size[..., b] = t[..., a].abs() + t[..., b].abs()
+        err, tol = (y.double() - out).abs(), 2.0 ** -8 * out.abs() + 2.0 ** -18 * size + 2.0 ** -133
+        assert (err <= tol).all(), (float((err - tol).max()), int((err > tol).sum()))
+
+
+def test_large_heads_without_the_norm():
+    g = gen(6)
+    q = rows(g, 70, 64).view(1, 10, 7, 64)
+    freq = S.segquant_rotary_frequencies([16]).to(DEV)
+    pos = torch.zeros(10, 1, device=DEV, dtype=torch.int32)
+    assert torch.equal(S.segquant_qk_rotary(q, None, pos, freq, [16], norm=False)[0], q)
