@@ -404,7 +404,8 @@ int segquant_rmsnorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
  *   out = bf16_rne(t'); elements from R on are not turned
  * R is the sum of the axis widths: the first axis has the first
  * axis_width[0] / 2 pairs, and so on.  Angles are formed in fp64 and reduced
- * before they are rounded: any int32 position is as good as a small one.
+ * before they are rounded: any int32 position is as good as a small one, at
+ * frequencies up to 2^48 in magnitude.
  * The norm takes any finite head, as segquant_rmsnorm_quantize.
  *   q, k        device bf16 [B][L][heads][D], any strides, which are HOST
  *               arrays of three: elements between samples, tokens and heads,

@@ -26,8 +26,13 @@ __device__ __forceinline__ float2 turn(int position, double freq) {
   const double u = (double)position * freq, u_lo = __builtin_fma((double)position, freq, -u);
   const double t = u * kTurn;
   const double t_lo = __builtin_fma(u, kTurn, -t) + __builtin_fma(u, kTurnLo, u_lo * kTurn);
-  const double quarter = __builtin_rint(4.0 * t);
-  const float x = (float)((t - 0.25 * quarter) + t_lo) * 6.28318530717958647692f;
+  double quarter = __builtin_rint(4.0 * t);
+  double rest = (t - 0.25 * quarter) + t_lo;
+  // past 2^40 turns or so what the rounding left is whole quarters itself
+  const double more = __builtin_rint(4.0 * rest);
+  rest -= 0.25 * more;
+  quarter = (quarter - 4.0 * __builtin_floor(0.25 * quarter)) + more;
+  const float x = (float)rest * 6.28318530717958647692f;
   const int q = (int)(quarter - 4.0 * __builtin_floor(0.25 * quarter));  // 0..3
   const float z = x * x;
   float s = __builtin_fmaf(z, 2.7557319e-6f, -1.9841270e-4f);  // 1/9!, -1/7!
