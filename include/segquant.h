@@ -424,9 +424,10 @@ int segquant_rmsnorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int6
  * SEGQ_ROTARY_MAX_HEAD, 16-byte aligned q, k, outputs and gammas, 8-byte aligned
  * freq, B * L * heads <= 2^30 for q and k together.  B or L may be 0.  An output
  * must not overlap itself, the other or, but for its own as above, an input:
- * SEGQ_ERR_SHAPE.  Beside another tensor of the same sample and token strides
- * (q and k inside one QKV matrix) the overlap is exact, else an output's whole
- * extent counts where its rows are not evenly spaced.
+ * SEGQ_ERR_SHAPE.  Beside another tensor of the same sample and token strides,
+ * and heads side by side in both or of one stride (q and k inside one QKV
+ * matrix), the overlap is exact; else a tensor's whole extent counts where its
+ * rows are not evenly spaced.
  */
 int segquant_qk_rotary(int64_t B, int64_t L, int32_t D, const uint16_t *q, int32_t q_heads,
                        const int64_t *q_stride, uint16_t *q_out, const int64_t *q_out_stride,

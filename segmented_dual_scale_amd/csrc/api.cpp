@@ -932,33 +932,56 @@ struct Heads {
   int64_t heads;
 };
 
+// A dimension that two tensors share: the stride, and how many of it each has.
+struct Level {
+  I128 stride;
+  int64_t nx, ny;
+};
+
+// Whether runs of wx and wy bytes at the levels, the widest stride first, share bytes,
+// y `at` bytes behind x.  Of each level only the distances are looked at over which
+// what is inside it could meet: two or three, unless a tensor overlaps itself.  Where
+// `steps` of them do not settle it, the two count as meeting.
+static bool levels_meet(const Level *v, int n, I128 wx, I128 wy, I128 at, int &steps) {
+  if (n == 0) return at > -wy && at < wx;
+  I128 ex = wx, ey = wy;  // of what is inside
+  for (int i = 1; i < n; ++i) {
+    ex += v[i].stride * (v[i].nx - 1);
+    ey += v[i].stride * (v[i].ny - 1);
+  }
+  I128 first = floor_div(-ey - at, v->stride) + 1, last = floor_div(ex - 1 - at, v->stride);
+  if (first < 1 - v->nx) first = 1 - v->nx;
+  if (last > v->ny - 1) last = v->ny - 1;
+  if (n == 1) return first <= last;
+  for (I128 i = first; i <= last; ++i)
+    if (--steps < 0 || levels_meet(v + 1, n - 1, wx, wy, at + i * v->stride, steps)) return true;
+  return false;
+}
+
 static bool heads_meet(const Heads &x, const Heads &y, int64_t B, int64_t L, int64_t D) {
   bool ex, ey;
   const Rows rx = head_rows(x.p, x.stride, B, L, x.heads, D, ex);
   const Rows ry = head_rows(y.p, y.stride, B, L, y.heads, D, ey);
+  if (!rows_meet(rx, ry)) return false;
   const bool same = (B == 1 || x.stride[0] == y.stride[0]) && (L == 1 || x.stride[1] == y.stride[1]);
   const bool whole = (x.heads == 1 || x.stride[2] == D) && (y.heads == 1 || y.stride[2] == D);
-  if ((ex && ey) || !same || !whole) return rows_meet(rx, ry);
-  if (!rows_meet(rx, ry)) return false;
-  // two columns of one matrix per sample: offsets of a token of y from one of x
-  const I128 d = ((I128)reinterpret_cast<uintptr_t>(y.p) - (I128)reinterpret_cast<uintptr_t>(x.p));
-  const I128 wx = 2 * (I128)x.heads * D, wy = 2 * (I128)y.heads * D;
-  // walk the shorter of the two dimensions, at most 2^15 either way
-  const int walk = B <= L ? 0 : 1;
-  const int64_t n = walk ? L : B, other = walk ? B : L;
-  const I128 step = 2 * (I128)x.stride[walk], ld = 2 * (I128)x.stride[1 - walk];
-  for (int64_t i = 1 - n; i < n; ++i) {
-    const I128 at = d + i * step;  // at + j ld inside (-wy, wx) for some |j| < other?
-    if (other == 1 || ld == 0) {
-      if (at > -wy && at < wx) return true;
-      continue;
-    }
-    I128 first = floor_div(-wy - at, ld) + 1, last = floor_div(wx - 1 - at, ld);
-    if (first < 1 - other) first = 1 - other;
-    if (last > other - 1) last = other - 1;
-    if (first <= last) return true;
+  const bool apart = x.heads == 1 || y.heads == 1 || x.stride[2] == y.stride[2];
+  if ((ex && ey) || !same || !(whole || apart)) return true;
+  Level v[3] = {{2 * (I128)x.stride[0], B, B}, {2 * (I128)x.stride[1], L, L}, {0, 1, 1}};
+  I128 wx = 2 * (I128)D, wy = wx;
+  if (whole) wx *= x.heads, wy *= y.heads;
+  else v[2] = {2 * (I128)(x.heads > 1 ? x : y).stride[2], x.heads, y.heads};
+  int n = 0;  // levels without a stride or of one element drop out; the widest first
+  for (const Level l : v) {
+    if (l.stride == 0 || (l.nx == 1 && l.ny == 1)) continue;
+    int i = n++;
+    for (; i > 0 && v[i - 1].stride < l.stride; --i) v[i] = v[i - 1];
+    v[i] = l;
   }
-  return false;
+  int steps = 1 << 20;
+  return levels_meet(v, n, wx, wy,
+                     (I128)reinterpret_cast<uintptr_t>(y.p) - (I128)reinterpret_cast<uintptr_t>(x.p),
+                     steps);
 }
 
 static int check_heads(const uint16_t *p, const int64_t *stride, int64_t B, int64_t L,
