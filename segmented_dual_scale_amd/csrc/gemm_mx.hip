@@ -538,12 +538,19 @@ static hipError_t launch_rows(const MxGemmProblem &p, hipStream_t s) {
 }
 
 // Up to 16 rows.  Two column tiles a workgroup where that leaves a workgroup per
-// CU; as many waves as leave each two steps of K and the chip about 4096.
-static hipError_t launch_one_row_tile(const MxGemmProblem &p, hipStream_t s) {
+// CU; as many waves as leave each two steps of K and the chip about 4096.  The same for
+// rows of bf16 and of codes, which so have the same sums: 4x1536x6144 on 16 waves 4.7
+// and 3.7 us, on 8 5.4 and 4.3; 1x4096x4096 4.2 and 3.8, 4.2 and 3.8.
+static int one_row_tile_waves(const MxGemmProblem &p) {
   const int64_t nt = p.N / 16, kt = mx_tiles_k(p.K);
-  if (nt >= 512) return kt >= 16 ? launch_rows<8, 1, 2>(p, s) : launch_rows<4, 1, 2>(p, s);
-  if (kt >= 32 && nt <= 256) return launch_rows<16, 1, 1>(p, s);
-  return kt >= 16 ? launch_rows<8, 1, 1>(p, s) : launch_rows<4, 1, 1>(p, s);
+  return kt >= 32 && nt <= 256 ? 16 : kt >= 16 ? 8 : 4;
+}
+
+static hipError_t launch_one_row_tile(const MxGemmProblem &p, hipStream_t s) {
+  const int waves = one_row_tile_waves(p);
+  if (p.N / 16 >= 512) return waves == 8 ? launch_rows<8, 1, 2>(p, s) : launch_rows<4, 1, 2>(p, s);
+  if (waves == 16) return launch_rows<16, 1, 1>(p, s);
+  return waves == 8 ? launch_rows<8, 1, 1>(p, s) : launch_rows<4, 1, 1>(p, s);
 }
 
 template <int WAVES, int MT, int NT>
@@ -582,16 +589,14 @@ static bool mx_few_rows(int64_t M, int64_t N, int64_t K) {
   return 32 * K <= 96 * 512 && mx_groups(M, N, 4) <= 256;
 }
 
-// Up to 16 rows: every workgroup quantises all of z, up to 48 values a thread.  In a
-// captured graph, where a second launch costs least, with no activation / SiLU /
-// GELU: 4 x 1536 (24 values) 3.8 / 4.6 / 5.3 us against 5.3 / 5.8 / 6.3 in two
-// launches, 8 x 1536 (48) 4.6 / 6.1 / 7.6 against 5.4 / 6.2 / 6.2, 16 x 1536 (96)
-// 5.8 / 8.8 / 11.8 against 5.6 / 6.2 / 6.3 (N = 9216); from the host the second
-// launch costs 3 us more.
-static int fused_waves(int64_t K) { return mx_tiles_k(K) >= 16 ? 8 : 4; }
-
+// Up to 16 rows: every workgroup quantises all of z, up to 48 values a thread of 8 waves
+// (of 4 up to K = 1920).  In a captured graph, where a second launch costs least, with no
+// activation / SiLU / GELU: 4 x 1536 (24 values) 3.8 / 4.6 / 5.3 us against 5.3 / 5.8 /
+// 6.3 in two launches, 8 x 1536 (48) 4.6 / 6.1 / 7.6 against 5.4 / 6.2 / 6.2, 16 x 1536
+// (96) 5.8 / 8.8 / 11.8 against 5.6 / 6.2 / 6.3 (N = 9216); from the host the
+// second launch costs 3 us more.
 bool mx_quantises_inside(int64_t M, int64_t K) {
-  return M <= 16 && M * K <= 48 * 64 * fused_waves(K);
+  return M <= 16 && M * K <= 48 * 64 * (mx_tiles_k(K) >= 16 ? 8 : 4);
 }
 
 // Two column tiles a workgroup where that leaves a workgroup per CU.
@@ -602,10 +607,11 @@ hipError_t launch_gemm_mx_bf16(const MxGemmProblem &p, const uint16_t *z, int64_
   if (p.M > 16)
     return mx_groups(p.M, p.N, 2) <= 256 ? launch_fused<8, 2, 2>(a, act, s)
                                          : launch_fused<8, 2, 4>(a, act, s);
-  const bool eight = fused_waves(p.K) == 8;
+  const int waves = one_row_tile_waves(p);
   if (p.N / 16 >= 512)
-    return eight ? launch_fused<8, 1, 2>(a, act, s) : launch_fused<4, 1, 2>(a, act, s);
-  return eight ? launch_fused<8, 1, 1>(a, act, s) : launch_fused<4, 1, 1>(a, act, s);
+    return waves == 8 ? launch_fused<8, 1, 2>(a, act, s) : launch_fused<4, 1, 2>(a, act, s);
+  if (waves == 16) return launch_fused<16, 1, 1>(a, act, s);
+  return waves == 8 ? launch_fused<8, 1, 1>(a, act, s) : launch_fused<4, 1, 1>(a, act, s);
 }
 
 // The cheapest tile shape, or -1 for the kernel that splits K over its waves.
