@@ -303,7 +303,10 @@ size_t segquant_mxfp4_scale_bytes(int64_t R, int64_t K);
 
 /*
  * segquant_quantize_mxfp4 -- x = bf16_rne(act(z)), or z itself
- * (SEGQ_ACT_NONE), as MXFP4; act as in segquant_groupnorm_quantize.
+ * (SEGQ_ACT_NONE), as MXFP4.  act(z) is within 2^-17 of its true value, relative,
+ * down to 2^-125 (the bound of segquant_groupnorm_quantize, not its bits).  SiLU
+ * and GELU of an infinity of either sign make their block NaN, as z = NaN does: at
+ * one end the formulas are an infinity, at the other an infinity times 0.
  *   z_bf16      device bf16 [M][ld_z]
  *   codes, scales  device, the arrays of M rows and K columns, 16- and 4-byte
  *               aligned; they must not overlap each other or z_bf16
