@@ -614,32 +614,31 @@ hipError_t launch_gemm_mx_bf16(const MxGemmProblem &p, const uint16_t *z, int64_
   return waves == 8 ? launch_fused<8, 1, 1>(a, act, s) : launch_fused<4, 1, 1>(a, act, s);
 }
 
-// The cheapest tile shape, or -1 for the kernel that splits K over its waves.
-static int mx_choice(const MxGemmArgs &a) {
+static MxGemmArgs mx_args(const MxGemmProblem &p) {
+  return {p, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K), (int32_t)mx_row_tiles(p.M),
+          (int32_t)mx_row_tiles(p.N), 0, 0};
+}
+
+int mx_choice(int64_t M, int64_t N, int64_t K) {
+  MxGemmProblem p{};
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  const MxGemmArgs a = mx_args(p);
   int best = 0;
   for (int i = 1; i < (int)(sizeof kMxTiles / sizeof kMxTiles[0]); ++i)
     if (mx_cost(kMxTiles[i], a) < mx_cost(kMxTiles[best], a)) best = i;
   return mx_rows_cost(a) < mx_cost(kMxTiles[best], a) && a.mt <= 65535 ? -1 : best;
 }
 
-static MxGemmArgs mx_args(const MxGemmProblem &p) {
-  return {p, (int32_t)mx_tiles_k(p.K), (int32_t)mx_scale_tiles_k(p.K), (int32_t)mx_row_tiles(p.M),
-          (int32_t)mx_row_tiles(p.N), 0, 0};
-}
-
 bool mx_rows_inside(int64_t M, int64_t N, int64_t K) {
-  if (M <= 16 || !mx_few_rows(M, N, K)) return false;
-  MxGemmProblem p{};
-  p.M = M;
-  p.N = N;
-  p.K = K;
-  return mx_choice(mx_args(p)) < 0;
+  return M > 16 && mx_few_rows(M, N, K) && mx_choice(M, N, K) < 0;
 }
 
 hipError_t launch_gemm_mx(const MxGemmProblem &p, hipStream_t s) {
   if (p.M <= 16) return launch_one_row_tile(p, s);
   const MxGemmArgs a = mx_args(p);
-  const int best = mx_choice(a);
+  const int best = mx_choice(p.M, p.N, p.K);
   // eight waves where the product of bf16 input has them, so that both give the same
   // bits (of up to four steps the order is the same); otherwise by time
   if (best < 0)

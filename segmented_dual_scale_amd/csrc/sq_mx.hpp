@@ -54,6 +54,9 @@ struct MxGemmProblem {
 };
 
 hipError_t launch_gemm_mx(const MxGemmProblem &p, hipStream_t s);
+// Its form for more than 16 rows: the tile shape in its table that costs least, or -1
+// for the kernel that splits K over its waves.
+int mx_choice(int64_t M, int64_t N, int64_t K);
 // Whether the product of bf16 input of this size quantises it itself: with any
 // activation; with none.  And that product (x and x_scale of the problem unused).
 bool mx_quantises_inside(int64_t M, int64_t K);
