@@ -580,10 +580,15 @@ static int64_t mx_groups(int64_t M, int64_t N, int nt) {
 }
 
 // More than 16 rows of bf16 without an activation: each workgroup quantises its 32 rows,
-// up to 96 values a thread, where one workgroup a CU or fewer do that.  In a captured
-// graph against two launches: 77x1536x1536 5.6 us against 6.2, 77x1536x512 3.7 against
-// 5.0, 77x4608x1536 6.7 against 6.4 (at two a CU 9.5 against 6.7); from the host the
-// second launch costs 3 us more.  An activation on top costs more than it: SiLU
+// up to 96 values a thread (K 1536), where one workgroup a CU or fewer do that.  In a
+// captured graph against two launches, us, by K:
+//                                      512        1024       1536       2048       2560
+//   77 rows, N 1536,  72 workgroups  3.7 / 5.1  4.7 / 5.3  5.6 / 5.8  6.5 / 5.9  7.7 / 6.4
+//   300,     N 1536, 240             4.5 / 5.3  5.4 / 5.9  6.4 / 6.5  7.9 / 6.9  9.7 / 7.5
+//   77,      N 4608, 216             4.4 / 5.2  5.4 / 5.7  6.5 / 6.2  7.8 / 6.5  9.0 / 7.0
+//   160,     N 4608, 360             5.8 / 5.6  7.5 / 6.3  9.4 / 7.0  11.5 / 7.3  13.8 / 8.3
+// The one cell inside the limit that loses, by 0.2 to 0.3 us, gains 2.5 us from the host, as
+// every other does (7.5 against 10.1).  An activation on top costs more than a launch: SiLU
 // 77x1536x1536 8.7 against 6.9.
 static bool mx_few_rows(int64_t M, int64_t N, int64_t K) {
   return 32 * K <= 96 * 512 && mx_groups(M, N, 4) <= 256;
