@@ -310,7 +310,8 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
   // scales: 1 KiB of four tiles a copy, in the same orders: its 16 bytes 16 g + r
   auto scale_src = [&](int s, int q, int g, int r) {
     if (q < kXS)
-      return a.p.x_scale + (((int64_t)min(tm * kXT + q * 4 + g, a.mt - 1) * a.ks + s) << 8) + 16 * r;
+      return a.p.x_scale + (((int64_t)min(tm * kXT + q * 4 + g, a.mt - 1) * a.ks + s) << 8) +
+             16 * r;
     return a.p.w_scale +
            (((int64_t)min(tn * kWT + (q - kXS) * 4 + (g & 2) + (r >> 1 & 1), a.nt - 1) * a.ks + s)
             << 8) +
@@ -470,9 +471,8 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_lds_kernel(MxGemmArgs a)
 
 template <int RM, int RN, int WM, int WN, int SCALES>
 static hipError_t launch_mx_lds(MxGemmArgs a, hipStream_t s) {
-  const bool wide =
-      ((reinterpret_cast<uintptr_t>(a.p.x_scale) | reinterpret_cast<uintptr_t>(a.p.w_scale)) & 15) ==
-      0;
+  const bool wide = !((reinterpret_cast<uintptr_t>(a.p.x_scale) |
+                       reinterpret_cast<uintptr_t>(a.p.w_scale)) & 15);
   constexpr int kXT = WM * RM, kWT = WN * RN;
   constexpr int kLds = 4096 * (kXT + kWT) + 1024 * SCALES * ((kXT + 3) / 4 + kWT / 4);
   a.tiles_m = (a.mt + kXT - 1) / kXT;
@@ -519,9 +519,9 @@ static float mx_rows_cost(const MxGemmArgs &a) {
 // 24.8, 192x256 25.9; 3000x3200x2560 192x256 18.8, 224x256 20.0; 4096x1536x6144
 // 128x256 23.5, 128x128 24.4; 1024x1536x1536 64x128 5.2, split K 5.8, 128x128 6.5;
 // 256x1536x6144 split K 6.2, 64x128 10.4.  160x256 was left out: 3000x3200x2560 16.4
-// and 2048x4608x1536 12.1 against 12.7 with operands in the caches, but with operands
-// from memory, behind the norm and before the rotary positions, 4429x4608x1536 took 54
-// us in all against 47.
+// against 17.3 and 2048x4608x1536 12.1 against 12.7 with operands in the caches, but with
+// operands from memory, behind the norm and before the rotary positions, the three
+// kernels at 4429x4608x1536 took 55.6 us against 51.6 (one card, in turn, six times).
 constexpr MxTile kMxTiles[] = {
     {16, 16, 1, 0.78f, 5.5f}, {14, 16, 1, 0.69f, 6.5f}, {12, 16, 1, 0.59f, 5.6f},
     {8, 16, 1, 0.41f, 3.6f},  {8, 8, 2, 0.49f, 3.3f},   {4, 8, 3, 0.47f, 2.6f},
