@@ -214,7 +214,8 @@ int segquant_activate_quantize(const uint16_t *z_bf16, int64_t M, int64_t K, int
  * two.  The order of every sum is fixed: the same call gives the same bits.
  * Tensor pointers 16-byte aligned, ld_z, ld_xo and ld_mod multiples of 8,
  * ld_q of 16; C needs no alignment.  C <= 2^20, B <= 65535.  B or P may be 0.
- * Values above about 2^60 in magnitude overflow the fp32 squares.
+ * A group whose values or squared deviations add up to 2^128 or more overflows
+ * fp32.
  */
 int segquant_groupnorm_quantize(const uint16_t *z_bf16, int64_t B, int64_t P, int64_t C,
                                 int64_t ld_z, int32_t groups, float eps, const float *gamma,
@@ -264,6 +265,7 @@ size_t segquant_groupnorm_workspace_bytes(int64_t B, int64_t P, int64_t C, int32
  * ld_h, ld_b, ld_ho, ld_xo and ld_mod multiples of 8, ld_q of 16; K needs no
  * alignment; K-segment boundaries up to 4194240.  M may be 0.  Outputs must
  * not overlap each other or, but for h_out as above, inputs: SEGQ_ERR_SHAPE.
+ * A row whose values or squared deviations add up to 2^128 or more overflows fp32.
  */
 int segquant_adanorm_quantize(const uint16_t *h_bf16, int64_t M, int64_t K, int64_t ld_h,
                               const uint16_t *branch, int64_t ld_b, const uint16_t *gate,

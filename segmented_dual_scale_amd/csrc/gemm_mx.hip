@@ -4,9 +4,10 @@
 // blocks of 32 by their two powers of two and adds in fp32.
 //
 // On random operands a loop of that instruction alone reaches 6.25 PFLOP/s, its
-// power holding the clock down.  The product, in a row of calls:
-//   8192^3 227 us (4.8 PFLOP/s), 9216x4608x12288 217 us (4.8), 4096x1536x6144
-//   23.6 us (3.3), 4429x4608x1536 24.8 us (2.5), 4429x1536x1536 10.7 us (2.0)
+// power holding the clock down.  The product in a captured graph, by card:
+//   8192^3 222 to 230 us (4.9 PFLOP/s), 9216x4608x12288 208 to 220 (4.9), 4096x1536x6144
+//   22.3 to 23.5 (3.4), 4429x4608x1536 23.7 to 24.8 (2.6), 4429x1536x1536 10.7 to 11.1 (1.9)
+// and one launch at a time in a kernel trace 221, 25.2, 25.0 and 11.7 for the last four.
 // The smaller ones are launch, first loads and last stores, about 6 us, and parts of
 // a round of workgroups.  On operands of zeros, which leave the clock alone, the
 // first two take 170 and 157 us.
